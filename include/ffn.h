@@ -217,6 +217,76 @@ int ffn_swiglu_forward_traced(const void* X, const void* Wg, const void* Wu, con
                               int variant, void* workspace, size_t workspace_bytes, void* stream,
                               void** events, int n_events);
 
+/* ---------------------------------------------------------------- SwiGLU backward
+ * Gradients of ffn_swiglu_forward for the output gradient dY (M x P), with
+ * a = X Wg, b = X Wu, s = 1 / (1 + exp(-a)), h = a s b and dh = dY Wd^T:
+ *
+ *   da = dh * b * s (1 + a (1 - s)),  db = dh * a s        (* elementwise)
+ *   dX = da Wg^T + db Wu^T            M x N, bf16
+ *   dWg = X^T da, dWu = X^T db        N x O, grad_dtype
+ *   dWd = h^T dY                      O x P, grad_dtype
+ *
+ * bf16 inputs only; grad_dtype is FFN_BF16 (the weights' own type) or FFN_F32
+ * (for gradients that are summed over several calls).  The forward keeps no H,
+ * so a and b are recomputed.  dh, a and b stay fp32; h, da and db are rounded to
+ * bf16 once (they live in the workspace), sums accumulate in fp32 in a fixed
+ * order (no atomics: repeated calls are bitwise identical).  N below 2^23 and
+ * O below 2^22.  With M == 0 the weight gradients are zero-filled. */
+size_t ffn_swiglu_backward_workspace_size(int64_t M, int64_t N, int64_t O, int64_t P, int dtype);
+
+int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const void* Wd,
+                        const void* dY, void* dX, void* dWg, void* dWu, void* dWd, int64_t M,
+                        int64_t N, int64_t O, int64_t P, int dtype, int grad_dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- layer norm
+ * The norm in front of the FFN, over the last dimension, and its gradients:
+ *
+ *   mean = sum_j x_j / N, rstd = 1 / sqrt(sum_j (x_j - mean)^2 / N + eps)
+ *   y_j = (x_j - mean) rstd gamma_j + beta_j
+ *
+ *   z = (x - mean) rstd, t = dy gamma
+ *   dx = rstd (t - sum_j t_j / N - z sum_j t_j z_j / N)
+ *   dgamma = column sums of dy z, dbeta = column sums of dy
+ *
+ * X, Y, dY, dX: M x N; gamma, beta: N; all in `dtype` (FFN_BF16 or FFN_F32).
+ * mean, rstd: M fp32 (the forward writes them, each may be NULL there; the
+ * backward reads them).  dgamma, dbeta: N fp32.  Statistics and sums are fp32
+ * (the variance is the centred sum, not E[x^2] - mean^2), in a fixed order.  N a
+ * multiple of 8 up to 32768; eps >= 0.  Y may be X itself, and dX may be X or
+ * dY.  With M == 0 the forward does nothing and the backward zero-fills dgamma
+ * and dbeta. */
+int ffn_layernorm_forward(const void* X, const void* gamma, const void* beta, void* Y,
+                          float* mean, float* rstd, int64_t M, int64_t N, int dtype, float eps,
+                          void* stream);
+
+size_t ffn_layernorm_backward_workspace_size(int64_t M, int64_t N, int dtype);
+
+int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, const float* mean,
+                           const float* rstd, void* dX, float* dgamma, float* dbeta, int64_t M,
+                           int64_t N, int dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ---------------------------------------------------------------- orthogonalised update
+ * The update of a weight matrix by Newton-Schulz steps on its gradient (or
+ * momentum), as the Muon optimiser takes it:
+ *
+ *   X = G / (||G||_F + 1e-7), then `steps` times, with A = X X^T:
+ *   X <- 3.4445 X - 4.7750 A X + 2.0315 A^2 X;   U = X
+ *
+ * G: a stack of B matrices R x C in `dtype` (FFN_BF16 or FFN_F32), for instance
+ * the experts' gradients; each is treated by itself.  U: B x R x C bf16.  (With
+ * R > C the same polynomial is applied from the right.)  The norm is summed in
+ * fp64; products take fp16 operands with fp32 sums, X is carried in 22 bits, so U
+ * is within a few bf16 half steps of the exact iteration.  A matrix of zeros gives
+ * zeros; a NaN or infinity in a matrix makes that matrix's U NaN.  R and C
+ * multiples of 8 below 2^22, R * C and min(R, C)^2 below 2^31, B up to 65535,
+ * 1 <= steps <= 32.  U must not overlap G.  With B == 0 nothing is done. */
+size_t ffn_orthogonalize_workspace_size(int64_t B, int64_t R, int64_t C, int dtype);
+
+int ffn_orthogonalize(const void* G, void* U, int64_t B, int64_t R, int64_t C, int dtype,
+                      int steps, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- MoE
  * Grouped form over the per-expert token lists of a top-k Mixture-of-Experts
  * layer (the MoE tile-signalling review, zhongzhuzhou.org, sections 2.1-2.2:

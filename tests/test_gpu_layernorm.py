@@ -1,0 +1,143 @@
+"""GPU parity of the layer norm and its gradients against their fp64 forms, within the bounds of
+training_ref."""
+from __future__ import annotations
+
+import pytest
+
+import transformer_ffn_fusion_amd as ffn
+
+import training_ref as ref
+
+pytestmark = pytest.mark.gpu
+SHAPES = [(1, 8), (1, 4096), (3, 72), (5, 512), (7, 520), (13, 1032), (2, 2048), (33, 2056), (6, 4104),
+          (5, 8192), (3, 8200), (2, 16384), (3, 16392), (2, 32768), (1030, 136), (2053, 24), (700, 1024)]
+
+
+def make(M, N, dtype, seed=0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, N, generator=g) + 0.5
+    x = x * (1 + 30 * (torch.rand(N, generator=g) < 0.05))     # a few large channels
+    return {k: v.to(dtype).cuda() for k, v in dict(
+        X=x, dY=torch.randn(M, N, generator=g), gamma=1 + 0.3 * torch.randn(N, generator=g),
+        beta=0.3 * torch.randn(N, generator=g)).items()}
+
+
+def forward(x, eps=1e-5, Y=None):
+    import torch
+    M = x["X"].shape[0]
+    nan = torch.full((M,), float("nan"), device="cuda")
+    out = dict(Y=torch.full_like(x["X"], float("nan")) if Y is None else Y, mean=nan, rstd=nan.clone())
+    ffn.ffn_layernorm_forward(x["X"], x["gamma"], x["beta"], out["Y"], out["mean"], out["rstd"], eps=eps)
+    torch.cuda.synchronize()
+    return out
+
+
+def backward(x, mean, rstd, ws=None, dX=None):
+    import torch
+    nan = torch.full((x["X"].shape[1],), float("nan"), device="cuda")
+    out = dict(dX=torch.full_like(x["X"], float("nan")) if dX is None else dX, dgamma=nan, dbeta=nan.clone())
+    ffn.ffn_layernorm_backward(x["X"], x["dY"], x["gamma"], mean, rstd, out["dX"], out["dgamma"],
+                               out["dbeta"], ws=ws)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward_and_backward(shape, dtype):
+    import torch
+    print(f"case layer norm {shape} {dtype}", flush=True)
+    x = make(*shape, getattr(torch, dtype), seed=shape[0] + shape[1])
+    f = forward(x)
+    ref.check(f, ref.layernorm_forward(x["X"], x["gamma"], x["beta"], 1e-5), f"{shape} forward")
+    b = backward(x, f["mean"], f["rstd"])
+    ref.check(b, ref.layernorm_backward(x["X"], x["dY"], x["gamma"], f["mean"], f["rstd"]),
+              f"{shape} backward")
+
+
+def test_statistics_are_optional_and_calls_repeat_bitwise():
+    import torch
+    x = make(301, 1288, torch.bfloat16, seed=2)
+    f = forward(x)
+    Y = torch.empty_like(x["X"])
+    ffn.ffn_layernorm_forward(x["X"], x["gamma"], x["beta"], Y)
+    ws = ffn.workspace(ffn.ffn_layernorm_backward_workspace_size(301, 1288))
+    first = backward(x, f["mean"], f["rstd"], ws)
+    ws.fill_(0xFF)
+    again = backward(x, f["mean"], f["rstd"], ws)
+    assert torch.equal(Y, f["Y"])
+    assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_in_place():
+    import torch
+    for dtype in (torch.bfloat16, torch.float32):
+        x = make(37, 1544, dtype, seed=4)
+        f = forward(x)
+        y = x["X"].clone()
+        ffn.ffn_layernorm_forward(y, x["gamma"], x["beta"], y)
+        assert torch.equal(y, f["Y"])
+        b = backward(x, f["mean"], f["rstd"])
+        for name in ("X", "dY"):
+            z = {**x, name: x[name].clone()}
+            assert torch.equal(backward(z, f["mean"], f["rstd"], dX=z[name])["dX"], b["dX"])
+
+
+def test_constant_rows_and_large_offsets():
+    """Rows without spread: y = beta, and a finite gradient; an offset of 1000 costs no digits
+    beyond fp32's of the inputs."""
+    import torch
+    x = make(9, 264, torch.float32, seed=6)
+    x["X"][4] = 3.0
+    x["X"][5] = 0.0
+    x["X"][6] += 1000.0
+    f = forward(x)
+    ref.check(f, ref.layernorm_forward(x["X"], x["gamma"], x["beta"], 1e-5), "offsets")
+    assert torch.equal(f["Y"][4], x["beta"]) and torch.equal(f["Y"][5], x["beta"])
+    b = backward(x, f["mean"], f["rstd"])
+    ref.check(b, ref.layernorm_backward(x["X"], x["dY"], x["gamma"], f["mean"], f["rstd"]), "offsets")
+
+
+def test_nan_rows_stay_alone():
+    import torch
+    x = make(40, 520, torch.bfloat16, seed=8)
+    clean = forward(x)
+    x["X"][11, 3] = float("nan")
+    x["X"][12, 5] = float("inf")
+    f = forward(x)
+    keep = torch.ones(40, dtype=torch.bool, device="cuda")
+    keep[11:13] = False
+    assert torch.equal(f["Y"][keep], clean["Y"][keep])
+    assert bool(torch.isnan(f["Y"][11:13].float()).all())
+
+
+def test_no_rows():
+    import torch
+    x = make(0, 64, torch.bfloat16)
+    f = forward(x)
+    b = backward(x, f["mean"], f["rstd"])
+    assert not bool(b["dgamma"].any()) and not bool(b["dbeta"].any())
+
+
+def test_differences():
+    """Directional differences of the fp64 forward against the gradients."""
+    import torch
+    x = make(11, 72, torch.float32, seed=10)
+    f = forward(x)
+    b = backward(x, f["mean"], f["rstd"])
+    w = {k: ref.d(v) for k, v in x.items()}
+
+    def loss(v):
+        c = v["X"] - v["X"].mean(1, keepdim=True)
+        y = c * (c.square().mean(1, keepdim=True) + 1e-5).pow(-0.5) * v["gamma"] + v["beta"]
+        return float((y * w["dY"]).sum())
+    g = torch.Generator().manual_seed(3)
+    for src, grad in (("X", "dX"), ("gamma", "dgamma"), ("beta", "dbeta")):
+        v = torch.randn(w[src].shape, generator=g).double()
+        num = (loss({**w, src: w[src] + 1e-5 * v}) - loss({**w, src: w[src] - 1e-5 * v})) / 2e-5
+        got = float((ref.d(b[grad]) * v).sum())
+        # fp32 statistics and sums: a few hundred roundings of the magnitudes
+        slack = 300 * ref.U_F32 * float((ref.d(b[grad]).abs() * v.abs()).sum() + 30)
+        print(f"  {grad}: {got:.7f}, by differences {num:.7f}", flush=True)
+        assert abs(got - num) <= slack + 1e-5

@@ -1,0 +1,114 @@
+"""GPU parity of the orthogonalised update against the fp64 iteration (bounds: training_ref)."""
+from __future__ import annotations
+
+import pytest
+
+import transformer_ffn_fusion_amd as ffn
+
+import training_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def gradient(R, C, seed=0, rank=None, spread=0.5):
+    """X^T dA over `rank` tokens, channels of unequal size."""
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    T = rank or 2 * max(R, C)
+    x = torch.randn(R, T, generator=g) * torch.exp(spread * torch.randn(R, 1, generator=g))
+    y = torch.randn(T, C, generator=g) * torch.exp(spread * torch.randn(1, C, generator=g))
+    return x @ y / T
+
+
+def run(G, steps=5, ws=None):
+    import torch
+    U = torch.full(G.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    ffn.ffn_orthogonalize(G, U, steps=steps, ws=ws)
+    torch.cuda.synchronize()
+    return U
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("shape", [
+    (8, 8), (8, 264), (264, 8), (64, 64), (72, 200), (200, 72), (128, 512), (136, 136), (264, 520),
+    (520, 264), (392, 400), (1032, 256),
+])
+def test_shapes(shape, dtype):
+    import torch
+    print(f"case orthogonalize {shape} {dtype}", flush=True)
+    G = gradient(*shape, seed=sum(shape)).to(getattr(torch, dtype)).cuda()
+    ref.check_orthogonalize(run(G), G, 5, str(shape))
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 6])
+def test_steps(steps):
+    G = gradient(136, 264, seed=steps).cuda()
+    ref.check_orthogonalize(run(G, steps), G, steps, f"{steps} steps")
+
+
+def test_large_tiles():
+    # tiles of 256 x 256 for the outer product (4136 x 2056) and the symmetric ones
+    G = gradient(2056, 4136, seed=1).bfloat16().cuda()
+    ref.check_orthogonalize(run(G), G, 5, "2056 x 4136")
+    Gt = G.t().contiguous()
+    ref.check_orthogonalize(run(Gt), Gt, 5, "4136 x 2056")
+
+
+@pytest.mark.parametrize("kind", ["rank 1", "rank 16", "orthogonal", "one large direction", "tiny", "huge"])
+def test_spectra(kind):
+    import torch
+    R, C = 200, 328
+    if kind == "rank 1":
+        G = gradient(R, C, 3, rank=1)
+    elif kind == "rank 16":
+        G = gradient(R, C, 4, rank=16)
+    elif kind == "orthogonal":
+        G = torch.linalg.qr(torch.randn(C, R, generator=torch.Generator().manual_seed(5)))[0].t().contiguous()
+    elif kind == "one large direction":
+        G = gradient(R, C, 6) + 100 * gradient(R, C, 7, rank=1)
+    else:
+        G = gradient(R, C, 8) * (1e-25 if kind == "tiny" else 1e30)   # squares leave fp32's range
+    G = G.cuda()
+    if kind == "tiny":   # far below the norm's epsilon: X = G / 1e-7, grown by 3.4445 each step
+        got, want = ref.d(run(G)), ref.orthogonalize(G)
+        assert float((got - want).abs().max()) <= 1e-9 and float(want.abs().max()) < 1e-10
+        return
+    ref.check_orthogonalize(run(G), G, 5, kind)
+
+
+def test_stack_is_each_alone_bitwise():
+    import torch
+    G = torch.stack([gradient(136, 72, s) * 10.0 ** s for s in range(5)]).cuda()
+    U = run(G)
+    for e in range(5):
+        ref.check_orthogonalize(U[e], G[e], 5, f"matrix {e}")
+        assert torch.equal(run(G[e].contiguous()), U[e])
+
+
+def test_repeat_bitwise_dirty_workspace_and_guard():
+    import torch
+    G = gradient(200, 136, 9).cuda()
+    need = ffn.ffn_orthogonalize_workspace_size(1, 200, 136)
+    raw = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    raw[need:] = 0xA5
+    first = run(G, ws=raw[:need])
+    raw[:need] = 0xFF
+    assert torch.equal(run(G, ws=raw[:need]), first)
+    assert bool((raw[need:] == 0xA5).all())
+
+
+def test_zeros_nan_and_infinity():
+    import torch
+    G = torch.stack([gradient(72, 136, s) for s in range(4)]).cuda()
+    G[0] = 0.0
+    G[1, 3, 5] = float("nan")
+    G[2, 70, 2] = float("inf")
+    U = run(G)
+    assert not bool(U[0].any())
+    assert bool(torch.isnan(U[1].float()).all()) and bool(torch.isnan(U[2].float()).all())
+    ref.check_orthogonalize(U[3], G[3], 5, "beside them")
+
+
+def test_empty_stack():
+    import torch
+    ffn.ffn_orthogonalize(torch.empty(0, 8, 8, device="cuda"), torch.empty(0, 8, 8, dtype=torch.bfloat16, device="cuda"))

@@ -21,6 +21,9 @@ __all__ = [
     "FFNError", "lib", "lib_path", "ffn_workspace_size", "ffn_forward", "ffn_forward_ex",
     "ffn_forward_family",
     "ffn_forward_noalloc", "NOALLOC_SCRATCH_BYTES",
+    "ffn_swiglu_workspace_size", "ffn_swiglu_forward", "ffn_swiglu_backward_workspace_size",
+    "ffn_swiglu_backward", "ffn_layernorm_forward", "ffn_layernorm_backward_workspace_size",
+    "ffn_layernorm_backward", "ffn_orthogonalize_workspace_size", "ffn_orthogonalize",
     "moe_workspace_size", "moe_route", "moe_ffn_forward", "ffn_last_error", "workspace",
 ]
 
@@ -97,6 +100,21 @@ def lib():
         L.ffn_backward_traced.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64,
                                           i32, i32, vp, sz, vp, ctypes.POINTER(vp), i32]
         L.ffn_backward_traced.restype = i32
+        L.ffn_swiglu_backward_workspace_size.argtypes = [i64, i64, i64, i64, i32]
+        L.ffn_swiglu_backward_workspace_size.restype = sz
+        L.ffn_swiglu_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64,
+                                          i32, i32, vp, sz, vp]
+        L.ffn_swiglu_backward.restype = i32
+        L.ffn_layernorm_forward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, ctypes.c_float, vp]
+        L.ffn_layernorm_forward.restype = i32
+        L.ffn_layernorm_backward_workspace_size.argtypes = [i64, i64, i32]
+        L.ffn_layernorm_backward_workspace_size.restype = sz
+        L.ffn_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, vp, sz, vp]
+        L.ffn_layernorm_backward.restype = i32
+        L.ffn_orthogonalize_workspace_size.argtypes = [i64, i64, i64, i32]
+        L.ffn_orthogonalize_workspace_size.restype = sz
+        L.ffn_orthogonalize.argtypes = [vp, vp, i64, i64, i64, i32, i32, vp, sz, vp]
+        L.ffn_orthogonalize.restype = i32
         L.ffn_last_error.argtypes = []
         L.ffn_last_error.restype = ctypes.c_char_p
         L.ffn_version.restype = i32
@@ -331,6 +349,109 @@ def ffn_swiglu_forward(X, Wg, Wu, Wd, Y, variant=VARIANT_AUTO, ws=None, stream=N
     _check(lib().ffn_swiglu_forward(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(Y), M, N, O, P,
                                     dt, int(variant), _ptr(ws), ws.numel(), _stream(stream)))
     return Y
+
+
+def ffn_swiglu_backward_workspace_size(M, N, O, P, dtype=BF16) -> int:
+    return lib().ffn_swiglu_backward_workspace_size(M, N, O, P, dtype)
+
+
+def ffn_swiglu_backward(X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, ws=None, stream=None):
+    """Gradients of ``ffn_swiglu_forward`` for the output gradient ``dY``; writes dX (bf16) and
+    dWg, dWu, dWd (all bf16 or all fp32) in place.  Every input is bf16."""
+    import torch
+    M, N = _dims(X, "X", 2)
+    O = _dims(Wg, "Wg", 2)[1]
+    P = _dims(Wd, "Wd", 2)[1]
+    bf = torch.bfloat16
+    _arg(X, "X", (M, N), bf)
+    _arg(Wg, "Wg", (N, O), bf)
+    _arg(Wu, "Wu", (N, O), bf)
+    _arg(Wd, "Wd", (O, P), bf)
+    _arg(dY, "dY", (M, P), bf)
+    _arg(dX, "dX", (M, N), bf)
+    _dims(dWg, "dWg", 2)
+    gdt = _dtype_code(dWg)
+    _arg(dWg, "dWg", (N, O), dWg.dtype)
+    _arg(dWu, "dWu", (N, O), dWg.dtype)
+    _arg(dWd, "dWd", (O, P), dWg.dtype)
+    _ws_arg(ws)
+    _on_device(X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, ws)
+    if ws is None:
+        ws = workspace(ffn_swiglu_backward_workspace_size(M, N, O, P), X.device)
+    _check(lib().ffn_swiglu_backward(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(dY), _ptr(dX),
+                                     _ptr(dWg), _ptr(dWu), _ptr(dWd), M, N, O, P, BF16, gdt,
+                                     _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def ffn_layernorm_forward(X, gamma, beta, Y, mean=None, rstd=None, eps=1e-5, stream=None):
+    """``Y = (X - mean) rstd gamma + beta`` over the last dimension of X (M x N, bf16 or fp32);
+    ``Y`` and, when given, ``mean`` and ``rstd`` (M, fp32) are written in place."""
+    import torch
+    M, N = _dims(X, "X", 2)
+    dt = _dtype_code(X)
+    _arg(X, "X", (M, N), X.dtype)
+    _arg(gamma, "gamma", (N,), X.dtype)
+    _arg(beta, "beta", (N,), X.dtype)
+    _arg(Y, "Y", (M, N), X.dtype)
+    _arg(mean, "mean", (M,), torch.float32, optional=True)
+    _arg(rstd, "rstd", (M,), torch.float32, optional=True)
+    _on_device(X, gamma, beta, Y, mean, rstd)
+    _check(lib().ffn_layernorm_forward(_ptr(X), _ptr(gamma), _ptr(beta), _ptr(Y), _ptr(mean),
+                                       _ptr(rstd), M, N, dt, float(eps), _stream(stream)))
+    return Y
+
+
+def ffn_layernorm_backward_workspace_size(M, N, dtype=BF16) -> int:
+    return lib().ffn_layernorm_backward_workspace_size(M, N, dtype)
+
+
+def ffn_layernorm_backward(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws=None, stream=None):
+    """Gradients of ``ffn_layernorm_forward``: dX in X's type, dgamma and dbeta (N, fp32), written
+    in place.  ``mean`` and ``rstd`` are what the forward wrote."""
+    import torch
+    M, N = _dims(X, "X", 2)
+    dt = _dtype_code(X)
+    f32 = torch.float32
+    _arg(X, "X", (M, N), X.dtype)
+    _arg(dY, "dY", (M, N), X.dtype)
+    _arg(gamma, "gamma", (N,), X.dtype)
+    _arg(mean, "mean", (M,), f32)
+    _arg(rstd, "rstd", (M,), f32)
+    _arg(dX, "dX", (M, N), X.dtype)
+    _arg(dgamma, "dgamma", (N,), f32)
+    _arg(dbeta, "dbeta", (N,), f32)
+    _ws_arg(ws)
+    _on_device(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws)
+    if ws is None:
+        ws = workspace(ffn_layernorm_backward_workspace_size(M, N, dt), X.device)
+    _check(lib().ffn_layernorm_backward(_ptr(X), _ptr(dY), _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                        _ptr(dX), _ptr(dgamma), _ptr(dbeta), M, N, dt, _ptr(ws),
+                                        ws.numel(), _stream(stream)))
+
+
+def ffn_orthogonalize_workspace_size(B, R, C, dtype=BF16) -> int:
+    return lib().ffn_orthogonalize_workspace_size(B, R, C, dtype)
+
+
+def ffn_orthogonalize(G, U, steps=5, ws=None, stream=None):
+    """Newton-Schulz orthogonalisation of a gradient ``G`` (R x C, or a stack B x R x C; bf16 or
+    fp32); ``U`` (the same shape, bf16) is written in place."""
+    import torch
+    if G is None:
+        raise ValueError("G must not be None")
+    if G.dim() not in (2, 3):
+        raise ValueError(f"G must have 2 or 3 dimensions (got shape {tuple(G.shape)})")
+    B, R, C = (1, *G.shape) if G.dim() == 2 else G.shape
+    dt = _dtype_code(G)
+    _arg(G, "G", G.shape, G.dtype)
+    _arg(U, "U", G.shape, torch.bfloat16)
+    _ws_arg(ws)
+    _on_device(G, U, ws)
+    if ws is None:
+        ws = workspace(ffn_orthogonalize_workspace_size(B, R, C, dt), G.device)
+    _check(lib().ffn_orthogonalize(_ptr(G), _ptr(U), B, R, C, dt, int(steps), _ptr(ws), ws.numel(),
+                                   _stream(stream)))
+    return U
 
 
 def _route_outputs(M, E, k, topk_ids, topk_w, expert_offsets, sorted_entries):

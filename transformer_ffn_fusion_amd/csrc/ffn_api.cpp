@@ -175,6 +175,21 @@ BackwardLayout backward_layout(int64_t M, int64_t O, int64_t P) {
     return L;
 }
 
+// ---- SwiGLU backward workspace layout
+struct SwigluBackwardLayout {
+    size_t dH = 0, H = 0, dAB = 0, total = 0;
+};
+
+SwigluBackwardLayout swiglu_backward_layout(int64_t M, int64_t O) {
+    SwigluBackwardLayout L;
+    size_t off = 0;
+    L.dH = off;      off += align_up(sizeof(float) * M * O);
+    L.H = off;       off += align_up(sizeof(uint16_t) * M * O);
+    L.dAB = off;     off += align_up(sizeof(uint16_t) * M * 2 * O);
+    L.total = off ? off : kAlign;
+    return L;
+}
+
 // ---- MoE workspace layout
 struct MoeLayout {
     size_t ids, w, counts, offsets, sorted, pos, tiles, tile_count, blk_counts, blk_base, part,
@@ -608,6 +623,193 @@ int ffn_swiglu_forward_traced(const void* X, const void* Wg, const void* Wu, con
     if (!events) return fail(FFN_EINVAL, "events must not be NULL");
     return swiglu_forward(X, Wg, Wu, Wd, Y, M, N, O, P, dtype, variant, workspace,
                           workspace_bytes, stream, events, n_events);
+}
+
+// ---------------------------------------------------------------- SwiGLU backward
+
+size_t ffn_swiglu_backward_workspace_size(int64_t M, int64_t N, int64_t O, int64_t P, int dtype) {
+    if (check_dims(M, N, O, P) != FFN_OK || dtype != FFN_BF16) return 0;
+    return swiglu_backward_layout(M, O).total;
+}
+
+int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const void* Wd,
+                        const void* dY, void* dX, void* dWg, void* dWu, void* dWd, int64_t M,
+                        int64_t N, int64_t O, int64_t P, int dtype, int grad_dtype,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_dims(M, N, O, P);
+    if (rc) return rc;
+    if (dtype != FFN_F32 && dtype != FFN_BF16) return fail(FFN_EINVAL, "unknown dtype %d", dtype);
+    if (dtype != FFN_BF16) return fail(FFN_EUNSUPPORTED, "the backward takes bf16 only");
+    if (grad_dtype != FFN_F32 && grad_dtype != FFN_BF16)
+        return fail(FFN_EINVAL, "unknown gradient dtype %d", grad_dtype);
+    // a half-tile (128 rows, or 64 rows of X, da | db or dY) is addressed with 32-bit byte offsets
+    if (N >= ((int64_t)1 << 23) || O >= ((int64_t)1 << 22))
+        return fail(FFN_EUNSUPPORTED, "the SwiGLU backward takes N below 2^23 and O below 2^22 "
+                    "(got %lld, %lld)", (long long)N, (long long)O);
+    if (!Wg || !Wu || !Wd || !dWg || !dWu || !dWd || (M > 0 && (!X || !dY || !dX)))
+        return fail(FFN_EINVAL, "X, Wg, Wu, Wd, dY, dX, dWg, dWu and dWd must not be NULL");
+    if (!workspace) return fail(FFN_EINVAL, "workspace must not be NULL");
+    const void* ps[] = {X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd};
+    const char* nm[] = {"X", "Wg", "Wu", "Wd", "dY", "dX", "dWg", "dWu", "dWd"};
+    for (int i = 0; i < 9; ++i)
+        if (ps[i] && !aligned16(ps[i])) return fail(FFN_EALIGN, "%s is not 16-byte aligned", nm[i]);
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+        return fail(FFN_EALIGN, "workspace is not 256-byte aligned");
+    const SwigluBackwardLayout L = swiglu_backward_layout(M, O);
+    if (workspace_bytes < L.total)
+        return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (M == 0) {
+        const int64_t words = grad_dtype == FFN_F32 ? 1 : 2;   // gradients per 4-byte word
+        void* zp[3] = {dWg, dWu, dWd};
+        const int64_t zn[3] = {N * O / words, N * O / words, O * P / words};
+        for (int i = 0; i < 3; ++i)
+            if ((rc = launched(ffn::launch_zero_f32((float*)zp[i], zn[i], st), "zero fill"))) return rc;
+        return ok();
+    }
+    char* ws = static_cast<char*>(workspace);
+    ffn::SwigluBackwardIO io;
+    io.X = static_cast<const uint16_t*>(X);
+    io.Wg = static_cast<const uint16_t*>(Wg);
+    io.Wu = static_cast<const uint16_t*>(Wu);
+    io.Wd = static_cast<const uint16_t*>(Wd);
+    io.dY = static_cast<const uint16_t*>(dY);
+    io.dX = static_cast<uint16_t*>(dX);
+    io.dWg = dWg;
+    io.dWu = dWu;
+    io.dWd = dWd;
+    io.grad_f32 = grad_dtype == FFN_F32;
+    io.dH = reinterpret_cast<float*>(ws + L.dH);
+    io.H = reinterpret_cast<uint16_t*>(ws + L.H);
+    io.dAB = reinterpret_cast<uint16_t*>(ws + L.dAB);
+    io.M = M;
+    io.N = N;
+    io.O = O;
+    io.P = P;
+    if ((rc = launched(ffn::launch_swiglu_backward(io, st), "SwiGLU backward kernels"))) return rc;
+    return ok();
+}
+
+// ---------------------------------------------------------------- layer norm
+
+static int check_layernorm(int64_t M, int64_t N, int dtype) {
+    if (dtype != FFN_F32 && dtype != FFN_BF16) return fail(FFN_EINVAL, "unknown dtype %d", dtype);
+    if (M < 0) return fail(FFN_EINVAL, "M must be >= 0 (got %lld)", (long long)M);
+    if (N < 1) return fail(FFN_EINVAL, "N must be >= 1 (got %lld)", (long long)N);
+    if (N % 8 || N > ffn::kLnMaxN)
+        return fail(FFN_EUNSUPPORTED, "the layer norm takes N a multiple of 8 up to %lld (got %lld)",
+                    (long long)ffn::kLnMaxN, (long long)N);
+    if (M >= ((int64_t)1 << 31)) return fail(FFN_EUNSUPPORTED, "M must be below 2^31");
+    return FFN_OK;
+}
+
+int ffn_layernorm_forward(const void* X, const void* gamma, const void* beta, void* Y,
+                          float* mean, float* rstd, int64_t M, int64_t N, int dtype, float eps,
+                          void* stream) {
+    int rc = check_layernorm(M, N, dtype);
+    if (rc) return rc;
+    if (!(eps >= 0.0f)) return fail(FFN_EINVAL, "eps must be >= 0");
+    if (!gamma || !beta || (M > 0 && (!X || !Y)))
+        return fail(FFN_EINVAL, "X, gamma, beta and Y must not be NULL");
+    const void* ps[] = {X, gamma, beta, Y, mean, rstd};
+    const char* nm[] = {"X", "gamma", "beta", "Y", "mean", "rstd"};
+    for (int i = 0; i < 6; ++i)
+        if (ps[i] && !aligned16(ps[i])) return fail(FFN_EALIGN, "%s is not 16-byte aligned", nm[i]);
+    if (M == 0) return ok();
+    rc = launched(ffn::launch_layernorm_forward(X, gamma, beta, Y, mean, rstd, M, N,
+                                                dtype == FFN_F32, eps,
+                                                reinterpret_cast<hipStream_t>(stream)),
+                  "layer norm kernel");
+    if (rc) return rc;
+    return ok();
+}
+
+size_t ffn_layernorm_backward_workspace_size(int64_t M, int64_t N, int dtype) {
+    if (check_layernorm(M, N, dtype) != FFN_OK) return 0;
+    const size_t n = align_up(sizeof(float) * ffn::layernorm_partial_floats(M, N));
+    return n ? n : kAlign;
+}
+
+int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, const float* mean,
+                           const float* rstd, void* dX, float* dgamma, float* dbeta, int64_t M,
+                           int64_t N, int dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    int rc = check_layernorm(M, N, dtype);
+    if (rc) return rc;
+    if (!gamma || !dgamma || !dbeta || (M > 0 && (!X || !dY || !mean || !rstd || !dX)))
+        return fail(FFN_EINVAL, "X, dY, gamma, mean, rstd, dX, dgamma and dbeta must not be NULL");
+    if (!workspace) return fail(FFN_EINVAL, "workspace must not be NULL");
+    const void* ps[] = {X, dY, gamma, mean, rstd, dX, dgamma, dbeta};
+    const char* nm[] = {"X", "dY", "gamma", "mean", "rstd", "dX", "dgamma", "dbeta"};
+    for (int i = 0; i < 8; ++i)
+        if (ps[i] && !aligned16(ps[i])) return fail(FFN_EALIGN, "%s is not 16-byte aligned", nm[i]);
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+        return fail(FFN_EALIGN, "workspace is not 256-byte aligned");
+    const size_t need = ffn_layernorm_backward_workspace_size(M, N, dtype);
+    if (workspace_bytes < need)
+        return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (M == 0) {
+        if ((rc = launched(ffn::launch_zero_f32(dgamma, N, st), "zero fill"))) return rc;
+        if ((rc = launched(ffn::launch_zero_f32(dbeta, N, st), "zero fill"))) return rc;
+        return ok();
+    }
+    rc = launched(ffn::launch_layernorm_backward(X, dY, gamma, mean, rstd, dX, dgamma, dbeta,
+                                                 static_cast<float*>(workspace), M, N,
+                                                 dtype == FFN_F32, st),
+                  "layer norm backward kernels");
+    if (rc) return rc;
+    return ok();
+}
+
+// ---------------------------------------------------------------- orthogonalised update
+
+static int check_orthogonalize(int64_t B, int64_t R, int64_t C, int dtype) {
+    if (dtype != FFN_F32 && dtype != FFN_BF16) return fail(FFN_EINVAL, "unknown dtype %d", dtype);
+    if (B < 0) return fail(FFN_EINVAL, "B must be >= 0 (got %lld)", (long long)B);
+    if (R < 1 || C < 1)
+        return fail(FFN_EINVAL, "R and C must be >= 1 (got %lld, %lld)", (long long)R, (long long)C);
+    if (R % 8 || C % 8)
+        return fail(FFN_EUNSUPPORTED, "R and C must be multiples of 8 (got %lld, %lld)",
+                    (long long)R, (long long)C);
+    // a half-tile (128 rows) is addressed with 32-bit byte offsets
+    if (R >= ((int64_t)1 << 22) || C >= ((int64_t)1 << 22))
+        return fail(FFN_EUNSUPPORTED, "R and C must be below 2^22 (got %lld, %lld)", (long long)R,
+                    (long long)C);
+    const int64_t m = R < C ? R : C;
+    if (R * C >= ((int64_t)1 << 31) || m * m >= ((int64_t)1 << 31))
+        return fail(FFN_EUNSUPPORTED, "R * C and min(R, C)^2 must be below 2^31");
+    if (B > 65535) return fail(FFN_EUNSUPPORTED, "B must be at most 65535 (got %lld)", (long long)B);
+    return FFN_OK;
+}
+
+size_t ffn_orthogonalize_workspace_size(int64_t B, int64_t R, int64_t C, int dtype) {
+    if (check_orthogonalize(B, R, C, dtype) != FFN_OK) return 0;
+    const size_t n = ffn::orthogonalize_layout(B, R, C).total;
+    return n ? n : kAlign;
+}
+
+int ffn_orthogonalize(const void* G, void* U, int64_t B, int64_t R, int64_t C, int dtype,
+                      int steps, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_orthogonalize(B, R, C, dtype);
+    if (rc) return rc;
+    if (steps < 1 || steps > 32) return fail(FFN_EINVAL, "steps must be 1 to 32 (got %d)", steps);
+    if (B > 0 && (!G || !U)) return fail(FFN_EINVAL, "G and U must not be NULL");
+    if (!workspace) return fail(FFN_EINVAL, "workspace must not be NULL");
+    if (G && !aligned16(G)) return fail(FFN_EALIGN, "G is not 16-byte aligned");
+    if (U && !aligned16(U)) return fail(FFN_EALIGN, "U is not 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+        return fail(FFN_EALIGN, "workspace is not 256-byte aligned");
+    const size_t need = ffn_orthogonalize_workspace_size(B, R, C, dtype);
+    if (workspace_bytes < need)
+        return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    if (B == 0) return ok();
+    rc = launched(ffn::launch_orthogonalize(G, dtype == FFN_F32, static_cast<uint16_t*>(U), B, R, C,
+                                            steps, static_cast<char*>(workspace),
+                                            reinterpret_cast<hipStream_t>(stream)),
+                  "orthogonalisation kernels");
+    if (rc) return rc;
+    return ok();
 }
 
 // ---------------------------------------------------------------- MoE

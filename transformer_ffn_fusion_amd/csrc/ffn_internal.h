@@ -190,6 +190,42 @@ size_t colsum_partial_floats(int64_t O, int64_t P);   // row-chunk partials of t
 hipError_t launch_ffn_backward(const BackwardIO& io, hipStream_t stream, void** events,
                                int n_events);
 
+// ---- layer norm (layernorm.hip)
+
+constexpr int64_t kLnMaxN = 32768;         // a row is held by one workgroup's registers
+constexpr int64_t kLnBackwardBlocks = 256; // most workgroups of the backward's row kernel
+size_t layernorm_partial_floats(int64_t M, int64_t N);   // the workgroups' column sums
+hipError_t launch_layernorm_forward(const void* X, const void* gamma, const void* beta, void* Y,
+                                    float* mean, float* rstd, int64_t M, int64_t N, bool f32,
+                                    float eps, hipStream_t stream);
+hipError_t launch_layernorm_backward(const void* X, const void* dY, const void* gamma,
+                                     const float* mean, const float* rstd, void* dX, float* dgamma,
+                                     float* dbeta, float* part, int64_t M, int64_t N, bool f32,
+                                     hipStream_t stream);
+
+// ---- SwiGLU backward (ffn_swiglu_backward.hip)
+
+struct SwigluBackwardIO {
+    const uint16_t *X = nullptr, *Wg = nullptr, *Wu = nullptr, *Wd = nullptr, *dY = nullptr;
+    uint16_t* dX = nullptr;                                     // M x N bf16
+    void *dWg = nullptr, *dWu = nullptr, *dWd = nullptr;        // bf16 or fp32
+    bool grad_f32 = false;
+    float* dH = nullptr;        // workspace, M x O fp32: dY Wd^T
+    uint16_t* H = nullptr;      // workspace, M x O bf16
+    uint16_t* dAB = nullptr;    // workspace, M x 2 O bf16: da, then db, per row
+    int64_t M = 0, N = 0, O = 0, P = 0;
+};
+hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream);
+
+// ---- orthogonalised updates (orthogonalize.hip)
+
+struct OrthogonalizeLayout {   // workspace byte offsets, 256-byte aligned
+    size_t hi[2], lo, sym, poly, diag, scale, norm, total;
+};
+OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C);
+hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B, int64_t R,
+                                int64_t C, int steps, char* ws, hipStream_t stream);
+
 // ---- measurement support (ceilings.hip): the box's own MFMA and HBM ceilings
 
 int ceiling_sink_floats();
