@@ -175,21 +175,6 @@ BackwardLayout backward_layout(int64_t M, int64_t O, int64_t P) {
     return L;
 }
 
-// ---- SwiGLU backward workspace layout
-struct SwigluBackwardLayout {
-    size_t dH = 0, H = 0, dAB = 0, total = 0;
-};
-
-SwigluBackwardLayout swiglu_backward_layout(int64_t M, int64_t O) {
-    SwigluBackwardLayout L;
-    size_t off = 0;
-    L.dH = off;      off += align_up(sizeof(float) * M * O);
-    L.H = off;       off += align_up(sizeof(uint16_t) * M * O);
-    L.dAB = off;     off += align_up(sizeof(uint16_t) * M * 2 * O);
-    L.total = off ? off : kAlign;
-    return L;
-}
-
 // ---- MoE workspace layout
 struct MoeLayout {
     size_t ids, w, counts, offsets, sorted, pos, tiles, tile_count, blk_counts, blk_base, part,
@@ -629,7 +614,7 @@ int ffn_swiglu_forward_traced(const void* X, const void* Wg, const void* Wu, con
 
 size_t ffn_swiglu_backward_workspace_size(int64_t M, int64_t N, int64_t O, int64_t P, int dtype) {
     if (check_dims(M, N, O, P) != FFN_OK || dtype != FFN_BF16) return 0;
-    return swiglu_backward_layout(M, O).total;
+    return ffn::swiglu_backward_layout(M, N, O, P).total;
 }
 
 int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const void* Wd,
@@ -655,9 +640,9 @@ int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const voi
         if (ps[i] && !aligned16(ps[i])) return fail(FFN_EALIGN, "%s is not 16-byte aligned", nm[i]);
     if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
         return fail(FFN_EALIGN, "workspace is not 256-byte aligned");
-    const SwigluBackwardLayout L = swiglu_backward_layout(M, O);
-    if (workspace_bytes < L.total)
-        return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
+    const size_t need = ffn::swiglu_backward_layout(M, N, O, P).total;
+    if (workspace_bytes < need)
+        return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (M == 0) {
         const int64_t words = grad_dtype == FFN_F32 ? 1 : 2;   // gradients per 4-byte word
@@ -667,7 +652,6 @@ int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const voi
             if ((rc = launched(ffn::launch_zero_f32((float*)zp[i], zn[i], st), "zero fill"))) return rc;
         return ok();
     }
-    char* ws = static_cast<char*>(workspace);
     ffn::SwigluBackwardIO io;
     io.X = static_cast<const uint16_t*>(X);
     io.Wg = static_cast<const uint16_t*>(Wg);
@@ -679,9 +663,7 @@ int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const voi
     io.dWu = dWu;
     io.dWd = dWd;
     io.grad_f32 = grad_dtype == FFN_F32;
-    io.dH = reinterpret_cast<float*>(ws + L.dH);
-    io.H = reinterpret_cast<uint16_t*>(ws + L.H);
-    io.dAB = reinterpret_cast<uint16_t*>(ws + L.dAB);
+    io.ws = static_cast<char*>(workspace);
     io.M = M;
     io.N = N;
     io.O = O;

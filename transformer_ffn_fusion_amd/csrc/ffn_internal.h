@@ -210,17 +210,24 @@ struct SwigluBackwardIO {
     uint16_t* dX = nullptr;                                     // M x N bf16
     void *dWg = nullptr, *dWu = nullptr, *dWd = nullptr;        // bf16 or fp32
     bool grad_f32 = false;
-    float* dH = nullptr;        // workspace, M x O fp32: dY Wd^T
-    uint16_t* H = nullptr;      // workspace, M x O bf16
-    uint16_t* dAB = nullptr;    // workspace, M x 2 O bf16: da, then db, per row
+    char* ws = nullptr;         // swiglu_backward_layout
     int64_t M = 0, N = 0, O = 0, P = 0;
 };
+struct SwigluBackwardLayout {   // workspace byte offsets, 256-byte aligned
+    size_t dH;                  // M x O fp32: dY Wd^T
+    size_t H;                   // M x O bf16
+    size_t dAB;                 // M x 2 O bf16: da, then db, per row
+    size_t part, count, total;  // joins of split products: sums, one counter per tile
+    int64_t counters;
+};
+SwigluBackwardLayout swiglu_backward_layout(int64_t M, int64_t N, int64_t O, int64_t P);
 hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream);
 
 // ---- orthogonalised updates (orthogonalize.hip)
 
 struct OrthogonalizeLayout {   // workspace byte offsets, 256-byte aligned
-    size_t hi[2], lo, sym, poly, diag, scale, norm, total;
+    size_t hi[2], lo, sym, poly, diag, scale, norm, part, count, total;
+    int64_t counters;
 };
 OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C);
 hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B, int64_t R,

@@ -27,16 +27,16 @@ namespace ffn {
 
 namespace {
 
-using Large = TileCfg<256, 256, 2, 4>;   // eight waves, one workgroup per CU
-using Small = TileCfg<128, 128, 2, 2>;   // four waves, two workgroups per CU
-
 struct SwigluBackwardArgs {
     const uint16_t *X, *Wg, *Wu, *Wd, *dY;
     uint16_t* dX;
     void *dWg, *dWu, *dWd;
     float* dH;
     uint16_t *H, *dAB;
+    float* part;        // sums of split products (tile_join)
+    uint32_t* count;
     int64_t M, N, O, P;
+    int splits;         // of this step
 };
 
 // The steps above.  GATED's tile holds the gate's columns in its first half and
@@ -53,6 +53,15 @@ struct StepShape {
     // output columns, in the tile's terms (the gated step: hidden columns, TJ / 2 a tile)
     static __host__ __device__ int64_t cols(int64_t N, int64_t O, int64_t P) {
         return kStep == STEP_DX ? N : kStep == STEP_DGU ? 2 * O : kStep == STEP_DD ? P : O;
+    }
+    // k-tiles, over both products of the dX step
+    static __host__ __device__ int depth(int64_t M, int64_t N, int64_t O, int64_t P) {
+        const int64_t K = kStep == STEP_DH ? P : kStep == STEP_GATED ? N : kStep == STEP_DX ? O : M;
+        return (int)((K + kTileK - 1) / kTileK) * (kStep == STEP_DX ? 2 : 1);
+    }
+    static TilePlan plan(int64_t M, int64_t N, int64_t O, int64_t P) {
+        return tile_plan(rows(M, N, O), cols(N, O, P), kStep == STEP_GATED ? 2 : 1,
+                         depth(M, N, O, P), 1, false);
     }
     template <class Cfg>
     static __host__ __device__ constexpr int width() {
@@ -78,44 +87,44 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
     const int64_t M = g.M, N = g.N, O = g.O, P = g.P;
     const int64_t I = S::rows(M, N, O), J = S::cols(N, O, P);
     constexpr int kWidth = S::template width<Cfg>();
-    int64_t ti, tj;
-    if (!tile_place(blockIdx.x, (I + Cfg::TI - 1) / Cfg::TI, (J + kWidth - 1) / kWidth, &ti, &tj))
+    TilePlace at;
+    if (!tile_place<false>(blockIdx.x, (I + Cfg::TI - 1) / Cfg::TI, (J + kWidth - 1) / kWidth,
+                           g.splits, &at))
         return;
-    const int64_t i0 = ti * Cfg::TI, j0 = tj * kWidth;
+    const int64_t i0 = at.ti * Cfg::TI, j0 = at.tj * kWidth;
 
-    TileOps op;
-    op.pairs = kStep == STEP_DX ? 2 : 1;
-    const uint16_t *A, *B, *A2 = nullptr, *B2 = nullptr;
+    TileOperand A, B;
+    int64_t K;
+    const uint16_t *a2 = nullptr, *b2 = nullptr, *b_half2 = nullptr;
     if constexpr (kStep == STEP_DH) {
-        A = g.dY; op.lda = P; B = g.Wd; op.ldb = P; op.K = P;
+        A.p = g.dY; A.ld = P; B.p = g.Wd; B.ld = P; K = P;
     } else if constexpr (kStep == STEP_GATED) {
-        A = g.X; op.lda = N; B = g.Wg; op.ldb = O; op.K = N;
+        A.p = g.X; A.ld = N; B.p = g.Wg; B.ld = O; K = N;
+        b_half2 = g.Wu;
     } else if constexpr (kStep == STEP_DX) {
-        A = g.dAB; op.lda = 2 * O; B = g.Wg; op.ldb = O; op.K = O;
-        A2 = g.dAB + O; B2 = g.Wu;
+        A.p = g.dAB; A.ld = 2 * O; B.p = g.Wg; B.ld = O; K = O;
+        a2 = g.dAB + O; b2 = g.Wu;
     } else if constexpr (kStep == STEP_DGU) {
-        A = g.X; op.lda = N; B = g.dAB; op.ldb = 2 * O; op.K = M;
+        A.p = g.X; A.ld = N; B.p = g.dAB; B.ld = 2 * O; K = M;
     } else {
-        A = g.H; op.lda = O; B = g.dY; op.ldb = P; op.K = M;
+        A.p = g.H; A.ld = O; B.p = g.dY; B.ld = P; K = M;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        op.a[0][h] = half_walk<S::kAS>(A, op.lda, I, op.K, i0 + h * Cfg::HI);
-        if constexpr (kStep == STEP_GATED)
-            op.b[0][h] = half_walk<S::kBS>(h ? g.Wu : g.Wg, op.ldb, J, op.K, j0);
-        else
-            op.b[0][h] = half_walk<S::kBS>(B, op.ldb, J, op.K, j0 + h * Cfg::HJ);
-        if constexpr (kStep == STEP_DX) {
-            op.a[1][h] = half_walk<S::kAS>(A2, op.lda, I, op.K, i0 + h * Cfg::HI);
-            op.b[1][h] = half_walk<S::kBS>(B2, op.ldb, J, op.K, j0 + h * Cfg::HJ);
-        } else {
-            op.a[1][h] = op.a[0][h];
-            op.b[1][h] = op.b[0][h];
-        }
-    }
+    A.n = I;
+    B.n = J;
+    A.at[0] = i0;
+    A.at[1] = i0 + Cfg::HI;
+    B.at[0] = j0;
+    B.at[1] = kStep == STEP_GATED ? j0 : j0 + Cfg::HJ;
+    constexpr int kPairs = kStep == STEP_DX ? 2 : 1;
+    const int nt = S::depth(M, N, O, P), depth = (nt + g.splits - 1) / g.splits;
+    const int t0 = at.split * depth, t1 = t0 + depth < nt ? t0 + depth : nt;
     TileAcc<Cfg> acc;
     tile_clear<Cfg>(acc);
-    tile_product<Cfg, S::kAS, S::kBS, false>(smem, op, acc);
+    tile_product<Cfg, S::kAS, S::kBS, false, kPairs>(smem, A, B, K, a2, b2, b_half2, t0, t1, acc);
+    if (g.splits > 1 &&
+        !tile_join<Cfg>(smem, g.part + at.tile * g.splits * (Cfg::TI * Cfg::TJ), g.count + at.tile,
+                        at.split, g.splits, acc))
+        return;
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -178,31 +187,25 @@ hipError_t launch_step_cfg(const SwigluBackwardArgs& g, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const int64_t I = S::rows(g.M, g.N, g.O), J = S::cols(g.N, g.O, g.P);
     constexpr int kWidth = S::template width<Cfg>();
-    const int64_t grid = tile_grid((I + Cfg::TI - 1) / Cfg::TI, (J + kWidth - 1) / kWidth);
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::kThreads), Cfg::kLds, stream, g);
+    const int64_t tiles = tile_count((I + Cfg::TI - 1) / Cfg::TI, (J + kWidth - 1) / kWidth, false);
+    hipLaunchKernelGGL(kern, dim3((unsigned)tile_grid(tiles, g.splits)), dim3(Cfg::kThreads),
+                       Cfg::kLds, stream, g);
     return hipGetLastError();
 }
 
-// Tile choice: the fewer rounds of the chip's CUs, weighted by what a round
-// takes.  A round of large tiles (one per CU) does four times the work of a
-// round of small ones at two per CU in 1 / 0.65 of the time.
 template <int kStep, bool kGradF32>
-hipError_t launch_step(const SwigluBackwardArgs& g, hipStream_t stream) {
-    using S = StepShape<kStep>;
-    const int64_t I = S::rows(g.M, g.N, g.O), J = S::cols(g.N, g.O, g.P), cus = device_cus();
-    const int64_t large = ((I + Large::TI - 1) / Large::TI) *
-                          ((J + S::template width<Large>() - 1) / S::template width<Large>());
-    const int64_t small = ((I + Small::TI - 1) / Small::TI) *
-                          ((J + S::template width<Small>() - 1) / S::template width<Small>());
-    const double t_large = (double)((large + cus - 1) / cus);
-    const double t_small = 0.65 * (double)((small + 2 * cus - 1) / (2 * cus));
-    if (t_large <= t_small) return launch_step_cfg<Large, kStep, kGradF32>(g, stream);
-    return launch_step_cfg<Small, kStep, kGradF32>(g, stream);
+hipError_t launch_step(SwigluBackwardArgs g, hipStream_t stream) {
+    const TilePlan plan = StepShape<kStep>::plan(g.M, g.N, g.O, g.P);
+    g.splits = plan.splits;
+    if (plan.tile == TILE_LARGE) return launch_step_cfg<TileLarge, kStep, kGradF32>(g, stream);
+    if (plan.tile == TILE_MID) return launch_step_cfg<TileMid, kStep, kGradF32>(g, stream);
+    return launch_step_cfg<TileSmall, kStep, kGradF32>(g, stream);
 }
 
 template <bool kGradF32>
-hipError_t launch_all(const SwigluBackwardArgs& g, hipStream_t stream) {
-    hipError_t e;
+hipError_t launch_all(const SwigluBackwardArgs& g, int64_t counters, hipStream_t stream) {
+    hipError_t e = launch_zero_f32(reinterpret_cast<float*>(g.count), counters, stream);
+    if (e != hipSuccess) return e;
     if ((e = launch_step<STEP_DH, false>(g, stream)) != hipSuccess) return e;
     if ((e = launch_step<STEP_GATED, false>(g, stream)) != hipSuccess) return e;
     if ((e = launch_step<STEP_DX, false>(g, stream)) != hipSuccess) return e;
@@ -210,12 +213,63 @@ hipError_t launch_all(const SwigluBackwardArgs& g, hipStream_t stream) {
     return launch_step<STEP_DD, kGradF32>(g, stream);
 }
 
+// What the five steps' joins need at most: they run one after the other.
+TilePlan join_need(int64_t M, int64_t N, int64_t O, int64_t P) {
+    TilePlan most{0, 1, 0, 0};
+    const TilePlan plans[] = {StepShape<STEP_DH>::plan(M, N, O, P), StepShape<STEP_GATED>::plan(M, N, O, P),
+                              StepShape<STEP_DX>::plan(M, N, O, P), StepShape<STEP_DGU>::plan(M, N, O, P),
+                              StepShape<STEP_DD>::plan(M, N, O, P)};
+    for (const TilePlan& p : plans) {
+        if (p.part_floats > most.part_floats) most.part_floats = p.part_floats;
+        if (p.counters > most.counters) most.counters = p.counters;
+    }
+    return most;
+}
+
 }  // namespace
 
+SwigluBackwardLayout swiglu_backward_layout(int64_t M, int64_t N, int64_t O, int64_t P) {
+    SwigluBackwardLayout L;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    const TilePlan join = M > 0 ? join_need(M, N, O, P) : TilePlan{0, 1, 0, 0};
+    L.dH = take(sizeof(float) * M * O);
+    L.H = take(sizeof(uint16_t) * M * O);
+    L.dAB = take(sizeof(uint16_t) * M * 2 * O);
+    L.part = take(sizeof(float) * join.part_floats);
+    L.count = take(sizeof(uint32_t) * join.counters);
+    L.counters = join.counters;
+    L.total = off ? off : 256;
+    return L;
+}
+
 hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream) {
-    const SwigluBackwardArgs g{io.X,  io.Wg,  io.Wu, io.Wd, io.dY,  io.dX, io.dWg, io.dWu,
-                               io.dWd, io.dH, io.H,  io.dAB, io.M, io.N,  io.O,   io.P};
-    return io.grad_f32 ? launch_all<true>(g, stream) : launch_all<false>(g, stream);
+    const SwigluBackwardLayout L = swiglu_backward_layout(io.M, io.N, io.O, io.P);
+    SwigluBackwardArgs g;
+    g.X = io.X;
+    g.Wg = io.Wg;
+    g.Wu = io.Wu;
+    g.Wd = io.Wd;
+    g.dY = io.dY;
+    g.dX = io.dX;
+    g.dWg = io.dWg;
+    g.dWu = io.dWu;
+    g.dWd = io.dWd;
+    g.dH = reinterpret_cast<float*>(io.ws + L.dH);
+    g.H = reinterpret_cast<uint16_t*>(io.ws + L.H);
+    g.dAB = reinterpret_cast<uint16_t*>(io.ws + L.dAB);
+    g.part = reinterpret_cast<float*>(io.ws + L.part);
+    g.count = reinterpret_cast<uint32_t*>(io.ws + L.count);
+    g.M = io.M;
+    g.N = io.N;
+    g.O = io.O;
+    g.P = io.P;
+    g.splits = 1;
+    return io.grad_f32 ? launch_all<true>(g, L.counters, stream) : launch_all<false>(g, L.counters, stream);
 }
 
 }  // namespace ffn

@@ -5,10 +5,8 @@
 //
 // Each operand is either k-contiguous (element (i, k) at i * ld + k) or
 // k-strided (element (i, k) at k * ld + i), chosen at compile time.  Both are
-// staged by direct global->LDS loads in 1 KiB units, in the layouts of
-// ffn_device.h: a k-contiguous unit is one 16-index x 32-deep fragment, a
-// k-strided one a block of 8 k-rows x 64 indices that the transposing LDS read
-// turns into fragments.
+// staged by direct global->LDS loads; a k-strided one becomes fragments through
+// the transposing LDS read.
 //
 // Schedule.  A k-tile is 64 deep and cut into four half-tiles: the first and
 // second half of A's indices (A0, A1) and of B's (B0, B1).  One k-tile takes
@@ -85,129 +83,174 @@ using TileAcc = floatx4_t[2][2][Cfg::FI][Cfg::FJ];
 __device__ __forceinline__ void tile_barrier() { asm volatile("s_barrier" ::: "memory"); }
 __device__ __forceinline__ void tile_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// One operand half on its way through k: where the next k-tile starts and how
-// many bytes lie between there and the operand's end.
-struct HalfWalk {
-    uint64_t at;
-    int64_t left;
+// One operand of a tile: its first element, leading dimension and index count,
+// and the first index of each half-tile.
+struct TileOperand {
+    const uint16_t* p;
+    int64_t ld, n;
+    int64_t at[2];
 };
 
-// A half starting at index i0 of an operand of n indices and depth K.
-template <bool kStrided>
-__device__ __forceinline__ HalfWalk half_walk(const uint16_t* p, int64_t ld, int64_t n, int64_t K,
-                                              int64_t i0) {
-    HalfWalk h;
-    const int64_t off = (kStrided ? i0 : i0 * ld) * 2;
-    h.at = reinterpret_cast<uint64_t>(p) + (uint64_t)off;
-    h.left = (kStrided ? K * ld : n * ld) * 2 - off;
-    return h;
+// Direct load of 16 bytes per lane from `base` + the lane's offset to LDS address
+// `lds` (+ 16 per lane); past the end (`any` false) or out of range it brings
+// zeros and reads no memory.  Every lane's offset is in bounds or kOOB, so the
+// resource's size only has to refuse kOOB.
+__device__ __forceinline__ void tile_dma(uint64_t base, bool any, uint32_t off, uint32_t lds) {
+    int32x4_t srd;
+    srd.x = (int)(uint32_t)base;
+    srd.y = (int)(uint32_t)(base >> 32);
+    srd.z = any ? 0x7fffffff : 0;
+    srd.w = kRsrcWord3;
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(lds), "v"(off), "s"(srd)
+        : "m0");
 }
 
-// What a wave loads of a half-tile of H indices: unit u = wave + W x covers, of
-// a k-contiguous operand, fragment u % (H / 16) of k-half u / (H / 16); of a
-// k-strided one block (r, c) of k-half u / (H / 16), with u % (H / 16) =
-// r (H / 64) + c.
+// LDS layouts of a half-tile (H indices x 64 k), in 1 KiB units whose slot l (16
+// bytes) is written by lane l of the loading wave.  LDS serves 256 bytes a cycle.
+//
+//  k-contiguous: unit q holds indices 8q .. 8q + 7, a whole 128-byte line of each;
+//  the 8-deep k-group c of index r lies in slot 8r + (c ^ r).  A fragment read
+//  takes k-group 4 kh + lane / 16 of index lane % 16 = 8q + r: 8 lanes with the
+//  same k-group fill the 8 slots' columns, no bank conflicts.  (Units of 16
+//  indices x 32 k read half lines: 8192^3 734 us against 6xx.)
+//
+//  k-strided: unit (kh, g, c) holds k-rows 32 kh + 8 g .. + 7 and indices 64 c ..
+//  64 c + 63, 128 contiguous bytes a row; the 8-index group u of row r lies in
+//  slot 8r + (u ^ 2 (r + g) mod 8).  One transposing read takes, per 16 lanes, 4
+//  rows x 2 neighbouring groups; with the row in the swizzle the 16 lanes cover
+//  half of the 256 bytes, with the parity of g the next 16 lanes the other half.
+__device__ __forceinline__ int strided_swizzle(int r, int g) { return 2 * (r ^ (g & 1)) & 7; }
+
+// What a wave loads of a half-tile: units wave, wave + W, ...
 template <bool kStrided, int H, int W, int U>
 struct HalfLoads {
-    uint32_t off[U];    // byte offsets of this lane's 16 bytes, from the half's place
-    uint32_t tail[U];   // the same in the last k-tile: out of range past K
+    uint32_t off[2][U];   // this lane's byte offset from the k-tile, per half; kOOB past the indices
+    bool past[U];         // in the last k-tile: past K
+    uint64_t base[2];     // where each half's next k-tile starts
 
-    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t K) {
+    __device__ __forceinline__ void init(const TileOperand& o, int64_t K, int wave, int lane) {
         const int rem = (int)(K - (K - 1) / kTileK * kTileK);   // 1 .. 64
 #pragma unroll
         for (int x = 0; x < U; ++x) {
-            const int u = wave + W * x, kh = u / (H / 16), q = u % (H / 16);
+            const int u = wave + W * x, r = lane >> 3;
+            int i, k;   // this lane's first index and k, in the half-tile
+            uint32_t at;
             if constexpr (kStrided) {
-                const int r = q / (H / 64), c = q % (H / 64);
-                off[x] = (uint32_t)((32 * kh + 8 * r) * ld * 2) + 128u * c +
-                         wtile_dma_off(lane, (uint32_t)(ld * 2));
-                tail[x] = off[x];
+                const int kh = u / (H / 16), g = u % (H / 16) / (H / 64), c = u % (H / 64);
+                i = 64 * c + 8 * ((lane & 7) ^ strided_swizzle(r, g));
+                k = 32 * kh + 8 * g + r;
+                at = (uint32_t)k * (uint32_t)(o.ld * 2) + 2u * i;
             } else {
-                const int k = 32 * kh + 8 * ((lane & 3) ^ ((lane >> 3) & 3));
-                off[x] = (uint32_t)((16 * q + (lane >> 2)) * ld * 2) + 2u * k;
-                tail[x] = k < rem ? off[x] : kOOB;
+                i = 8 * u + r;
+                k = 8 * ((lane & 7) ^ r);
+                at = (uint32_t)i * (uint32_t)(o.ld * 2) + 2u * k;
             }
+            past[x] = k >= rem;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) off[h][x] = o.at[h] + i < o.n ? at : kOOB;
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) start(o.p, o.ld, o.at[h], h);
     }
-    // Loads the k-tile at `h` to `dst` (the half-tile's place in LDS) and moves on.
-    __device__ __forceinline__ void issue(HalfWalk& h, int64_t step, bool any, bool last, int wave,
-                                          char* dst) const {
-        const int32x4_t srd = make_srd(reinterpret_cast<const void*>(h.at), any ? h.left : 0);
+    __device__ __forceinline__ void start(const uint16_t* p, int64_t ld, int64_t at, int h) {
+        const uint64_t b = reinterpret_cast<uint64_t>(p + (kStrided ? at : at * ld));
+        base[h] = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b) |
+                  (uint64_t)((uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) & 0xffffu) << 32;
+    }
+    // Loads half h's next k-tile to `lds` and moves on by `step` bytes.
+    __device__ __forceinline__ void issue(int h, bool any, bool last, uint64_t step, int wave,
+                                          uint32_t lds) {
 #pragma unroll
         for (int x = 0; x < U; ++x)
-            dma16(srd, !kStrided && last ? tail[x] : off[x], dst + (wave + W * x) * 1024);
-        h.at += (uint64_t)step;
-        h.left -= step;
+            tile_dma(base[h], any, last && past[x] ? kOOB : off[h][x], lds + (wave + W * x) * 1024);
+        base[h] += step;
     }
 };
 
 // Fragment f (of the half-tile's H / 16) of k-half kh, for this lane.
 template <bool kStrided, int H>
 __device__ __forceinline__ uint4 half_frag(const char* half, int f, int kh, int lane) {
-    const char* st = half + kh * (H / 16) * 1024;
+    const int g = lane >> 4;
     if constexpr (!kStrided) {
-        return ld16(st + f * kFrag + 16 * xfrag_slot(lane & 15, lane >> 4));
+        const int i = lane & 15, r = i & 7;
+        return ld16(half + f * 2048 + (i >> 3) * 1024 + r * 128 + 16 * ((4 * kh + g) ^ r));
     } else {
-        const char* p = st + wtile_tr_base(lane, H / 64, f & 3) + 1024 * (f >> 2);
+        // the 8-byte chunk this lane supplies: row j of the read's four, 8-index group
+        // 2f + q / 2, half q % 2 of it; the second read takes rows j + 4
+        const int j = (lane & 15) >> 2, q = lane & 3;
+        const char* p = half + (kh * (H / 16) + g * (H / 64) + (f >> 2)) * 1024 + 128 * j +
+                        16 * ((2 * (f & 3) + (q >> 1)) ^ strided_swizzle(j, g)) + 8 * (q & 1);
         const uint2 lo = lds_read_tr16(p);
-        const uint2 hi = lds_read_tr16(p + 512);
+        const uint2 hi = lds_read_tr16(p + 512);   // (j + 4 swizzles as j does)
         return make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
 }
 
-// The operands of one tile.  A sum over two products with the same depth and
-// leading dimensions (C = A B^T + A' B'^T) walks the second pair after the
-// first: set `pairs` to 2.
-struct TileOps {
-    HalfWalk a[2][2], b[2][2];   // [pair][half]
-    int64_t lda, ldb;
-    int64_t K;                   // depth of each pair, at least 1
-    int pairs;
-};
-
-// acc += the tile's product.  smem: Cfg::kLds bytes.  Every wave of the
-// workgroup calls it; on return the LDS is free and every wave has passed a
-// common barrier.
-template <class Cfg, bool kAS, bool kBS, bool kF16>
-__device__ __forceinline__ void tile_product(char* smem, const TileOps& op, TileAcc<Cfg>& acc) {
+// acc += A B^T over depth K (at least 1), and with kPairs = 2 + A' B'^T of the same
+// depth, leading dimensions and indices, A' and B' starting at a2 and b2 (for halves
+// of one operand that lie in two matrices, b_half2 is where the second half's
+// operand starts; else null).  smem: Cfg::kLds bytes.  Every wave of the workgroup
+// calls it; on return the LDS is free and every wave has passed a common barrier.
+// The k-tiles t0 <= t < t1 of the ceil(K / 64) kPairs there are (t0 < t1).
+template <class Cfg, bool kAS, bool kBS, bool kF16, int kPairs>
+__device__ __forceinline__ void tile_product(char* smem, const TileOperand& A, const TileOperand& B,
+                                             int64_t K, const uint16_t* a2, const uint16_t* b2,
+                                             const uint16_t* b_half2, int t0, int t1,
+                                             TileAcc<Cfg>& acc) {
     constexpr int FI = Cfg::FI, FJ = Cfg::FJ, UA = Cfg::UA, UB = Cfg::UB;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wi = wave / Cfg::WJ, wj = wave % Cfg::WJ;
-    const int per = (int)((op.K + kTileK - 1) / kTileK);   // k-tiles of a pair
-    const int nt = per * op.pairs;
-    const int64_t step_a = kAS ? op.lda * kTileK * 2 : kTileK * 2;
-    const int64_t step_b = kBS ? op.ldb * kTileK * 2 : kTileK * 2;
+    const int per = (int)((K + kTileK - 1) / kTileK);   // k-tiles of a pair
+    const int nt = per * kPairs;
+    const uint64_t step_a = (uint64_t)(kAS ? A.ld * kTileK * 2 : kTileK * 2);
+    const uint64_t step_b = (uint64_t)(kBS ? B.ld * kTileK * 2 : kTileK * 2);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)((lds_void_t*)smem);
 
     HalfLoads<kAS, Cfg::HI, Cfg::kWaves, UA> la;
     HalfLoads<kBS, Cfg::HJ, Cfg::kWaves, UB> lb;
-    la.init(wave, lane, op.lda, op.K);
-    lb.init(wave, lane, op.ldb, op.K);
-    HalfWalk a[2] = {op.a[0][0], op.a[0][1]}, b[2] = {op.b[0][0], op.b[0][1]};
+    la.init(A, K, wave, lane);
+    lb.init(B, K, wave, lane);
+    if (b_half2) lb.start(b_half2, B.ld, B.at[1], 1);
+    if (kPairs == 2 && t0 >= per) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            la.start(a2, A.ld, A.at[h], h);
+            lb.start(b2, B.ld, B.at[h], h);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        la.base[h] += step_a * (uint64_t)(t0 >= per ? t0 - per : t0);
+        lb.base[h] += step_b * (uint64_t)(t0 >= per ? t0 - per : t0);
+    }
 
-    auto place_a = [&](int t, int h) { return smem + (t & 1) * Cfg::kBuf + h * Cfg::kHalfA; };
-    auto place_b = [&](int t, int h) {
-        return smem + (t & 1) * Cfg::kBuf + 2 * Cfg::kHalfA + h * Cfg::kHalfB;
+    // k-tile t lies in LDS buffer (t - t0) % 2, `buf` below
+    auto load_a = [&](int t, int buf, int h) {
+        if (kPairs == 2 && t == per && t > t0) la.start(a2, A.ld, A.at[h], h);
+        la.issue(h, t < t1, t == nt - 1 || (kPairs == 2 && t == per - 1), step_a, wave,
+                 lds0 + buf * Cfg::kBuf + h * Cfg::kHalfA);
     };
-    auto load_a = [&](int t, int h) {
-        if (t == per) a[h] = op.a[1][h];   // the second pair (or past the end)
-        la.issue(a[h], step_a, t < nt, t == per - 1 || t == nt - 1, wave, place_a(t, h));
-    };
-    auto load_b = [&](int t, int h) {
-        if (t == per) b[h] = op.b[1][h];
-        lb.issue(b[h], step_b, t < nt, t == per - 1 || t == nt - 1, wave, place_b(t, h));
+    auto load_b = [&](int t, int buf, int h) {
+        if (kPairs == 2 && t == per && t > t0) lb.start(b2, B.ld, B.at[h], h);
+        lb.issue(h, t < t1, t == nt - 1 || (kPairs == 2 && t == per - 1), step_b, wave,
+                 lds0 + buf * Cfg::kBuf + 2 * Cfg::kHalfA + h * Cfg::kHalfB);
     };
 
-    uint4 fa[FI][2], fb0[FJ][2], fb1[FJ][2], fbn[FJ][2];
-    auto read_a = [&](int t, int h) {
-        const char* p = place_a(t, h);
+    uint4 fa[FI][2], fb[FJ][2], fb0[2][FJ][2];   // fb0: B0 of the even and of the odd k-tiles
+    auto read_a = [&](int buf, int h) {
+        const char* p = smem + buf * Cfg::kBuf + h * Cfg::kHalfA;
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh)
 #pragma unroll
             for (int x = 0; x < FI; ++x) fa[x][kh] = half_frag<kAS, Cfg::HI>(p, FI * wi + x, kh, lane);
     };
-    auto read_b = [&](int t, int h, uint4 (&f)[FJ][2]) {
-        const char* p = place_b(t, h);
+    auto read_b = [&](int buf, int h, uint4 (&f)[FJ][2]) {
+        const char* p = smem + buf * Cfg::kBuf + 2 * Cfg::kHalfA + h * Cfg::kHalfB;
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh)
 #pragma unroll
@@ -215,6 +258,7 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOps& op, Tile
     };
     // the middle and the end of a phase: products of the held A half with f
     auto multiply = [&](floatx4_t (&c)[FI][FJ], const uint4 (&f)[FJ][2]) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         tile_fence();
         tile_barrier();
         tile_fence();
@@ -229,44 +273,49 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOps& op, Tile
                     c[x][y] = mfma16<kF16>(f[y][kh], fa[x][kh], c[x][y]);
         if constexpr (Cfg::kPingPong) __builtin_amdgcn_s_setprio(0);
         tile_fence();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         if constexpr (Cfg::kPingPong) tile_barrier();
         tile_fence();
     };
+    // the four phases of k-tile t, which lies in buffer `buf`
+    auto k_tile = [&](int t, int buf) __attribute__((always_inline)) {
+        read_a(buf, 0);
+        tile_fence();
+        load_a(t + 1, buf ^ 1, 1);
+        wait_vmcnt<3 * UA + 2 * UB>();
+        multiply(acc[0][0], fb0[buf]);
+        read_b(buf, 1, fb);
+        tile_fence();
+        load_b(t + 2, buf, 0);
+        wait_vmcnt<2 * UA + 3 * UB>();
+        multiply(acc[0][1], fb);
+        read_a(buf, 1);
+        tile_fence();
+        load_a(t + 2, buf, 0);
+        wait_vmcnt<3 * UA + 2 * UB>();
+        multiply(acc[1][1], fb);
+        read_b(buf ^ 1, 0, fb0[buf ^ 1]);   // past the last k-tile: zeros, not used
+        tile_fence();
+        load_b(t + 2, buf, 1);
+        wait_vmcnt<2 * UA + 3 * UB>();
+        multiply(acc[1][0], fb0[buf]);
+    };
 
-    load_b(0, 0);
-    load_a(0, 0);
-    load_b(0, 1);
-    load_a(0, 1);
-    load_b(1, 0);
-    load_a(1, 0);
-    load_b(1, 1);
+    load_b(t0, 0, 0);
+    load_a(t0, 0, 0);
+    load_b(t0, 0, 1);
+    load_a(t0, 0, 1);
+    load_b(t0 + 1, 1, 0);
+    load_a(t0 + 1, 1, 0);
+    load_b(t0 + 1, 1, 1);
     wait_vmcnt<2 * UA + 3 * UB>();
     tile_barrier();
     if (Cfg::kPingPong && wave >= Cfg::kWaves / 2) tile_barrier();
-    read_b(0, 0, fb0);
-    for (int t = 0; t < nt; ++t) {
-        read_a(t, 0);
-        load_a(t + 1, 1);
-        wait_vmcnt<3 * UA + 2 * UB>();
-        multiply(acc[0][0], fb0);
-        read_b(t, 1, fb1);
-        load_b(t + 2, 0);
-        wait_vmcnt<2 * UA + 3 * UB>();
-        multiply(acc[0][1], fb1);
-        read_a(t, 1);
-        load_a(t + 2, 0);
-        wait_vmcnt<3 * UA + 2 * UB>();
-        multiply(acc[1][1], fb1);
-        read_b(t + 1, 0, fbn);   // past the last k-tile: zeros, not used
-        load_b(t + 2, 1);
-        wait_vmcnt<2 * UA + 3 * UB>();
-        multiply(acc[1][0], fb0);
-#pragma unroll
-        for (int y = 0; y < FJ; ++y) {
-            fb0[y][0] = fbn[y][0];
-            fb0[y][1] = fbn[y][1];
-        }
+    read_b(0, 0, fb0[0]);
+    // two k-tiles a turn, so that every LDS place is a constant; an odd count is
+    // made even with a k-tile of zeros
+    for (int t = t0; t < t1; t += 2) {
+        k_tile(t, 0);
+        k_tile(t + 1, 1);
     }
     wait_vmcnt<0>();
     if (Cfg::kPingPong && wave < Cfg::kWaves / 2) tile_barrier();
@@ -297,25 +346,147 @@ __device__ __forceinline__ void tile_clear(TileAcc<Cfg>& acc) {
                 for (int y = 0; y < Cfg::FJ; ++y) acc[p][q][x][y] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 }
 
-// Workgroup -> output tile.  Workgroups reach the 8 XCDs round-robin and each
-// XCD has an L2 of its own: XCD x takes a contiguous run of a grouped order
-// (groups of 8 tile rows, rows fastest), a compact rectangle whose panels its
-// L2 shares.  Returns false for the padding workgroups.
-__host__ __device__ __forceinline__ int64_t tile_grid(int64_t nI, int64_t nJ) {
-    return 8 * ((nI * nJ + 7) / 8);
+// Work of one launch: nI x nJ output tiles (kTri: the lower triangle of a square
+// of nI x nI), each cut into `splits` ranges of k-tiles.  Workgroups reach the 8
+// XCDs round-robin and each XCD has an L2 of its own: XCD x takes a contiguous run
+// of a grouped order (groups of 8 tile rows, rows fastest; a tile's splits side by
+// side), a compact rectangle whose panels its L2 shares.
+struct TilePlace {
+    int64_t ti, tj, tile;   // tile: the tile's number
+    int split;
+};
+__host__ __device__ __forceinline__ int64_t tile_count(int64_t nI, int64_t nJ, bool tri) {
+    return tri ? nI * (nI + 1) / 2 : nI * nJ;
 }
-__device__ __forceinline__ bool tile_place(int64_t w, int64_t nI, int64_t nJ, int64_t* ti,
-                                           int64_t* tj) {
+__host__ __device__ __forceinline__ int64_t tile_grid(int64_t tiles, int splits) {
+    return 8 * ((tiles * splits + 7) / 8);
+}
+// Returns false for the padding workgroups.
+template <bool kTri>
+__device__ __forceinline__ bool tile_place(int64_t w, int64_t nI, int64_t nJ, int splits,
+                                           TilePlace* at) {
     constexpr int64_t G = 8;
-    const int64_t n = nI * nJ, per = (n + 7) / 8;
-    const int64_t t = (w & 7) * per + (w >> 3);
-    if (t >= n || (w >> 3) >= per) return false;
-    const int64_t r = t / (G * nJ);
-    const int64_t rows = nI - r * G < G ? nI - r * G : G;
-    const int64_t rem = t - r * G * nJ;
-    *tj = rem / rows;
-    *ti = r * G + rem % rows;
+    const int64_t n = tile_count(nI, nJ, kTri) * splits, per = (n + 7) / 8;
+    const int64_t u = (w & 7) * per + (w >> 3);
+    if (u >= n || (w >> 3) >= per) return false;
+    const int64_t t = u / splits;
+    at->tile = t;
+    at->split = (int)(u % splits);
+    if constexpr (kTri) {
+        int64_t r = (int64_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+        while (r * (r + 1) / 2 > t) --r;
+        while ((r + 1) * (r + 2) / 2 <= t) ++r;
+        at->ti = r;
+        at->tj = t - r * (r + 1) / 2;
+    } else {
+        const int64_t r = t / (G * nJ);
+        const int64_t rows = nI - r * G < G ? nI - r * G : G;
+        const int64_t rem = t - r * G * nJ;
+        at->tj = rem / rows;
+        at->ti = r * G + rem % rows;
+    }
     return true;
+}
+
+// The join of a tile's splits.  Each split's workgroup writes its sums, raises the
+// tile's counter, and the one that finds itself last adds all of them in ascending
+// split order (so the result does not depend on who is last) and goes on to the
+// epilogue; the others are done.  No workgroup waits for another.
+//
+// The sums cross XCDs, whose L2s are not coherent with each other: they are
+// written through to memory (sc0 sc1) and have arrived there (vmcnt 0 in every
+// wave, then the barrier) before the counter is raised, and the last workgroup
+// reads them with loads that do not stop at its L2 either.  A device-scope release
+// fence would write back the XCD's whole L2 instead.
+//
+// part: splits x (TI * TJ) floats of this tile; count: the tile's counter, 0 before
+// the first and again after the last split.  Returns whether to go on, with acc the
+// sum.  smem is used for one word.
+constexpr int kCpolThrough = 17;   // buffer cache-policy bits sc0, sc1: system scope
+
+template <class Cfg>
+__device__ __forceinline__ bool tile_join(char* smem, float* part, uint32_t* count, int split,
+                                          int splits, TileAcc<Cfg>& acc) {
+    constexpr int kFrags = 4 * Cfg::FI * Cfg::FJ;
+    constexpr uint32_t kBytes = (uint32_t)Cfg::TI * Cfg::TJ * 4;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(part, (int64_t)kBytes * splits);
+    const uint32_t lane_off = threadIdx.x * 16u;
+    floatx4_t* v = &acc[0][0][0][0];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned int, v[f]), rs,
+            lane_off + f * (Cfg::kThreads * 16), (int)(kBytes * (uint32_t)split), kCpolThrough);
+    wait_vmcnt<0>();
+    __syncthreads();
+    uint32_t* last = reinterpret_cast<uint32_t*>(smem);
+    if (threadIdx.x == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *last = before == (uint32_t)splits - 1;
+        if (*last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool go = *last != 0;
+    __syncthreads();   // the word is free again
+    if (!go) return false;
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) v[f] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) {
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+            v[f] += __builtin_bit_cast(floatx4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                      rs, lane_off + f * (Cfg::kThreads * 16),
+                                                      (int)(kBytes * (uint32_t)s), kCpolThrough));
+    }
+    return true;
+}
+
+// ---- host side: which tile, how many splits
+
+using TileLarge = TileCfg<256, 256, 2, 4>;   // eight waves, one workgroup per CU
+using TileMid = TileCfg<256, 128, 4, 2>;     // eight waves, one workgroup per CU
+using TileSmall = TileCfg<128, 128, 2, 2>;   // four waves, two workgroups per CU
+
+enum { TILE_LARGE = 0, TILE_MID = 1, TILE_SMALL = 2 };
+struct TilePlan {
+    int tile, splits;
+    int64_t part_floats, counters;   // workspace of the join (0 without splits)
+};
+
+// The plan with the least estimated time, in microseconds, for an I x J output (J
+// in the tile's terms: `share` operand columns of a tile belong to one output
+// column) of `nt` k-tiles, `batch` times.  Measured per k-tile with every CU at
+// work: 1.42 (large), 0.88 (mid), 0.95 (small, two per CU; 0.62 alone); a join
+// moves a tile's sums `splits` times through one CU at about 0.1 MB/us and costs
+// 2 us of latency.  Splits beyond one round of the CUs would only add work.
+inline TilePlan tile_plan(int64_t I, int64_t J, int share, int64_t nt, int64_t batch, bool tri) {
+    struct Kind { int ti, tj, slots; double per, bytes; };
+    const Kind kinds[3] = {{256, 256, 256, 1.42, 262144.0}, {256, 128, 256, 0.88, 131072.0},
+                           {128, 128, 512, 0.95, 65536.0}};
+    TilePlan best{TILE_LARGE, 1, 0, 0};
+    double best_t = 1e30;
+    for (int k = 0; k < 3; ++k) {
+        if (tri && kinds[k].ti != kinds[k].tj) continue;
+        const int64_t wj = kinds[k].tj / share;
+        const int64_t tiles = batch * tile_count((I + kinds[k].ti - 1) / kinds[k].ti, (J + wj - 1) / wj, tri);
+        for (int64_t s = 1; s <= 16 && s <= nt; ++s) {
+            if (s > 1 && tiles * s > kinds[k].slots) break;
+            const int64_t depth = (nt + s - 1) / s;
+            if ((nt + depth - 1) / depth != s) continue;   // an empty last split
+            const int64_t units = tiles * s;
+            const double per = k == TILE_SMALL && units <= 256 ? 0.62 : kinds[k].per;
+            double t = (double)((units + kinds[k].slots - 1) / kinds[k].slots) * (double)depth * per;
+            if (s > 1) t += 2.0 + (double)s * kinds[k].bytes * 1e-5;
+            if (t < best_t) {
+                best_t = t;
+                best.tile = k;
+                best.splits = (int)s;
+                best.part_floats = s > 1 ? units * (int64_t)kinds[k].ti * kinds[k].tj : 0;
+                best.counters = s > 1 ? tiles : 0;
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace ffn

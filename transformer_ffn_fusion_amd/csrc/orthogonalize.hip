@@ -37,9 +37,6 @@ namespace ffn {
 
 namespace {
 
-using Large = TileCfg<256, 256, 2, 4>;
-using Small = TileCfg<128, 128, 2, 2>;
-
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr double kNsEps = 1e-7;
 constexpr float kScaleX = 64.0f, kScaleSym = 1024.0f;
@@ -54,6 +51,10 @@ struct OrthoArgs {
     uint16_t *sym, *poly;   // off-diagonals of A and b A + c A^2, fp16, m x m
     float *diag, *scale;    // diagonals of A and of b A + c A^2
     double* norm;           // kNormBlocks partial sums per matrix
+    float* part;            // sums of split products, and a counter per tile (tile_join)
+    uint32_t* count;
+    int64_t counters;
+    int splits;             // of this product
     int64_t R, C, m, n;     // m = min(R, C), n = max(R, C)
     int last;               // the last step writes U
 };
@@ -98,6 +99,8 @@ template <bool kF32>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs g) {
     __shared__ double s[4];
     const int64_t size = g.R * g.C, base = (int64_t)blockIdx.y * size;
+    if (blockIdx.x == 0 && blockIdx.y == 0)   // before any product of this call
+        for (int64_t k = threadIdx.x; k < g.counters; k += 256) g.count[k] = 0;
     double q = 0.0;
     for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; k < size; k += kNormBlocks * 1024) {
         float v[4];
@@ -133,18 +136,21 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoArgs g) {
 }
 
 // PROD_SYM: E = offdiag(A), D.  PROD_POLY: b A + c A^2.  PROD_X: the step.
+// The first two are symmetric: only tiles on and below the diagonal are computed,
+// and each tile below it is also written transposed.
 enum { PROD_SYM = 0, PROD_POLY = 1, PROD_X = 2 };
 
 template <class Cfg, int kProd, bool kTall>
 __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     constexpr bool kAS = kProd == PROD_SYM && kTall;
     constexpr bool kBS = kProd == PROD_SYM ? kTall : kProd == PROD_X && !kTall;
+    constexpr bool kTri = kProd != PROD_X;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int64_t m = g.m, I = kProd == PROD_X ? g.R : m, J = kProd == PROD_X ? g.C : m;
-    int64_t ti, tj;
-    if (!tile_place(blockIdx.x, (I + Cfg::TI - 1) / Cfg::TI, (J + Cfg::TJ - 1) / Cfg::TJ, &ti, &tj))
-        return;
-    const int64_t i0 = ti * Cfg::TI, j0 = tj * Cfg::TJ;
+    const int64_t nI = (I + Cfg::TI - 1) / Cfg::TI, nJ = (J + Cfg::TJ - 1) / Cfg::TJ;
+    TilePlace at;
+    if (!tile_place<kTri>(blockIdx.x, nI, nJ, g.splits, &at)) return;
+    const int64_t i0 = at.ti * Cfg::TI, j0 = at.tj * Cfg::TJ;
     const int64_t at_x = (int64_t)blockIdx.y * g.R * g.C, at_m = (int64_t)blockIdx.y * m * m;
     const uint16_t* hi = g.hi + at_x;
     const uint16_t* poly = g.poly + at_m;
@@ -152,76 +158,58 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     float* diag = g.diag + blockIdx.y * m;
     float* scale = g.scale + blockIdx.y * m;
 
-    TileOps op;
-    op.pairs = 1;
-    const uint16_t *A, *B;
+    TileOperand A, B;
+    int64_t K;
     if constexpr (kProd == PROD_SYM) {
-        A = B = hi; op.lda = op.ldb = g.C; op.K = g.n;
+        A.p = B.p = hi; A.ld = B.ld = g.C; K = g.n;
     } else if constexpr (kProd == PROD_POLY) {
-        A = B = sym; op.lda = op.ldb = m; op.K = m;
+        A.p = B.p = sym; A.ld = B.ld = m; K = m;
     } else if constexpr (kTall) {
-        A = hi; op.lda = g.C; B = poly; op.ldb = m; op.K = m;   // X (poly), poly symmetric
+        A.p = hi; A.ld = g.C; B.p = poly; B.ld = m; K = m;   // X (poly), poly symmetric
     } else {
-        A = poly; op.lda = m; B = hi; op.ldb = g.C; op.K = m;   // (poly) X
+        A.p = poly; A.ld = m; B.p = hi; B.ld = g.C; K = m;   // (poly) X
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        op.a[0][h] = op.a[1][h] = half_walk<kAS>(A, op.lda, I, op.K, i0 + h * Cfg::HI);
-        op.b[0][h] = op.b[1][h] = half_walk<kBS>(B, op.ldb, J, op.K, j0 + h * Cfg::HJ);
-    }
+    A.n = I;
+    B.n = J;
+    A.at[0] = i0;
+    A.at[1] = i0 + Cfg::HI;
+    B.at[0] = j0;
+    B.at[1] = j0 + Cfg::HJ;
+    const int nt = (int)((K + kTileK - 1) / kTileK), depth = (nt + g.splits - 1) / g.splits;
+    const int t0 = at.split * depth, t1 = t0 + depth < nt ? t0 + depth : nt;
     TileAcc<Cfg> acc;
     tile_clear<Cfg>(acc);
-    tile_product<Cfg, kAS, kBS, true>(smem, op, acc);
+    tile_product<Cfg, kAS, kBS, true, 1>(smem, A, B, K, nullptr, nullptr, nullptr, t0, t1, acc);
+    if (g.splits > 1) {
+        const int64_t tile = (int64_t)blockIdx.y * tile_count(nI, nJ, kTri) + at.tile;
+        if (!tile_join<Cfg>(smem, g.part + tile * g.splits * (Cfg::TI * Cfg::TJ), g.count + tile,
+                            at.split, g.splits, acc))
+            return;
+    }
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // one 16 x 16 fragment per wave, transposed: rows of 16 fp16 in 40 bytes
+    uint16_t* turn = reinterpret_cast<uint16_t*>(smem) + wave * (16 * 20);
+    const bool mirror = kTri && at.ti != at.tj;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int x = 0; x < Cfg::FI; ++x) {
-            const int64_t i = i0 + tile_row<Cfg>(wave, p, x) + (lane & 15);
-            if (i >= I) continue;
+            const int64_t ib = i0 + tile_row<Cfg>(wave, p, x), i = ib + (lane & 15);
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int y = 0; y < Cfg::FJ; ++y) {
-                    const int64_t j = j0 + tile_col<Cfg>(wave, q, y) + 4 * (lane >> 4);
-                    if (j >= J) continue;
+                    const int64_t jb = j0 + tile_col<Cfg>(wave, q, y), j = jb + 4 * (lane >> 4);
+                    const bool in = i < I && j < J;
                     float v[4] = {acc[p][q][x][y][0], acc[p][q][x][y][1], acc[p][q][x][y][2],
                                   acc[p][q][x][y][3]};
-                    if constexpr (kProd == PROD_SYM) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if (i == j + r) {
-                                diag[i] = v[r] * (1.0f / (kScaleX * kScaleX));
-                                v[r] = 0.f;
-                            } else {
-                                v[r] *= kScaleSym / (kScaleX * kScaleX);
-                            }
-                        }
-                        store4_f16(g.sym + at_m + i * m + j, v);
-                    } else if constexpr (kProd == PROD_POLY) {
-                        float e[4];
-                        load4_f16(sym + i * m + j, e);
-                        const float di = diag[i];
-                        const float4 dj = *reinterpret_cast<const float4*>(diag + j);
-                        const float d[4] = {dj.x, dj.y, dj.z, dj.w};
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float sq = v[r] * (1.0f / (kScaleSym * kScaleSym));
-                            if (i == j + r) {
-                                scale[i] = kNsB * di + kNsC * (sq + di * di);
-                                v[r] = 0.f;
-                            } else {
-                                const float off = e[r] * (1.0f / kScaleSym);
-                                v[r] = kScaleSym * (kNsB * off + kNsC * (sq + (di + d[r]) * off));
-                            }
-                        }
-                        store4_f16(g.poly + at_m + i * m + j, v);
-                    } else {
-                        const int64_t at = at_x + i * g.C + j;
+                    if constexpr (kProd == PROD_X) {
+                        if (!in) continue;
+                        const int64_t at_e = at_x + i * g.C + j;
                         float h[4], l[4], s[4];
-                        load4_f16(g.hi + at, h);
-                        load4_f16(g.lo + at, l);
+                        load4_f16(g.hi + at_e, h);
+                        load4_f16(g.lo + at_e, l);
                         if constexpr (kTall) {
                             const float4 t = *reinterpret_cast<const float4*>(scale + j);
                             s[0] = t.x; s[1] = t.y; s[2] = t.z; s[3] = t.w;
@@ -232,11 +220,56 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
                         for (int r = 0; r < 4; ++r)
                             v[r] = kNsA * (h[r] + l[r]) + s[r] * h[r] + v[r] * (1.0f / kScaleSym);
                         if (g.last) {
-                            *reinterpret_cast<uint2*>(g.U + at) =
+                            *reinterpret_cast<uint2*>(g.U + at_e) =
                                 make_uint2(pack_bf16x2(v[0] * (1.0f / kScaleX), v[1] * (1.0f / kScaleX)),
                                            pack_bf16x2(v[2] * (1.0f / kScaleX), v[3] * (1.0f / kScaleX)));
                         } else {
-                            store4_pair(g.hi_next + at, g.lo + at, v);
+                            store4_pair(g.hi_next + at_e, g.lo + at_e, v);
+                        }
+                    } else {
+                        uint16_t* out = (kProd == PROD_SYM ? g.sym : g.poly) + at_m;
+                        if (in) {
+                            if constexpr (kProd == PROD_SYM) {
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    if (i == j + r) {
+                                        diag[i] = v[r] * (1.0f / (kScaleX * kScaleX));
+                                        v[r] = 0.f;
+                                    } else {
+                                        v[r] *= kScaleSym / (kScaleX * kScaleX);
+                                    }
+                                }
+                            } else {
+                                float e[4];
+                                load4_f16(sym + i * m + j, e);
+                                const float di = diag[i];
+                                const float4 dj = *reinterpret_cast<const float4*>(diag + j);
+                                const float d[4] = {dj.x, dj.y, dj.z, dj.w};
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    const float sq = v[r] * (1.0f / (kScaleSym * kScaleSym));
+                                    if (i == j + r) {
+                                        scale[i] = kNsB * di + kNsC * (sq + di * di);
+                                        v[r] = 0.f;
+                                    } else {
+                                        const float off = e[r] * (1.0f / kScaleSym);
+                                        v[r] = kScaleSym * (kNsB * off + kNsC * (sq + (di + d[r]) * off));
+                                    }
+                                }
+                            }
+                            store4_f16(out + i * m + j, v);
+                        }
+                        if (mirror) {   // the same for the whole workgroup
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                turn[(4 * (lane >> 4) + r) * 20 + (lane & 15)] = (uint16_t)bits_f16(v[r]);
+                            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                            // row jb + lane % 16 of the transpose, columns ib + 4 (lane / 16)
+                            const uint2 w = *reinterpret_cast<const uint2*>(
+                                turn + (lane & 15) * 20 + 4 * (lane >> 4));
+                            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                            const int64_t mi = jb + (lane & 15), mj = ib + 4 * (lane >> 4);
+                            if (mi < m && mj < m) *reinterpret_cast<uint2*>(out + mi * m + mj) = w;
                         }
                     }
                 }
@@ -250,22 +283,28 @@ hipError_t launch_product_cfg(const OrthoArgs& g, int64_t batch, hipStream_t str
     hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(kern), Cfg::kLds, lds_set);
     if (e != hipSuccess) return e;
     const int64_t I = kProd == PROD_X ? g.R : g.m, J = kProd == PROD_X ? g.C : g.m;
-    const int64_t grid = tile_grid((I + Cfg::TI - 1) / Cfg::TI, (J + Cfg::TJ - 1) / Cfg::TJ);
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid, (unsigned)batch), dim3(Cfg::kThreads), Cfg::kLds,
-                       stream, g);
+    const int64_t tiles = tile_count((I + Cfg::TI - 1) / Cfg::TI, (J + Cfg::TJ - 1) / Cfg::TJ,
+                                     kProd != PROD_X);
+    hipLaunchKernelGGL(kern, dim3((unsigned)tile_grid(tiles, g.splits), (unsigned)batch),
+                       dim3(Cfg::kThreads), Cfg::kLds, stream, g);
     return hipGetLastError();
 }
 
+template <int kProd>
+TilePlan product_plan(int64_t B, int64_t R, int64_t C) {
+    const int64_t m = R < C ? R : C, K = kProd == PROD_SYM ? (R < C ? C : R) : m;
+    return tile_plan(kProd == PROD_X ? R : m, kProd == PROD_X ? C : m, 1, (K + kTileK - 1) / kTileK,
+                     B, kProd != PROD_X);
+}
+
 template <int kProd, bool kTall>
-hipError_t launch_product(const OrthoArgs& g, int64_t batch, hipStream_t stream) {
-    const int64_t I = kProd == PROD_X ? g.R : g.m, J = kProd == PROD_X ? g.C : g.m;
-    const int64_t cus = device_cus();
-    const int64_t large = batch * ((I + Large::TI - 1) / Large::TI) * ((J + Large::TJ - 1) / Large::TJ);
-    const int64_t small = batch * ((I + Small::TI - 1) / Small::TI) * ((J + Small::TJ - 1) / Small::TJ);
-    const double t_large = (double)((large + cus - 1) / cus);
-    const double t_small = 0.65 * (double)((small + 2 * cus - 1) / (2 * cus));
-    if (t_large <= t_small) return launch_product_cfg<Large, kProd, kTall>(g, batch, stream);
-    return launch_product_cfg<Small, kProd, kTall>(g, batch, stream);
+hipError_t launch_product(OrthoArgs g, int64_t batch, hipStream_t stream) {
+    const TilePlan plan = product_plan<kProd>(batch, g.R, g.C);
+    g.splits = plan.splits;
+    if (plan.tile == TILE_LARGE) return launch_product_cfg<TileLarge, kProd, kTall>(g, batch, stream);
+    if constexpr (kProd == PROD_X)
+        if (plan.tile == TILE_MID) return launch_product_cfg<TileMid, kProd, kTall>(g, batch, stream);
+    return launch_product_cfg<TileSmall, kProd, kTall>(g, batch, stream);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -289,6 +328,16 @@ OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C) {
     L.diag = take(sizeof(float) * B * m);
     L.scale = take(sizeof(float) * B * m);
     L.norm = take(sizeof(double) * B * kNormBlocks);
+    const TilePlan plans[] = {product_plan<PROD_SYM>(B, R, C), product_plan<PROD_POLY>(B, R, C),
+                              product_plan<PROD_X>(B, R, C)};
+    int64_t part = 0;
+    L.counters = 0;
+    for (const TilePlan& p : plans) {
+        if (p.part_floats > part) part = p.part_floats;
+        if (p.counters > L.counters) L.counters = p.counters;
+    }
+    L.part = take(sizeof(float) * part);
+    L.count = take(sizeof(uint32_t) * L.counters);
     L.total = off;
     return L;
 }
@@ -305,6 +354,10 @@ hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B,
     g.diag = reinterpret_cast<float*>(ws + L.diag);
     g.scale = reinterpret_cast<float*>(ws + L.scale);
     g.norm = reinterpret_cast<double*>(ws + L.norm);
+    g.part = reinterpret_cast<float*>(ws + L.part);
+    g.count = reinterpret_cast<uint32_t*>(ws + L.count);
+    g.counters = L.counters;
+    g.splits = 1;
     g.R = R;
     g.C = C;
     g.m = R < C ? R : C;
