@@ -37,6 +37,7 @@ struct SwigluBackwardArgs {
     uint32_t* count;
     int64_t M, N, O, P;
     int splits;         // of this step
+    int64_t clear;      // counters that the first step sets to 0
 };
 
 // The steps above.  GATED's tile holds the gate's columns in its first half and
@@ -69,15 +70,23 @@ struct StepShape {
     }
 };
 
-__device__ __forceinline__ void store4_bf16(uint16_t* p, const float (&v)[4]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+__device__ __forceinline__ void load8_f32(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-template <bool kGradF32>
-__device__ __forceinline__ void store4_grad(void* p, int64_t at, const float (&v)[4]) {
-    if constexpr (kGradF32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-        store4_bf16(static_cast<uint16_t*>(p) + at, v);
+template <bool kF32>
+__device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8]) {
+    if constexpr (kF32) {
+        float* q = static_cast<float*>(p) + at;
+        *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+    }
 }
 
 template <class Cfg, int kStep, bool kGradF32>
@@ -87,11 +96,14 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
     const int64_t M = g.M, N = g.N, O = g.O, P = g.P;
     const int64_t I = S::rows(M, N, O), J = S::cols(N, O, P);
     constexpr int kWidth = S::template width<Cfg>();
+    if constexpr (kStep == STEP_DH)   // a later step's counters (this one has no splits then)
+        if (blockIdx.x == 0)
+            for (int64_t k = threadIdx.x; k < g.clear; k += Cfg::kThreads) g.count[k] = 0;
     TilePlace at;
-    if (!tile_place<false>(blockIdx.x, (I + Cfg::TI - 1) / Cfg::TI, (J + kWidth - 1) / kWidth,
-                           g.splits, &at))
+    if (!tile_place<false>(blockIdx.x, (uint32_t)((I + Cfg::TI - 1) / Cfg::TI),
+                           (uint32_t)((J + kWidth - 1) / kWidth), (uint32_t)g.splits, &at))
         return;
-    const int64_t i0 = at.ti * Cfg::TI, j0 = at.tj * kWidth;
+    const int64_t i0 = (int64_t)at.ti * Cfg::TI, j0 = (int64_t)at.tj * kWidth;
 
     TileOperand A, B;
     int64_t K;
@@ -118,64 +130,67 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
     constexpr int kPairs = kStep == STEP_DX ? 2 : 1;
     const int nt = S::depth(M, N, O, P), depth = (nt + g.splits - 1) / g.splits;
     const int t0 = at.split * depth, t1 = t0 + depth < nt ? t0 + depth : nt;
+    // the epilogue's share of this thread; every column count is a multiple of 8: its
+    // eight columns are all in or all out
+    constexpr int kCols = kStep == STEP_GATED ? Cfg::HJ : Cfg::TJ;
+    const PartThread<Cfg, kCols> t;
+    const int64_t j = j0 + 8 * t.c;
+    const int rows = j >= J ? 0 : (int)(I - i0 < Cfg::TI ? I - i0 : Cfg::TI);
+    struct None {};
+    struct Dh { float v[8]; };
+    PartStates<Cfg, kCols, std::conditional_t<kStep == STEP_GATED, Dh, None>> states;
+    auto before = [&](int row, auto& d) {
+        if constexpr (kStep == STEP_GATED) load8_f32(g.dH + (i0 + row) * O + j, d.v);
+    };
+    if (g.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
+
     TileAcc<Cfg> acc;
     tile_clear<Cfg>(acc);
     tile_product<Cfg, S::kAS, S::kBS, false, kPairs>(smem, A, B, K, a2, b2, b_half2, t0, t1, acc);
-    if (g.splits > 1 &&
-        !tile_join<Cfg>(smem, g.part + at.tile * g.splits * (Cfg::TI * Cfg::TJ), g.count + at.tile,
-                        at.split, g.splits, acc))
-        return;
+    if (g.splits > 1) {
+        if (!tile_join<Cfg>(smem, g.part + (int64_t)at.tile * g.splits * (Cfg::TI * Cfg::TJ),
+                            g.count + at.tile, at.split, g.splits,
+                            (int)(I - i0 < Cfg::TI ? I - i0 : Cfg::TI), acc))
+            return;
+        states.load(t, rows, before);
+    }
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t place = t.place(2 * t.c), place_up = t.place(Cfg::HJ / 4 + 2 * t.c);
+    // the output of the other steps, its leading dimension, this thread's first column
+    constexpr bool kF32 = kStep == STEP_DH || ((kStep == STEP_DGU || kStep == STEP_DD) && kGradF32);
+    void* out = kStep == STEP_DH ? (void*)g.dH : kStep == STEP_DX ? (void*)g.dX
+                : kStep == STEP_DD ? g.dWd : j < O ? g.dWg : g.dWu;
+    const int64_t ld = kStep == STEP_DX ? N : kStep == STEP_DD ? P : O;
+    const int64_t jo = kStep == STEP_DGU && j >= O ? j - O : j;
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int x = 0; x < Cfg::FI; ++x) {
-            const int64_t i = i0 + tile_row<Cfg>(wave, p, x) + (lane & 15);
-            if (i >= I) continue;
-            // every column count is a multiple of 8: a lane's four are all in or all out
+    for (int p = 0; p < PartOf<Cfg>::kParts; ++p) {
+        part_put<Cfg>(smem, acc, p);
+        __syncthreads();
+        states.each(t, p, rows, before, [&](int k, int row, const auto& d) {
+            const int64_t i = i0 + row;
             if constexpr (kStep == STEP_GATED) {
+                float a[8], b[8], h[8], da[8], db[8];
+                t.get(smem, place, k, a);
+                t.get(smem, place_up, k, b);
 #pragma unroll
-                for (int y = 0; y < Cfg::FJ; ++y) {
-                    const int64_t j = j0 + tile_col<Cfg>(wave, 0, y) + 4 * (lane >> 4);
-                    if (j >= J) continue;
-                    const float4 d = *reinterpret_cast<const float4*>(g.dH + i * O + j);
-                    const float dh[4] = {d.x, d.y, d.z, d.w};
-                    float h[4], da[4], db[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float a = acc[p][0][x][y][r], b = acc[p][1][x][y][r];
-                        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-a));
-                        const float t = a * s;
-                        h[r] = t * b;
-                        da[r] = dh[r] * b * (s + t * (1.0f - s));
-                        db[r] = dh[r] * t;
-                    }
-                    store4_bf16(g.H + i * O + j, h);
-                    store4_bf16(g.dAB + i * 2 * O + j, da);
-                    store4_bf16(g.dAB + i * 2 * O + O + j, db);
+                for (int r = 0; r < 8; ++r) {
+                    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-a[r]));
+                    const float u = a[r] * s;
+                    h[r] = u * b[r];
+                    da[r] = d.v[r] * b[r] * (s + u * (1.0f - s));
+                    db[r] = d.v[r] * u;
                 }
+                store8<false>(g.H, i * O + j, h);
+                store8<false>(g.dAB, i * 2 * O + j, da);
+                store8<false>(g.dAB, i * 2 * O + O + j, db);
             } else {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int y = 0; y < Cfg::FJ; ++y) {
-                        const int64_t j = j0 + tile_col<Cfg>(wave, q, y) + 4 * (lane >> 4);
-                        if (j >= J) continue;
-                        const float v[4] = {acc[p][q][x][y][0], acc[p][q][x][y][1],
-                                            acc[p][q][x][y][2], acc[p][q][x][y][3]};
-                        if constexpr (kStep == STEP_DH)
-                            *reinterpret_cast<float4*>(g.dH + i * O + j) =
-                                make_float4(v[0], v[1], v[2], v[3]);
-                        else if constexpr (kStep == STEP_DX)
-                            store4_bf16(g.dX + i * N + j, v);
-                        else if constexpr (kStep == STEP_DGU)
-                            store4_grad<kGradF32>(j < O ? g.dWg : g.dWu, i * O + (j < O ? j : j - O), v);
-                        else
-                            store4_grad<kGradF32>(g.dWd, i * P + j, v);
-                    }
+                float v[8];
+                t.get(smem, place, k, v);
+                store8<kF32>(out, i * ld + jo, v);
             }
-        }
+        });
+        if (p + 1 < PartOf<Cfg>::kParts) __syncthreads();
+    }
 }
 
 template <class Cfg, int kStep, bool kGradF32>
@@ -204,9 +219,14 @@ hipError_t launch_step(SwigluBackwardArgs g, hipStream_t stream) {
 
 template <bool kGradF32>
 hipError_t launch_all(const SwigluBackwardArgs& g, int64_t counters, hipStream_t stream) {
-    hipError_t e = launch_zero_f32(reinterpret_cast<float*>(g.count), counters, stream);
-    if (e != hipSuccess) return e;
-    if ((e = launch_step<STEP_DH, false>(g, stream)) != hipSuccess) return e;
+    hipError_t e;
+    SwigluBackwardArgs first = g;
+    if (StepShape<STEP_DH>::plan(g.M, g.N, g.O, g.P).splits == 1) {
+        first.clear = counters;
+    } else if ((e = launch_zero_f32(reinterpret_cast<float*>(g.count), counters, stream)) != hipSuccess) {
+        return e;
+    }
+    if ((e = launch_step<STEP_DH, false>(first, stream)) != hipSuccess) return e;
     if ((e = launch_step<STEP_GATED, false>(g, stream)) != hipSuccess) return e;
     if ((e = launch_step<STEP_DX, false>(g, stream)) != hipSuccess) return e;
     if ((e = launch_step<STEP_DGU, kGradF32>(g, stream)) != hipSuccess) return e;
@@ -269,6 +289,7 @@ hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream
     g.O = io.O;
     g.P = io.P;
     g.splits = 1;
+    g.clear = 0;
     return io.grad_f32 ? launch_all<true>(g, L.counters, stream) : launch_all<false>(g, L.counters, stream);
 }
 

@@ -40,6 +40,8 @@
 // zeros or other rows and only reach outputs that are not stored.
 #pragma once
 
+#include <type_traits>
+
 #include "ffn_device.h"
 
 namespace ffn {
@@ -322,17 +324,142 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A, c
     tile_barrier();
 }
 
-// First output row (of 16) of A half p's fragment x, and first column of B half
-// q's fragment y, within the tile; lane l holds row + l % 16 and the four
-// columns from column + 4 (l / 16).
+// The way out: the sums go through LDS, the whole tile where it fits and else its
+// two halves of Cfg::HI rows after each other, so that a thread gets eight
+// consecutive columns of a row (16 bytes of bf16 or fp16, whole lines per wave) and
+// the epilogue is a short loop.  (Straight from the accumulators every fragment's
+// epilogue is code of its own, and the stores are half lines: the outer product of
+// a 4096 x 1792 update 40 -> 32 us.)  The 16-byte chunk c of row r lies at chunk
+// c ^ ((r ^ r / 8) mod 16): writes (16 rows, one column), reads along a row and
+// reads along a column meet 16 different chunks.
 template <class Cfg>
-__device__ __forceinline__ int tile_row(int wave, int p, int x) {
-    return p * Cfg::HI + 16 * (Cfg::FI * (wave / Cfg::WJ) + x);
+struct PartOf {
+    static constexpr int kParts = Cfg::TI * Cfg::TJ * 4 <= Cfg::kLds ? 1 : 2;
+    static constexpr int kRows = Cfg::TI / kParts;
+    static_assert(kRows * Cfg::TJ * 4 <= Cfg::kLds, "a part fits the LDS");
+};
+template <class Cfg>
+__device__ __forceinline__ uint32_t part_off(int row, int chunk) {
+    return (uint32_t)row * (Cfg::TJ * 4) + 16u * (uint32_t)(chunk ^ ((row ^ (row >> 3)) & 15));
 }
 template <class Cfg>
-__device__ __forceinline__ int tile_col(int wave, int q, int y) {
-    return q * Cfg::HJ + 16 * (Cfg::FJ * (wave % Cfg::WJ) + y);
+__device__ __forceinline__ void part_put(char* smem, const TileAcc<Cfg>& acc, int part) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wi = wave / Cfg::WJ, wj = wave % Cfg::WJ;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        if (PartOf<Cfg>::kParts == 2 && p != part) continue;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int x = 0; x < Cfg::FI; ++x)
+#pragma unroll
+                for (int y = 0; y < Cfg::FJ; ++y)
+                    *reinterpret_cast<floatx4_t*>(
+                        smem + part_off<Cfg>((PartOf<Cfg>::kParts == 2 ? 0 : p * Cfg::HI) +
+                                                 16 * (Cfg::FI * wi + x) + (lane & 15),
+                                             (q * Cfg::HJ + 16 * (Cfg::FJ * wj + y)) / 4 + (lane >> 4))) =
+                        acc[p][q][x][y];
+    }
 }
+// A thread's share of a part with kCols columns: the 8-column group `c` of every
+// kStep-th row from `row0`, kUnits rows.  kStep is 16, 32 or 64 and row0 below it, so in
+// a row k steps on, the swizzle differs from row0's by an exclusive-or with a
+// constant: one instruction per LDS access.
+template <class Cfg, int kCols>
+struct PartThread {
+    static constexpr int kStep = Cfg::kThreads / (kCols / 8);
+    static constexpr int kUnits = PartOf<Cfg>::kRows / kStep;
+    static_assert(kStep >= 16 && (kStep & (kStep - 1)) == 0 && kUnits * kStep == PartOf<Cfg>::kRows, "whole rows");
+    int c, row0;
+    __device__ __forceinline__ PartThread() {
+        c = threadIdx.x % (kCols / 8);
+        row0 = threadIdx.x / (kCols / 8);
+    }
+    // place of chunk `chunk` of row row0, to be stepped by `at`
+    __device__ __forceinline__ uint32_t place(int chunk) const {
+        return 16u * (uint32_t)(chunk ^ ((row0 ^ (row0 >> 3)) & 15));
+    }
+    __device__ __forceinline__ uint32_t at(uint32_t place, int k) const {
+        return (uint32_t)(row0 + k * kStep) * (Cfg::TJ * 4) + (place ^ (16u * ((kStep / 8 * k) & 15)));
+    }
+    // eight columns of row row0 + k kStep, from the group whose first chunk is at `place`
+    __device__ __forceinline__ void get(const char* smem, uint32_t place, int k, float (&v)[8]) const {
+        const floatx4_t a = *reinterpret_cast<const floatx4_t*>(smem + at(place, k));
+        const floatx4_t b = *reinterpret_cast<const floatx4_t*>(smem + at(place ^ 16u, k));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            v[r] = a[r];
+            v[4 + r] = b[r];
+        }
+    }
+    __device__ __forceinline__ void set(char* smem, uint32_t place, int k, const float (&v)[8]) const {
+        *reinterpret_cast<floatx4_t*>(smem + at(place, k)) = floatx4_t{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<floatx4_t*>(smem + at(place ^ 16u, k)) = floatx4_t{v[4], v[5], v[6], v[7]};
+    }
+};
+// Eight rows from row 8 r of a column.
+template <class Cfg>
+__device__ __forceinline__ void part_get_column(const char* smem, int r, int col, float (&v)[8]) {
+    const uint32_t base = (uint32_t)r * (8 * Cfg::TJ * 4) + 4u * (col & 3);
+    const uint32_t x = 16u * (uint32_t)((col >> 2) ^ ((8 * (r & 1) ^ r) & 15));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = *reinterpret_cast<const float*>(smem + base + k * (Cfg::TJ * 4) + (x ^ (16u * k)));
+}
+
+// What the epilogue reads per row of a thread, for every row of the tile.  The small
+// and mid tiles have registers left to load it before the products (kEarly: its
+// latency, 1 to 2 us, is hidden); the large tile loads four rows at a time after them.
+template <class Cfg, int kCols, class State>
+struct PartStates {
+    static constexpr bool kEarly = Cfg::FI * Cfg::FJ <= 4 && !std::is_empty<State>::value;
+    static constexpr int kUnits = PartThread<Cfg, kCols>::kUnits;
+    State early[kEarly ? PartOf<Cfg>::kParts : 1][kEarly ? kUnits : 1];
+
+    // before(row of the tile, state)
+    template <class Before>
+    __device__ __forceinline__ void load(const PartThread<Cfg, kCols>& t, int rows, Before&& before) {
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int p = 0; p < PartOf<Cfg>::kParts; ++p)
+#pragma unroll
+                for (int k = 0; k < kUnits; ++k) {
+                    const int row = p * PartOf<Cfg>::kRows + t.row0 + k * t.kStep;
+                    if (row < rows) before(row, early[p][k]);
+                }
+        }
+    }
+    // after(k, row of the tile, state) for every row of part p below `rows`
+    template <class Before, class After>
+    __device__ __forceinline__ void each(const PartThread<Cfg, kCols>& t, int p, int rows,
+                                         Before&& before, After&& after) {
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                const int row = p * PartOf<Cfg>::kRows + t.row0 + k * t.kStep;
+                if (row < rows) after(k, row, early[p][k]);
+            }
+        } else {
+            constexpr int kGroup = kUnits < 4 ? kUnits : 4;
+            static_assert(kUnits % kGroup == 0, "whole groups");
+#pragma unroll 1
+            for (int u = 0; u < kUnits; u += kGroup) {
+                State st[kGroup];
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    const int row = p * PartOf<Cfg>::kRows + t.row0 + (u + k) * t.kStep;
+                    if (row < rows) before(row, st[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    const int row = p * PartOf<Cfg>::kRows + t.row0 + (u + k) * t.kStep;
+                    if (row < rows) after(u + k, row, st[k]);
+                }
+            }
+        }
+    }
+};
 
 template <class Cfg>
 __device__ __forceinline__ void tile_clear(TileAcc<Cfg>& acc) {
@@ -352,8 +479,7 @@ __device__ __forceinline__ void tile_clear(TileAcc<Cfg>& acc) {
 // of a grouped order (groups of 8 tile rows, rows fastest; a tile's splits side by
 // side), a compact rectangle whose panels its L2 shares.
 struct TilePlace {
-    int64_t ti, tj, tile;   // tile: the tile's number
-    int split;
+    int ti, tj, tile, split;   // tile: the tile's number
 };
 __host__ __device__ __forceinline__ int64_t tile_count(int64_t nI, int64_t nJ, bool tri) {
     return tri ? nI * (nI + 1) / 2 : nI * nJ;
@@ -361,29 +487,31 @@ __host__ __device__ __forceinline__ int64_t tile_count(int64_t nI, int64_t nJ, b
 __host__ __device__ __forceinline__ int64_t tile_grid(int64_t tiles, int splits) {
     return 8 * ((tiles * splits + 7) / 8);
 }
-// Returns false for the padding workgroups.
+// Returns false for the padding workgroups.  (32-bit arithmetic: six 64-bit
+// divisions took 0.5 us of every launch.)
 template <bool kTri>
-__device__ __forceinline__ bool tile_place(int64_t w, int64_t nI, int64_t nJ, int splits,
+__device__ __forceinline__ bool tile_place(uint32_t w, uint32_t nI, uint32_t nJ, uint32_t splits,
                                            TilePlace* at) {
-    constexpr int64_t G = 8;
-    const int64_t n = tile_count(nI, nJ, kTri) * splits, per = (n + 7) / 8;
-    const int64_t u = (w & 7) * per + (w >> 3);
+    constexpr uint32_t G = 8;
+    const uint32_t n = (kTri ? nI * (nI + 1) / 2 : nI * nJ) * splits, per = (n + 7) / 8;
+    const uint32_t u = (w & 7) * per + (w >> 3);
     if (u >= n || (w >> 3) >= per) return false;
-    const int64_t t = u / splits;
-    at->tile = t;
-    at->split = (int)(u % splits);
+    const uint32_t t = splits == 1 ? u : u / splits;
+    at->tile = (int)t;
+    at->split = (int)(u - t * splits);
     if constexpr (kTri) {
-        int64_t r = (int64_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-        while (r * (r + 1) / 2 > t) --r;
-        while ((r + 1) * (r + 2) / 2 <= t) ++r;
-        at->ti = r;
-        at->tj = t - r * (r + 1) / 2;
+        uint32_t r = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+        if (r * (r + 1) / 2 > t) --r;   // the root is off by one at most
+        if ((r + 1) * (r + 2) / 2 <= t) ++r;
+        at->ti = (int)r;
+        at->tj = (int)(t - r * (r + 1) / 2);
     } else {
-        const int64_t r = t / (G * nJ);
-        const int64_t rows = nI - r * G < G ? nI - r * G : G;
-        const int64_t rem = t - r * G * nJ;
-        at->tj = rem / rows;
-        at->ti = r * G + rem % rows;
+        const uint32_t r = t / (G * nJ);
+        const uint32_t rows = nI - r * G < G ? nI - r * G : G;
+        const uint32_t rem = t - r * G * nJ;
+        const uint32_t tj = rem / rows;
+        at->tj = (int)tj;
+        at->ti = (int)(r * G + rem - tj * rows);
     }
     return true;
 }
@@ -400,23 +528,37 @@ __device__ __forceinline__ bool tile_place(int64_t w, int64_t nI, int64_t nJ, in
 // fence would write back the XCD's whole L2 instead.
 //
 // part: splits x (TI * TJ) floats of this tile; count: the tile's counter, 0 before
-// the first and again after the last split.  Returns whether to go on, with acc the
-// sum.  smem is used for one word.
+// the first and again after the last split; rows: the tile's rows that are wanted
+// (fragments past them are left out).  Returns whether to go on, with acc the sum.
+// smem is used for one word.
 constexpr int kCpolThrough = 17;   // buffer cache-policy bits sc0, sc1: system scope
 
 template <class Cfg>
 __device__ __forceinline__ bool tile_join(char* smem, float* part, uint32_t* count, int split,
-                                          int splits, TileAcc<Cfg>& acc) {
-    constexpr int kFrags = 4 * Cfg::FI * Cfg::FJ;
+                                          int splits, int rows, TileAcc<Cfg>& acc) {
     constexpr uint32_t kBytes = (uint32_t)Cfg::TI * Cfg::TJ * 4;
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(part, (int64_t)kBytes * splits);
-    const uint32_t lane_off = threadIdx.x * 16u;
-    floatx4_t* v = &acc[0][0][0][0];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = wave / Cfg::WJ;
+    auto wanted = [&](int p, int x) { return p * Cfg::HI + 16 * (Cfg::FI * wi + x) < rows; };
+    auto off = [&](int p, int x, int k) {   // k: fragment (q, y) of the block row
+        return (uint32_t)(((p * Cfg::FI + x) * 2 * Cfg::FJ + k) * (Cfg::kThreads * 16)) + threadIdx.x * 16u;
+    };
+    // The split's place is added to the lane's offset, not given as the instruction's scalar
+    // offset: with that, the compiler lets the next instruction overwrite the first of a
+    // 16-byte store's registers, and now and then the overwritten word is what arrives.
+    const uint32_t mine = kBytes * (uint32_t)split;
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f)
-        __builtin_amdgcn_raw_buffer_store_b128(
-            __builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned int, v[f]), rs,
-            lane_off + f * (Cfg::kThreads * 16), (int)(kBytes * (uint32_t)split), kCpolThrough);
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int x = 0; x < Cfg::FI; ++x) {
+            if (!wanted(p, x)) continue;
+#pragma unroll
+            for (int k = 0; k < 2 * Cfg::FJ; ++k)
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    __builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned int,
+                                       acc[p][k / Cfg::FJ][x][k % Cfg::FJ]),
+                    rs, mine + off(p, x, k), 0, kCpolThrough);
+        }
     wait_vmcnt<0>();
     __syncthreads();
     uint32_t* last = reinterpret_cast<uint32_t*>(smem);
@@ -429,15 +571,34 @@ __device__ __forceinline__ bool tile_join(char* smem, float* part, uint32_t* cou
     const bool go = *last != 0;
     __syncthreads();   // the word is free again
     if (!go) return false;
+    tile_clear<Cfg>(acc);
+    // ascending split order; each turn's loads are in flight together
+    constexpr int kHalves = Cfg::FI * Cfg::FJ <= 4 ? 2 : 1;   // of the tile at once: registers
+    constexpr int kRow = 2 * Cfg::FJ;
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f) v[f] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s) {
+    for (int p0 = 0; p0 < 2; p0 += kHalves)
+#pragma unroll 1
+        for (int s = 0; s < splits; ++s) {
+            floatx4_t v[kHalves][Cfg::FI][kRow];
 #pragma unroll
-        for (int f = 0; f < kFrags; ++f)
-            v[f] += __builtin_bit_cast(floatx4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                      rs, lane_off + f * (Cfg::kThreads * 16),
-                                                      (int)(kBytes * (uint32_t)s), kCpolThrough));
-    }
+            for (int p = 0; p < kHalves; ++p)
+#pragma unroll
+                for (int x = 0; x < Cfg::FI; ++x)
+                    if (wanted(p0 + p, x))
+#pragma unroll
+                        for (int k = 0; k < kRow; ++k)
+                            v[p][x][k] = __builtin_bit_cast(
+                                floatx4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                               rs, off(p0 + p, x, k), (int)(kBytes * (uint32_t)s), kCpolThrough));
+#pragma unroll
+            for (int p = 0; p < kHalves; ++p)
+#pragma unroll
+                for (int x = 0; x < Cfg::FI; ++x)
+                    if (wanted(p0 + p, x))
+#pragma unroll
+                        for (int k = 0; k < kRow; ++k)
+                            acc[p0 + p][k / Cfg::FJ][x][k % Cfg::FJ] += v[p][x][k];
+        }
     return true;
 }
 
@@ -455,28 +616,36 @@ struct TilePlan {
 
 // The plan with the least estimated time, in microseconds, for an I x J output (J
 // in the tile's terms: `share` operand columns of a tile belong to one output
-// column) of `nt` k-tiles, `batch` times.  Measured per k-tile with every CU at
-// work: 1.42 (large), 0.88 (mid), 0.95 (small, two per CU; 0.62 alone); a join
-// moves a tile's sums `splits` times through one CU at about 0.1 MB/us and costs
-// 2 us of latency.  Splits beyond one round of the CUs would only add work.
+// column) of `nt` k-tiles, `batch` times.  Measured on 256 CUs, k-contiguous bf16,
+// per k-tile with few and with all CUs at work: large 0.95 to 1.4, mid 0.54 to
+// 0.87, small 0.43 to 0.55 alone on a CU and 0.6 to 0.95 two on one; beside them a
+// launch takes about 4.5.  A join costs (large) 5.5 + 2.7 a split, (mid) 3 + 1.35,
+// (small) 2 + 1 -- the last workgroup reads every split's sums alone, at about 0.1
+// MB/us -- and 0.2 per MB that all tiles' splits write, less where few of a tile's
+// rows are wanted.  Splits beyond one round of the CUs would only add work.
 inline TilePlan tile_plan(int64_t I, int64_t J, int share, int64_t nt, int64_t batch, bool tri) {
-    struct Kind { int ti, tj, slots; double per, bytes; };
-    const Kind kinds[3] = {{256, 256, 256, 1.42, 262144.0}, {256, 128, 256, 0.88, 131072.0},
-                           {128, 128, 512, 0.95, 65536.0}};
+    struct Kind { int ti, tj, slots; double join, join_split; };
+    const Kind kinds[3] = {{256, 256, 256, 5.5, 2.7}, {256, 128, 256, 3.0, 1.35}, {128, 128, 512, 2.0, 1.0}};
     TilePlan best{TILE_LARGE, 1, 0, 0};
     double best_t = 1e30;
     for (int k = 0; k < 3; ++k) {
         if (tri && kinds[k].ti != kinds[k].tj) continue;
         const int64_t wj = kinds[k].tj / share;
         const int64_t tiles = batch * tile_count((I + kinds[k].ti - 1) / kinds[k].ti, (J + wj - 1) / wj, tri);
+        const double rows = I < kinds[k].ti ? (double)((I + 15) / 16 * 16) / kinds[k].ti : 1.0;
         for (int64_t s = 1; s <= 16 && s <= nt; ++s) {
             if (s > 1 && tiles * s > kinds[k].slots) break;
             const int64_t depth = (nt + s - 1) / s;
             if ((nt + depth - 1) / depth != s) continue;   // an empty last split
-            const int64_t units = tiles * s;
-            const double per = k == TILE_SMALL && units <= 256 ? 0.62 : kinds[k].per;
-            double t = (double)((units + kinds[k].slots - 1) / kinds[k].slots) * (double)depth * per;
-            if (s > 1) t += 2.0 + (double)s * kinds[k].bytes * 1e-5;
+            const int64_t units = tiles * s, rounds = (units + kinds[k].slots - 1) / kinds[k].slots;
+            const double busy = units < kinds[k].slots ? (double)units / kinds[k].slots : 1.0;
+            const double per = k == TILE_LARGE ? 0.95 + 0.45 * busy
+                               : k == TILE_MID ? 0.54 + 0.33 * busy
+                               : busy <= 0.5   ? 0.43 + 0.24 * busy
+                                               : 0.6 + 0.35 * busy;
+            const double mb = (double)units * kinds[k].ti * kinds[k].tj * 4e-6;
+            double t = 4.5 + (double)(rounds * depth) * per;
+            if (s > 1) t += kinds[k].join + rows * ((double)s * kinds[k].join_split + 0.2 * mb);
             if (t < best_t) {
                 best_t = t;
                 best.tile = k;

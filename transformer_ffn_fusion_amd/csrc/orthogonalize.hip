@@ -65,32 +65,42 @@ __device__ __forceinline__ float f16_bits(uint32_t v) {
 __device__ __forceinline__ uint32_t bits_f16(float v) {
     return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
-__device__ __forceinline__ void load4_f16(const uint16_t* p, float (&v)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    v[0] = f16_bits(w.x & 0xffffu); v[1] = f16_bits(w.x >> 16);
-    v[2] = f16_bits(w.y & 0xffffu); v[3] = f16_bits(w.y >> 16);
+__device__ __forceinline__ void unpack8_f16(const uint4& w, float (&v)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        v[2 * r] = f16_bits(u[r] & 0xffffu);
+        v[2 * r + 1] = f16_bits(u[r] >> 16);
+    }
 }
-__device__ __forceinline__ void store4_f16(uint16_t* p, const float (&v)[4]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(bits_f16(v[0]) | bits_f16(v[1]) << 16,
-                                              bits_f16(v[2]) | bits_f16(v[3]) << 16);
+__device__ __forceinline__ void store8_f16(uint16_t* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(bits_f16(v[0]) | bits_f16(v[1]) << 16, bits_f16(v[2]) | bits_f16(v[3]) << 16,
+                   bits_f16(v[4]) | bits_f16(v[5]) << 16, bits_f16(v[6]) | bits_f16(v[7]) << 16);
 }
 // v as hi + lo
-__device__ __forceinline__ void store4_pair(uint16_t* hi, uint16_t* lo, const float (&v)[4]) {
-    float l[4];
+__device__ __forceinline__ void store8_pair(uint16_t* hi, uint16_t* lo, const float (&v)[8]) {
+    float l[8];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) l[r] = v[r] - (float)(_Float16)v[r];
-    store4_f16(hi, v);
-    store4_f16(lo, l);
+    for (int r = 0; r < 8; ++r) l[r] = v[r] - (float)(_Float16)v[r];
+    store8_f16(hi, v);
+    store8_f16(lo, l);
+}
+__device__ __forceinline__ void load8_f32(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 template <bool kF32>
-__device__ __forceinline__ void load4_in(const void* p, int64_t at, float (&v)[4]) {
+__device__ __forceinline__ void load8_in(const void* p, int64_t at, float (&v)[8]) {
     if constexpr (kF32) {
-        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        load8_f32(static_cast<const float*>(p) + at, v);
     } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+        const uint4 w = ld16(static_cast<const uint16_t*>(p) + at);
         v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+        v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
     }
 }
 
@@ -102,11 +112,11 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs g) {
     if (blockIdx.x == 0 && blockIdx.y == 0)   // before any product of this call
         for (int64_t k = threadIdx.x; k < g.counters; k += 256) g.count[k] = 0;
     double q = 0.0;
-    for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; k < size; k += kNormBlocks * 1024) {
-        float v[4];
-        load4_in<kF32>(g.G, base + k, v);
+    for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; k < size; k += kNormBlocks * 2048) {
+        float v[8];
+        load8_in<kF32>(g.G, base + k, v);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) q += (double)v[r] * v[r];
+        for (int r = 0; r < 8; ++r) q += (double)v[r] * v[r];
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) q += __shfl_xor(q, d);
@@ -125,13 +135,13 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoArgs g) {
     for (int k = 0; k < kNormBlocks; ++k) q += s[k];
     const double by = (double)kScaleX / (sqrt(q) + kNsEps);
     const int64_t size = g.R * g.C, base = (int64_t)blockIdx.y * size;
-    for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; k < size;
-         k += (int64_t)gridDim.x * 1024) {
-        float v[4];
-        load4_in<kF32>(g.G, base + k, v);
+    for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; k < size;
+         k += (int64_t)gridDim.x * 2048) {
+        float v[8];
+        load8_in<kF32>(g.G, base + k, v);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = (float)((double)v[r] * by);
-        store4_pair(g.hi_next + base + k, g.lo + base + k, v);
+        for (int r = 0; r < 8; ++r) v[r] = (float)((double)v[r] * by);
+        store8_pair(g.hi_next + base + k, g.lo + base + k, v);
     }
 }
 
@@ -147,10 +157,10 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     constexpr bool kTri = kProd != PROD_X;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int64_t m = g.m, I = kProd == PROD_X ? g.R : m, J = kProd == PROD_X ? g.C : m;
-    const int64_t nI = (I + Cfg::TI - 1) / Cfg::TI, nJ = (J + Cfg::TJ - 1) / Cfg::TJ;
+    const uint32_t nI = (uint32_t)((I + Cfg::TI - 1) / Cfg::TI), nJ = (uint32_t)((J + Cfg::TJ - 1) / Cfg::TJ);
     TilePlace at;
-    if (!tile_place<kTri>(blockIdx.x, nI, nJ, g.splits, &at)) return;
-    const int64_t i0 = at.ti * Cfg::TI, j0 = at.tj * Cfg::TJ;
+    if (!tile_place<kTri>(blockIdx.x, nI, nJ, (uint32_t)g.splits, &at)) return;
+    const int64_t i0 = (int64_t)at.ti * Cfg::TI, j0 = (int64_t)at.tj * Cfg::TJ;
     const int64_t at_x = (int64_t)blockIdx.y * g.R * g.C, at_m = (int64_t)blockIdx.y * m * m;
     const uint16_t* hi = g.hi + at_x;
     const uint16_t* poly = g.poly + at_m;
@@ -177,103 +187,123 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     B.at[1] = j0 + Cfg::HJ;
     const int nt = (int)((K + kTileK - 1) / kTileK), depth = (nt + g.splits - 1) / g.splits;
     const int t0 = at.split * depth, t1 = t0 + depth < nt ? t0 + depth : nt;
+    const bool mirror = kTri && at.ti != at.tj;
+
+    // the epilogue's share of this thread, and what it reads
+    const PartThread<Cfg, Cfg::TJ> t;
+    const int64_t j = j0 + 8 * t.c;
+    const int rows = j >= J ? 0 : (int)(I - i0 < Cfg::TI ? I - i0 : Cfg::TI);
+    struct None {};
+    struct OfPoly { uint4 e; float d; };       // E, D_i
+    struct OfX { uint4 hi, lo; float s; };     // X, scale_i
+    using State = std::conditional_t<kProd == PROD_SYM, None,
+                                     std::conditional_t<kProd == PROD_POLY, OfPoly, OfX>>;
+    PartStates<Cfg, Cfg::TJ, State> states;
+    auto before = [&](int row, State& e) {
+        const int64_t i = i0 + row;
+        if constexpr (kProd == PROD_POLY) {
+            e.e = ld16(sym + i * m + j);
+            e.d = diag[i];
+        }
+        if constexpr (kProd == PROD_X) {
+            e.hi = ld16(hi + i * g.C + j);
+            e.lo = ld16(g.lo + at_x + i * g.C + j);
+            if constexpr (!kTall) e.s = scale[i];
+        }
+    };
+    if (g.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
+    // the column's factors: POLY b + c D_j, X from the right a + scale_j
+    float fj[8];
+    if constexpr (kProd == PROD_POLY || (kProd == PROD_X && kTall)) {
+        if (rows) load8_f32((kProd == PROD_POLY ? diag : scale) + j, fj);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) fj[r] = kProd == PROD_POLY ? kNsB + kNsC * fj[r] : kNsA + fj[r];
+    }
+
     TileAcc<Cfg> acc;
     tile_clear<Cfg>(acc);
     tile_product<Cfg, kAS, kBS, true, 1>(smem, A, B, K, nullptr, nullptr, nullptr, t0, t1, acc);
     if (g.splits > 1) {
         const int64_t tile = (int64_t)blockIdx.y * tile_count(nI, nJ, kTri) + at.tile;
         if (!tile_join<Cfg>(smem, g.part + tile * g.splits * (Cfg::TI * Cfg::TJ), g.count + tile,
-                            at.split, g.splits, acc))
+                            at.split, g.splits, (int)(I - i0 < Cfg::TI ? I - i0 : Cfg::TI), acc))
             return;
+        states.load(t, rows, before);
     }
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // one 16 x 16 fragment per wave, transposed: rows of 16 fp16 in 40 bytes
-    uint16_t* turn = reinterpret_cast<uint16_t*>(smem) + wave * (16 * 20);
-    const bool mirror = kTri && at.ti != at.tj;
+    uint16_t* out = (kProd == PROD_SYM ? g.sym : g.poly) + at_m;
+    const uint32_t place = t.place(2 * t.c);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < PartOf<Cfg>::kParts; ++p) {
+        part_put<Cfg>(smem, acc, p);
+        __syncthreads();
+        states.each(t, p, rows, before, [&](int k, int row, const State& e) {
+            const int64_t i = i0 + row;
+            float v[8];
+            t.get(smem, place, k, v);
+            if constexpr (kProd == PROD_X) {
+                float h[8], l[8];
+                unpack8_f16(e.hi, h);
+                unpack8_f16(e.lo, l);
 #pragma unroll
-        for (int x = 0; x < Cfg::FI; ++x) {
-            const int64_t ib = i0 + tile_row<Cfg>(wave, p, x), i = ib + (lane & 15);
+                for (int r = 0; r < 8; ++r)   // a (hi + lo) + scale hi + product
+                    v[r] = v[r] * (1.0f / kScaleSym) + (kTall ? fj[r] : kNsA + e.s) * h[r] + kNsA * l[r];
+                const int64_t at_e = at_x + i * g.C + j;
+                if (g.last) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int y = 0; y < Cfg::FJ; ++y) {
-                    const int64_t jb = j0 + tile_col<Cfg>(wave, q, y), j = jb + 4 * (lane >> 4);
-                    const bool in = i < I && j < J;
-                    float v[4] = {acc[p][q][x][y][0], acc[p][q][x][y][1], acc[p][q][x][y][2],
-                                  acc[p][q][x][y][3]};
-                    if constexpr (kProd == PROD_X) {
-                        if (!in) continue;
-                        const int64_t at_e = at_x + i * g.C + j;
-                        float h[4], l[4], s[4];
-                        load4_f16(g.hi + at_e, h);
-                        load4_f16(g.lo + at_e, l);
-                        if constexpr (kTall) {
-                            const float4 t = *reinterpret_cast<const float4*>(scale + j);
-                            s[0] = t.x; s[1] = t.y; s[2] = t.z; s[3] = t.w;
-                        } else {
-                            s[0] = s[1] = s[2] = s[3] = scale[i];
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            v[r] = kNsA * (h[r] + l[r]) + s[r] * h[r] + v[r] * (1.0f / kScaleSym);
-                        if (g.last) {
-                            *reinterpret_cast<uint2*>(g.U + at_e) =
-                                make_uint2(pack_bf16x2(v[0] * (1.0f / kScaleX), v[1] * (1.0f / kScaleX)),
-                                           pack_bf16x2(v[2] * (1.0f / kScaleX), v[3] * (1.0f / kScaleX)));
-                        } else {
-                            store4_pair(g.hi_next + at_e, g.lo + at_e, v);
-                        }
-                    } else {
-                        uint16_t* out = (kProd == PROD_SYM ? g.sym : g.poly) + at_m;
-                        if (in) {
-                            if constexpr (kProd == PROD_SYM) {
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    if (i == j + r) {
-                                        diag[i] = v[r] * (1.0f / (kScaleX * kScaleX));
-                                        v[r] = 0.f;
-                                    } else {
-                                        v[r] *= kScaleSym / (kScaleX * kScaleX);
-                                    }
-                                }
-                            } else {
-                                float e[4];
-                                load4_f16(sym + i * m + j, e);
-                                const float di = diag[i];
-                                const float4 dj = *reinterpret_cast<const float4*>(diag + j);
-                                const float d[4] = {dj.x, dj.y, dj.z, dj.w};
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const float sq = v[r] * (1.0f / (kScaleSym * kScaleSym));
-                                    if (i == j + r) {
-                                        scale[i] = kNsB * di + kNsC * (sq + di * di);
-                                        v[r] = 0.f;
-                                    } else {
-                                        const float off = e[r] * (1.0f / kScaleSym);
-                                        v[r] = kScaleSym * (kNsB * off + kNsC * (sq + (di + d[r]) * off));
-                                    }
-                                }
-                            }
-                            store4_f16(out + i * m + j, v);
-                        }
-                        if (mirror) {   // the same for the whole workgroup
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                turn[(4 * (lane >> 4) + r) * 20 + (lane & 15)] = (uint16_t)bits_f16(v[r]);
-                            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                            // row jb + lane % 16 of the transpose, columns ib + 4 (lane / 16)
-                            const uint2 w = *reinterpret_cast<const uint2*>(
-                                turn + (lane & 15) * 20 + 4 * (lane >> 4));
-                            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                            const int64_t mi = jb + (lane & 15), mj = ib + 4 * (lane >> 4);
-                            if (mi < m && mj < m) *reinterpret_cast<uint2*>(out + mi * m + mj) = w;
-                        }
-                    }
+                    for (int r = 0; r < 8; ++r) v[r] *= 1.0f / kScaleX;
+                    *reinterpret_cast<uint4*>(g.U + at_e) =
+                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                } else {
+                    store8_pair(g.hi_next + at_e, g.lo + at_e, v);
                 }
+            } else {
+                const bool on_diagonal = i >= j && i < j + 8;
+                float own = 0.f;   // the diagonal element's sum
+                if (on_diagonal) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) own = i == j + r ? v[r] : own;
+                }
+                if constexpr (kProd == PROD_SYM) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] *= kScaleSym / (kScaleX * kScaleX);
+                } else {
+                    // b E + c (E^2 + (D_i + D_j) E), E and the result times kScaleSym
+                    float o[8];
+                    unpack8_f16(e.e, o);
+                    const float ci = kNsC * e.d;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] = v[r] * (kNsC / kScaleSym) + o[r] * (fj[r] + ci);
+                }
+                if (on_diagonal) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] = i == j + r ? 0.f : v[r];
+                    if constexpr (kProd == PROD_SYM)
+                        diag[i] = own * (1.0f / (kScaleX * kScaleX));
+                    else   // b D + c (E^2 + D^2)
+                        scale[i] = kNsB * e.d + kNsC * (own * (1.0f / (kScaleSym * kScaleSym)) + e.d * e.d);
+                }
+                store8_f16(out + i * m + j, v);
+                if (mirror) t.set(smem, place, k, v);
+            }
+        });
+        if (kTri && mirror) {   // the same for the whole workgroup
+            __syncthreads();
+            // rows of the transpose: column jm of the tile, eight of its rows at a time
+            const int64_t ip = i0 + p * PartOf<Cfg>::kRows;
+#pragma unroll 2
+            for (int u = threadIdx.x; u < PartOf<Cfg>::kRows / 8 * Cfg::TJ; u += Cfg::kThreads) {
+                const int r = u % (PartOf<Cfg>::kRows / 8), col = u / (PartOf<Cfg>::kRows / 8);
+                const int64_t i = ip + 8 * r, jm = j0 + col;
+                if (i >= I || jm >= J) continue;
+                float v[8];
+                part_get_column<Cfg>(smem, r, col, v);
+                store8_f16(out + jm * m + i, v);
+            }
         }
+        if (p + 1 < PartOf<Cfg>::kParts) __syncthreads();
+    }
 }
 
 template <class Cfg, int kProd, bool kTall>
@@ -368,7 +398,7 @@ hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B,
     g.hi = hi[1];
     g.hi_next = hi[0];
     hipError_t e;
-    int64_t blocks = (R * C + 1023) / 1024;
+    int64_t blocks = (R * C + 2047) / 2048;
     if (blocks > 2048) blocks = 2048;
     if (f32) {
         hipLaunchKernelGGL(ortho_norm_kernel<true>, dim3(kNormBlocks, (unsigned)B), dim3(256), 0, stream, g);
