@@ -253,7 +253,7 @@ int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const voi
  * mean, rstd: M fp32 (the forward writes them, each may be NULL there; the
  * backward reads them).  dgamma, dbeta: N fp32.  Statistics and sums are fp32
  * (the variance is the centred sum, not E[x^2] - mean^2), in a fixed order.  N a
- * multiple of 8 up to 32768; eps >= 0.  Y may be X itself, and dX may be X or
+ * multiple of 8 up to 16384; eps >= 0.  Y may be X itself, and dX may be X or
  * dY.  With M == 0 the forward does nothing and the backward zero-fills dgamma
  * and dbeta. */
 int ffn_layernorm_forward(const void* X, const void* gamma, const void* beta, void* Y,

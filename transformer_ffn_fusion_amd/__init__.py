@@ -149,7 +149,8 @@ def _stream(stream):
     if stream is not None:
         return stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle, without building a Stream object per call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype_code(t):
@@ -185,7 +186,7 @@ def _arg(t, name, shape, dtype, optional=False):
         if optional:
             return
         raise ValueError(f"{name} must not be None")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -208,14 +209,15 @@ def _on_device(*ts):
     for t in ts:
         if t is None:
             continue
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"every tensor must be on the GPU (got one on {t.device})")
+        i = t.get_device()
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices ({dev} and {t.device})")
-    if dev is not None and dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+            dev = i
+        elif i != dev:
+            raise ValueError(f"tensors on different devices (cuda:{dev} and cuda:{i})")
+    if dev is not None and dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _torch_dtype(code):

@@ -192,7 +192,8 @@ hipError_t launch_ffn_backward(const BackwardIO& io, hipStream_t stream, void** 
 
 // ---- layer norm (layernorm.hip)
 
-constexpr int64_t kLnMaxN = 32768;         // a row is held by one workgroup's registers
+constexpr int64_t kLnMaxN = 16384;         // a row is held by one workgroup's registers
+constexpr int64_t kLnForwardBlocks = 2048;  // most workgroups of four waves of the forward
 constexpr int64_t kLnBackwardBlocks = 256; // most workgroups of the backward's row kernel
 size_t layernorm_partial_floats(int64_t M, int64_t N);   // the workgroups' column sums
 hipError_t launch_layernorm_forward(const void* X, const void* gamma, const void* beta, void* Y,
