@@ -139,8 +139,9 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
     struct None {};
     struct Dh { float v[8]; };
     PartStates<Cfg, kCols, std::conditional_t<kStep == STEP_GATED, Dh, None>> states;
-    auto before = [&](int row, auto& d) {
-        if constexpr (kStep == STEP_GATED) load8_f32(g.dH + (i0 + row) * O + j, d.v);
+    const int64_t first = (i0 + t.row0) * O + j;   // this thread's place in an M x O matrix
+    auto before = [&](int off, auto& d) {
+        if constexpr (kStep == STEP_GATED) load8_f32(g.dH + first + (int64_t)off * O, d.v);
     };
     if (g.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
 
@@ -155,40 +156,40 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
         states.load(t, rows, before);
     }
 
-    const uint32_t place = t.place(2 * t.c), place_up = t.place(Cfg::HJ / 4 + 2 * t.c);
-    // the output of the other steps, its leading dimension, this thread's first column
+    // the output of the other steps, its leading dimension, this thread's place there
     constexpr bool kF32 = kStep == STEP_DH || ((kStep == STEP_DGU || kStep == STEP_DD) && kGradF32);
     void* out = kStep == STEP_DH ? (void*)g.dH : kStep == STEP_DX ? (void*)g.dX
                 : kStep == STEP_DD ? g.dWd : j < O ? g.dWg : g.dWu;
     const int64_t ld = kStep == STEP_DX ? N : kStep == STEP_DD ? P : O;
-    const int64_t jo = kStep == STEP_DGU && j >= O ? j - O : j;
+    const int64_t at_out = (i0 + t.row0) * ld + (kStep == STEP_DGU && j >= O ? j - O : j);
+    const int64_t first2 = (i0 + t.row0) * 2 * O + j;   // in da | db
 #pragma unroll
     for (int p = 0; p < PartOf<Cfg>::kParts; ++p) {
         part_put<Cfg>(smem, acc, p);
         __syncthreads();
-        states.each(t, p, rows, before, [&](int k, int row, const auto& d) {
-            const int64_t i = i0 + row;
-            if constexpr (kStep == STEP_GATED) {
-                float a[8], b[8], h[8], da[8], db[8];
-                t.get(smem, place, k, a);
-                t.get(smem, place_up, k, b);
+        if constexpr (kStep == STEP_GATED) {
+            const uint32_t places[2] = {t.place(2 * t.c), t.place(Cfg::HJ / 4 + 2 * t.c)};
+            states.each(smem, t, places, p, rows, before, [&](int off, int, const float (&v)[2][8], const Dh& d) {
+                float h[8], da[8], db[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-a[r]));
-                    const float u = a[r] * s;
-                    h[r] = u * b[r];
-                    da[r] = d.v[r] * b[r] * (s + u * (1.0f - s));
+                    const float a = v[0][r], b = v[1][r];
+                    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-a));
+                    const float u = a * s;
+                    h[r] = u * b;
+                    da[r] = d.v[r] * b * (s + u * (1.0f - s));
                     db[r] = d.v[r] * u;
                 }
-                store8<false>(g.H, i * O + j, h);
-                store8<false>(g.dAB, i * 2 * O + j, da);
-                store8<false>(g.dAB, i * 2 * O + O + j, db);
-            } else {
-                float v[8];
-                t.get(smem, place, k, v);
-                store8<kF32>(out, i * ld + jo, v);
-            }
-        });
+                store8<false>(g.H, first + (int64_t)off * O, h);
+                store8<false>(g.dAB, first2 + (int64_t)off * 2 * O, da);
+                store8<false>(g.dAB, first2 + (int64_t)off * 2 * O + O, db);
+            });
+        } else {
+            const uint32_t places[1] = {t.place(2 * t.c)};
+            states.each(smem, t, places, p, rows, before, [&](int off, int, const float (&v)[1][8], const None&) {
+                store8<kF32>(out, at_out + (int64_t)off * ld, v[0]);
+            });
+        }
         if (p + 1 < PartOf<Cfg>::kParts) __syncthreads();
     }
 }

@@ -411,13 +411,19 @@ __device__ __forceinline__ void part_get_column(const char* smem, int r, int col
 // What the epilogue reads per row of a thread, for every row of the tile.  The small
 // and mid tiles have registers left to load it before the products (kEarly: its
 // latency, 1 to 2 us, is hidden); the large tile loads four rows at a time after them.
+//
+// The callbacks get a row as its distance `off` from the thread's first row, the same
+// for all threads: with a pointer to the first row, off * leading dimension is scalar
+// arithmetic.
 template <class Cfg, int kCols, class State>
 struct PartStates {
     static constexpr bool kEarly = Cfg::FI * Cfg::FJ <= 4 && !std::is_empty<State>::value;
-    static constexpr int kUnits = PartThread<Cfg, kCols>::kUnits;
+    static constexpr int kUnits = PartThread<Cfg, kCols>::kUnits, kStep = PartThread<Cfg, kCols>::kStep;
+    static constexpr int kGroup = kUnits < 4 ? kUnits : 4;
+    static_assert(kUnits % kGroup == 0, "whole groups");
     State early[kEarly ? PartOf<Cfg>::kParts : 1][kEarly ? kUnits : 1];
 
-    // before(row of the tile, state)
+    // before(off, state) for rows below `rows`
     template <class Before>
     __device__ __forceinline__ void load(const PartThread<Cfg, kCols>& t, int rows, Before&& before) {
         if constexpr (kEarly) {
@@ -425,37 +431,42 @@ struct PartStates {
             for (int p = 0; p < PartOf<Cfg>::kParts; ++p)
 #pragma unroll
                 for (int k = 0; k < kUnits; ++k) {
-                    const int row = p * PartOf<Cfg>::kRows + t.row0 + k * t.kStep;
-                    if (row < rows) before(row, early[p][k]);
+                    const int off = p * PartOf<Cfg>::kRows + k * kStep;
+                    if (t.row0 + off < rows) before(off, early[p][k]);
                 }
         }
     }
-    // after(k, row of the tile, state) for every row of part p below `rows`
-    template <class Before, class After>
-    __device__ __forceinline__ void each(const PartThread<Cfg, kCols>& t, int p, int rows,
+    // after(off, k, values, state) for the rows of part p below `rows`; values[g]: the
+    // eight sums at places[g]
+    template <int kGets, class Before, class After>
+    __device__ __forceinline__ void each(const char* smem, const PartThread<Cfg, kCols>& t,
+                                         const uint32_t (&places)[kGets], int p, int rows,
                                          Before&& before, After&& after) {
+        auto group = [&](int u, State* st) __attribute__((always_inline)) {
+            float v[kGroup][kGets][8];
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+                for (int g = 0; g < kGets; ++g) t.get(smem, places[g], u + k, v[k][g]);
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                const int off = p * PartOf<Cfg>::kRows + (u + k) * kStep;
+                if (t.row0 + off < rows) after(off, u + k, v[k], st[k]);
+            }
+        };
         if constexpr (kEarly) {
 #pragma unroll
-            for (int k = 0; k < kUnits; ++k) {
-                const int row = p * PartOf<Cfg>::kRows + t.row0 + k * t.kStep;
-                if (row < rows) after(k, row, early[p][k]);
-            }
+            for (int u = 0; u < kUnits; u += kGroup) group(u, &early[p][u]);
         } else {
-            constexpr int kGroup = kUnits < 4 ? kUnits : 4;
-            static_assert(kUnits % kGroup == 0, "whole groups");
 #pragma unroll 1
             for (int u = 0; u < kUnits; u += kGroup) {
                 State st[kGroup];
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
-                    const int row = p * PartOf<Cfg>::kRows + t.row0 + (u + k) * t.kStep;
-                    if (row < rows) before(row, st[k]);
+                    const int off = p * PartOf<Cfg>::kRows + (u + k) * kStep;
+                    if (t.row0 + off < rows) before(off, st[k]);
                 }
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    const int row = p * PartOf<Cfg>::kRows + t.row0 + (u + k) * t.kStep;
-                    if (row < rows) after(u + k, row, st[k]);
-                }
+                group(u, st);
             }
         }
     }

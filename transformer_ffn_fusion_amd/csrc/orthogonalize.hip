@@ -199,16 +199,18 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     using State = std::conditional_t<kProd == PROD_SYM, None,
                                      std::conditional_t<kProd == PROD_POLY, OfPoly, OfX>>;
     PartStates<Cfg, Cfg::TJ, State> states;
-    auto before = [&](int row, State& e) {
-        const int64_t i = i0 + row;
+    const int64_t ld = kProd == PROD_X ? g.C : m;
+    const int64_t first = (kProd == PROD_X ? at_x : 0) + (i0 + t.row0) * ld + j;
+    const float* row_vector = (kProd == PROD_POLY ? diag : scale) + i0 + t.row0;
+    auto before = [&](int off, State& e) {
         if constexpr (kProd == PROD_POLY) {
-            e.e = ld16(sym + i * m + j);
-            e.d = diag[i];
+            e.e = ld16(sym + first + (int64_t)off * ld);
+            e.d = row_vector[off];
         }
         if constexpr (kProd == PROD_X) {
-            e.hi = ld16(hi + i * g.C + j);
-            e.lo = ld16(g.lo + at_x + i * g.C + j);
-            if constexpr (!kTall) e.s = scale[i];
+            e.hi = ld16(g.hi + first + (int64_t)off * ld);
+            e.lo = ld16(g.lo + first + (int64_t)off * ld);
+            if constexpr (!kTall) e.s = row_vector[off];
         }
     };
     if (g.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
@@ -232,23 +234,26 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     }
 
     uint16_t* out = (kProd == PROD_SYM ? g.sym : g.poly) + at_m;
-    const uint32_t place = t.place(2 * t.c);
+    const uint32_t places[1] = {t.place(2 * t.c)};
+    // this thread's column of the diagonal in its row off: off + this, 0 to 7 if any
+    const int to_diagonal = kTri && !mirror ? (int)(i0 - j0) + t.row0 - 8 * t.c : -(1 << 30);
 #pragma unroll
     for (int p = 0; p < PartOf<Cfg>::kParts; ++p) {
         part_put<Cfg>(smem, acc, p);
         __syncthreads();
-        states.each(t, p, rows, before, [&](int k, int row, const State& e) {
-            const int64_t i = i0 + row;
+        states.each(smem, t, places, p, rows, before, [&](int off, int k, const float (&w)[1][8], const State& e) {
             float v[8];
-            t.get(smem, place, k, v);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = w[0][r];
             if constexpr (kProd == PROD_X) {
                 float h[8], l[8];
                 unpack8_f16(e.hi, h);
                 unpack8_f16(e.lo, l);
+                const float si = kTall ? 0.f : kNsA + e.s;
 #pragma unroll
                 for (int r = 0; r < 8; ++r)   // a (hi + lo) + scale hi + product
-                    v[r] = v[r] * (1.0f / kScaleSym) + (kTall ? fj[r] : kNsA + e.s) * h[r] + kNsA * l[r];
-                const int64_t at_e = at_x + i * g.C + j;
+                    v[r] = v[r] * (1.0f / kScaleSym) + (kTall ? fj[r] : si) * h[r] + kNsA * l[r];
+                const int64_t at_e = first + (int64_t)off * ld;
                 if (g.last) {
 #pragma unroll
                     for (int r = 0; r < 8; ++r) v[r] *= 1.0f / kScaleX;
@@ -259,12 +264,6 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
                     store8_pair(g.hi_next + at_e, g.lo + at_e, v);
                 }
             } else {
-                const bool on_diagonal = i >= j && i < j + 8;
-                float own = 0.f;   // the diagonal element's sum
-                if (on_diagonal) {
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) own = i == j + r ? v[r] : own;
-                }
                 if constexpr (kProd == PROD_SYM) {
 #pragma unroll
                     for (int r = 0; r < 8; ++r) v[r] *= kScaleSym / (kScaleX * kScaleX);
@@ -276,16 +275,22 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
 #pragma unroll
                     for (int r = 0; r < 8; ++r) v[r] = v[r] * (kNsC / kScaleSym) + o[r] * (fj[r] + ci);
                 }
-                if (on_diagonal) {
+                const int on = off + to_diagonal;
+                if ((unsigned)on < 8u) {
+                    float own = 0.f;   // the diagonal element's sum
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] = i == j + r ? 0.f : v[r];
+                    for (int r = 0; r < 8; ++r) {
+                        own = r == on ? w[0][r] : own;
+                        v[r] = r == on ? 0.f : v[r];
+                    }
+                    const int64_t i = i0 + t.row0 + off;
                     if constexpr (kProd == PROD_SYM)
                         diag[i] = own * (1.0f / (kScaleX * kScaleX));
                     else   // b D + c (E^2 + D^2)
                         scale[i] = kNsB * e.d + kNsC * (own * (1.0f / (kScaleSym * kScaleSym)) + e.d * e.d);
                 }
-                store8_f16(out + i * m + j, v);
-                if (mirror) t.set(smem, place, k, v);
+                store8_f16(out + first + (int64_t)off * ld, v);
+                if (mirror) t.set(smem, places[0], k, v);
             }
         });
         if (kTri && mirror) {   // the same for the whole workgroup
