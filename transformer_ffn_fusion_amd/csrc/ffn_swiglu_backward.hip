@@ -36,7 +36,8 @@ struct SwigluBackwardArgs {
     float* part;        // sums of split products (tile_join)
     uint32_t* count;
     int64_t M, N, O, P;
-    int splits;         // of this step
+    int64_t full;       // tiles of this step that are not split ...
+    int splits;         // ... and into how many the others are
     int64_t clear;      // counters that the first step sets to 0
 };
 
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
             for (int64_t k = threadIdx.x; k < g.clear; k += Cfg::kThreads) g.count[k] = 0;
     TilePlace at;
     if (!tile_place<false>(blockIdx.x, (uint32_t)((I + Cfg::TI - 1) / Cfg::TI),
-                           (uint32_t)((J + kWidth - 1) / kWidth), (uint32_t)g.splits, &at))
+                           (uint32_t)((J + kWidth - 1) / kWidth), (uint32_t)g.full, (uint32_t)g.splits, &at))
         return;
     const int64_t i0 = (int64_t)at.ti * Cfg::TI, j0 = (int64_t)at.tj * kWidth;
 
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
     B.at[0] = j0;
     B.at[1] = kStep == STEP_GATED ? j0 : j0 + Cfg::HJ;
     constexpr int kPairs = kStep == STEP_DX ? 2 : 1;
-    const int nt = S::depth(M, N, O, P), depth = (nt + g.splits - 1) / g.splits;
+    const int nt = S::depth(M, N, O, P), depth = (nt + at.splits - 1) / at.splits;
     const int t0 = at.split * depth, t1 = t0 + depth < nt ? t0 + depth : nt;
     // the epilogue's share of this thread; every column count is a multiple of 8: its
     // eight columns are all in or all out
@@ -143,14 +144,14 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
     auto before = [&](int off, auto& d) {
         if constexpr (kStep == STEP_GATED) load8_f32(g.dH + first + (int64_t)off * O, d.v);
     };
-    if (g.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
+    if (at.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
 
     TileAcc<Cfg> acc;
     tile_clear<Cfg>(acc);
     tile_product<Cfg, S::kAS, S::kBS, false, kPairs>(smem, A, B, K, a2, b2, b_half2, t0, t1, acc);
-    if (g.splits > 1) {
-        if (!tile_join<Cfg>(smem, g.part + (int64_t)at.tile * g.splits * (Cfg::TI * Cfg::TJ),
-                            g.count + at.tile, at.split, g.splits,
+    if (at.splits > 1) {
+        if (!tile_join<Cfg>(smem, g.part + (int64_t)at.joint * at.splits * (Cfg::TI * Cfg::TJ),
+                            g.count + at.joint, at.split, at.splits,
                             (int)(I - i0 < Cfg::TI ? I - i0 : Cfg::TI), acc))
             return;
         states.load(t, rows, before);
@@ -204,7 +205,7 @@ hipError_t launch_step_cfg(const SwigluBackwardArgs& g, hipStream_t stream) {
     const int64_t I = S::rows(g.M, g.N, g.O), J = S::cols(g.N, g.O, g.P);
     constexpr int kWidth = S::template width<Cfg>();
     const int64_t tiles = tile_count((I + Cfg::TI - 1) / Cfg::TI, (J + kWidth - 1) / kWidth, false);
-    hipLaunchKernelGGL(kern, dim3((unsigned)tile_grid(tiles, g.splits)), dim3(Cfg::kThreads),
+    hipLaunchKernelGGL(kern, dim3((unsigned)tile_grid(tiles, g.full, g.splits)), dim3(Cfg::kThreads),
                        Cfg::kLds, stream, g);
     return hipGetLastError();
 }
@@ -213,6 +214,7 @@ template <int kStep, bool kGradF32>
 hipError_t launch_step(SwigluBackwardArgs g, hipStream_t stream) {
     const TilePlan plan = StepShape<kStep>::plan(g.M, g.N, g.O, g.P);
     g.splits = plan.splits;
+    g.full = plan.full;
     if (plan.tile == TILE_LARGE) return launch_step_cfg<TileLarge, kStep, kGradF32>(g, stream);
     if (plan.tile == TILE_MID) return launch_step_cfg<TileMid, kStep, kGradF32>(g, stream);
     return launch_step_cfg<TileSmall, kStep, kGradF32>(g, stream);
@@ -236,7 +238,7 @@ hipError_t launch_all(const SwigluBackwardArgs& g, int64_t counters, hipStream_t
 
 // What the five steps' joins need at most: they run one after the other.
 TilePlan join_need(int64_t M, int64_t N, int64_t O, int64_t P) {
-    TilePlan most{0, 1, 0, 0};
+    TilePlan most{0, 1, 0, 0, 0};
     const TilePlan plans[] = {StepShape<STEP_DH>::plan(M, N, O, P), StepShape<STEP_GATED>::plan(M, N, O, P),
                               StepShape<STEP_DX>::plan(M, N, O, P), StepShape<STEP_DGU>::plan(M, N, O, P),
                               StepShape<STEP_DD>::plan(M, N, O, P)};
@@ -257,7 +259,7 @@ SwigluBackwardLayout swiglu_backward_layout(int64_t M, int64_t N, int64_t O, int
         off += (bytes + 255) / 256 * 256;
         return at;
     };
-    const TilePlan join = M > 0 ? join_need(M, N, O, P) : TilePlan{0, 1, 0, 0};
+    const TilePlan join = M > 0 ? join_need(M, N, O, P) : TilePlan{0, 1, 0, 0, 0};
     L.dH = take(sizeof(float) * M * O);
     L.H = take(sizeof(uint16_t) * M * O);
     L.dAB = take(sizeof(uint16_t) * M * 2 * O);
@@ -290,6 +292,7 @@ hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream
     g.O = io.O;
     g.P = io.P;
     g.splits = 1;
+    g.full = 0;
     g.clear = 0;
     return io.grad_f32 ? launch_all<true>(g, L.counters, stream) : launch_all<false>(g, L.counters, stream);
 }

@@ -485,31 +485,46 @@ __device__ __forceinline__ void tile_clear(TileAcc<Cfg>& acc) {
 }
 
 // Work of one launch: nI x nJ output tiles (kTri: the lower triangle of a square
-// of nI x nI), each cut into `splits` ranges of k-tiles.  Workgroups reach the 8
-// XCDs round-robin and each XCD has an L2 of its own: XCD x takes a contiguous run
-// of a grouped order (groups of 8 tile rows, rows fastest; a tile's splits side by
-// side), a compact rectangle whose panels its L2 shares.
+// of nI x nI).  The first `full` tiles are a workgroup's each; each of the others is
+// cut into `splits` ranges of k-tiles: all of them where there are few, or those that
+// would leave a last round of the CUs half empty.  Workgroups reach the 8 XCDs
+// round-robin and each XCD has an L2 of its own: XCD x takes a contiguous run of a
+// grouped order (groups of 8 tile rows, rows fastest; a tile's splits side by side), a
+// compact rectangle whose panels its L2 shares.
 struct TilePlace {
-    int ti, tj, tile, split;   // tile: the tile's number
+    int ti, tj;
+    int split, splits;   // which part of the tile's depth, of how many
+    int joint;           // the tile's number among the split ones
 };
 __host__ __device__ __forceinline__ int64_t tile_count(int64_t nI, int64_t nJ, bool tri) {
     return tri ? nI * (nI + 1) / 2 : nI * nJ;
 }
-__host__ __device__ __forceinline__ int64_t tile_grid(int64_t tiles, int splits) {
-    return 8 * ((tiles * splits + 7) / 8);
+__host__ __device__ __forceinline__ int64_t tile_grid(int64_t tiles, int64_t full, int splits) {
+    return 8 * ((full + 7) / 8 + ((tiles - full) * splits + 7) / 8);
 }
 // Returns false for the padding workgroups.  (32-bit arithmetic: six 64-bit
 // divisions took 0.5 us of every launch.)
 template <bool kTri>
-__device__ __forceinline__ bool tile_place(uint32_t w, uint32_t nI, uint32_t nJ, uint32_t splits,
-                                           TilePlace* at) {
+__device__ __forceinline__ bool tile_place(uint32_t w, uint32_t nI, uint32_t nJ, uint32_t full,
+                                           uint32_t splits, TilePlace* at) {
     constexpr uint32_t G = 8;
-    const uint32_t n = (kTri ? nI * (nI + 1) / 2 : nI * nJ) * splits, per = (n + 7) / 8;
+    const uint32_t tiles = kTri ? nI * (nI + 1) / 2 : nI * nJ, grid = (full + 7) / 8 * 8;
+    const bool part = w >= grid;
+    if (part) w -= grid;
+    const uint32_t n = part ? (tiles - full) * splits : full, per = (n + 7) / 8;
     const uint32_t u = (w & 7) * per + (w >> 3);
     if (u >= n || (w >> 3) >= per) return false;
-    const uint32_t t = splits == 1 ? u : u / splits;
-    at->tile = (int)t;
-    at->split = (int)(u - t * splits);
+    uint32_t t = u;
+    at->split = 0;
+    at->splits = 1;
+    at->joint = 0;
+    if (part && splits > 1) {
+        const uint32_t q = u / splits;
+        at->split = (int)(u - q * splits);
+        at->splits = (int)splits;
+        at->joint = (int)q;
+        t = full + q;
+    }
     if constexpr (kTri) {
         uint32_t r = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
         if (r * (r + 1) / 2 > t) --r;   // the root is off by one at most
@@ -622,6 +637,7 @@ using TileSmall = TileCfg<128, 128, 2, 2>;   // four waves, two workgroups per C
 enum { TILE_LARGE = 0, TILE_MID = 1, TILE_SMALL = 2 };
 struct TilePlan {
     int tile, splits;
+    int64_t full;                    // of one matrix's tiles: those that are not split
     int64_t part_floats, counters;   // workspace of the join (0 without splits)
 };
 
@@ -633,36 +649,45 @@ struct TilePlan {
 // launch takes about 4.5.  A join costs (large) 5.5 + 2.7 a split, (mid) 3 + 1.35,
 // (small) 2 + 1 -- the last workgroup reads every split's sums alone, at about 0.1
 // MB/us -- and 0.2 per MB that all tiles' splits write, less where few of a tile's
-// rows are wanted.  Splits beyond one round of the CUs would only add work.
+// rows are wanted.
 inline TilePlan tile_plan(int64_t I, int64_t J, int share, int64_t nt, int64_t batch, bool tri) {
     struct Kind { int ti, tj, slots; double join, join_split; };
     const Kind kinds[3] = {{256, 256, 256, 5.5, 2.7}, {256, 128, 256, 3.0, 1.35}, {128, 128, 512, 2.0, 1.0}};
-    TilePlan best{TILE_LARGE, 1, 0, 0};
+    TilePlan best{TILE_LARGE, 1, 0, 0, 0};
     double best_t = 1e30;
     for (int k = 0; k < 3; ++k) {
         if (tri && kinds[k].ti != kinds[k].tj) continue;
-        const int64_t wj = kinds[k].tj / share;
-        const int64_t tiles = batch * tile_count((I + kinds[k].ti - 1) / kinds[k].ti, (J + wj - 1) / wj, tri);
+        const int64_t wj = kinds[k].tj / share, slots = kinds[k].slots;
+        const int64_t each = tile_count((I + kinds[k].ti - 1) / kinds[k].ti, (J + wj - 1) / wj, tri);
+        const int64_t tiles = batch * each;
         const double rows = I < kinds[k].ti ? (double)((I + 15) / 16 * 16) / kinds[k].ti : 1.0;
+        // per k-tile with `units` workgroups at work
+        auto per = [&](int64_t units) {
+            const double busy = units < slots ? (double)units / (double)slots : 1.0;
+            return k == TILE_LARGE ? 0.95 + 0.45 * busy
+                   : k == TILE_MID ? 0.54 + 0.33 * busy
+                   : busy <= 0.5   ? 0.43 + 0.24 * busy
+                                   : 0.6 + 0.35 * busy;
+        };
         for (int64_t s = 1; s <= 16 && s <= nt; ++s) {
-            if (s > 1 && tiles * s > kinds[k].slots) break;
             const int64_t depth = (nt + s - 1) / s;
             if ((nt + depth - 1) / depth != s) continue;   // an empty last split
-            const int64_t units = tiles * s, rounds = (units + kinds[k].slots - 1) / kinds[k].slots;
-            const double busy = units < kinds[k].slots ? (double)units / kinds[k].slots : 1.0;
-            const double per = k == TILE_LARGE ? 0.95 + 0.45 * busy
-                               : k == TILE_MID ? 0.54 + 0.33 * busy
-                               : busy <= 0.5   ? 0.43 + 0.24 * busy
-                                               : 0.6 + 0.35 * busy;
-            const double mb = (double)units * kinds[k].ti * kinds[k].tj * 4e-6;
-            double t = 4.5 + (double)(rounds * depth) * per;
-            if (s > 1) t += kinds[k].join + rows * ((double)s * kinds[k].join_split + 0.2 * mb);
+            // whole rounds of the CUs stay unsplit; what is split is one round at most
+            const int64_t full = s == 1 ? tiles : tiles / slots * slots, rest = tiles - full;
+            if (s > 1 && (rest == 0 || rest * s > slots || (full && batch > 1))) continue;
+            double t = 4.5 + (double)((full + slots - 1) / slots * nt) * per(full);
+            if (s > 1) {
+                const double mb = (double)(rest * s) * kinds[k].ti * kinds[k].tj * 4e-6;
+                t += (double)depth * per(rest * s) + kinds[k].join +
+                     rows * ((double)s * kinds[k].join_split + 0.2 * mb);
+            }
             if (t < best_t) {
                 best_t = t;
                 best.tile = k;
                 best.splits = (int)s;
-                best.part_floats = s > 1 ? units * (int64_t)kinds[k].ti * kinds[k].tj : 0;
-                best.counters = s > 1 ? tiles : 0;
+                best.full = s == 1 ? each : full;
+                best.part_floats = s > 1 ? rest * s * (int64_t)kinds[k].ti * kinds[k].tj : 0;
+                best.counters = s > 1 ? rest : 0;
             }
         }
     }

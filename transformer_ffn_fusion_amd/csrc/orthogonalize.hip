@@ -54,7 +54,8 @@ struct OrthoArgs {
     float* part;            // sums of split products, and a counter per tile (tile_join)
     uint32_t* count;
     int64_t counters;
-    int splits;             // of this product
+    int64_t full;           // a matrix's tiles of this product that are not split ...
+    int splits;             // ... and into how many the others are
     int64_t R, C, m, n;     // m = min(R, C), n = max(R, C)
     int last;               // the last step writes U
 };
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     const int64_t m = g.m, I = kProd == PROD_X ? g.R : m, J = kProd == PROD_X ? g.C : m;
     const uint32_t nI = (uint32_t)((I + Cfg::TI - 1) / Cfg::TI), nJ = (uint32_t)((J + Cfg::TJ - 1) / Cfg::TJ);
     TilePlace at;
-    if (!tile_place<kTri>(blockIdx.x, nI, nJ, (uint32_t)g.splits, &at)) return;
+    if (!tile_place<kTri>(blockIdx.x, nI, nJ, (uint32_t)g.full, (uint32_t)g.splits, &at)) return;
     const int64_t i0 = (int64_t)at.ti * Cfg::TI, j0 = (int64_t)at.tj * Cfg::TJ;
     const int64_t at_x = (int64_t)blockIdx.y * g.R * g.C, at_m = (int64_t)blockIdx.y * m * m;
     const uint16_t* hi = g.hi + at_x;
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     A.at[1] = i0 + Cfg::HI;
     B.at[0] = j0;
     B.at[1] = j0 + Cfg::HJ;
-    const int nt = (int)((K + kTileK - 1) / kTileK), depth = (nt + g.splits - 1) / g.splits;
+    const int nt = (int)((K + kTileK - 1) / kTileK), depth = (nt + at.splits - 1) / at.splits;
     const int t0 = at.split * depth, t1 = t0 + depth < nt ? t0 + depth : nt;
     const bool mirror = kTri && at.ti != at.tj;
 
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
             if constexpr (!kTall) e.s = row_vector[off];
         }
     };
-    if (g.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
+    if (at.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
     // the column's factors: POLY b + c D_j, X from the right a + scale_j
     float fj[8];
     if constexpr (kProd == PROD_POLY || (kProd == PROD_X && kTall)) {
@@ -225,10 +226,10 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     TileAcc<Cfg> acc;
     tile_clear<Cfg>(acc);
     tile_product<Cfg, kAS, kBS, true, 1>(smem, A, B, K, nullptr, nullptr, nullptr, t0, t1, acc);
-    if (g.splits > 1) {
-        const int64_t tile = (int64_t)blockIdx.y * tile_count(nI, nJ, kTri) + at.tile;
-        if (!tile_join<Cfg>(smem, g.part + tile * g.splits * (Cfg::TI * Cfg::TJ), g.count + tile,
-                            at.split, g.splits, (int)(I - i0 < Cfg::TI ? I - i0 : Cfg::TI), acc))
+    if (at.splits > 1) {
+        const int64_t joint = (int64_t)blockIdx.y * (tile_count(nI, nJ, kTri) - g.full) + at.joint;
+        if (!tile_join<Cfg>(smem, g.part + joint * at.splits * (Cfg::TI * Cfg::TJ), g.count + joint,
+                            at.split, at.splits, (int)(I - i0 < Cfg::TI ? I - i0 : Cfg::TI), acc))
             return;
         states.load(t, rows, before);
     }
@@ -320,7 +321,7 @@ hipError_t launch_product_cfg(const OrthoArgs& g, int64_t batch, hipStream_t str
     const int64_t I = kProd == PROD_X ? g.R : g.m, J = kProd == PROD_X ? g.C : g.m;
     const int64_t tiles = tile_count((I + Cfg::TI - 1) / Cfg::TI, (J + Cfg::TJ - 1) / Cfg::TJ,
                                      kProd != PROD_X);
-    hipLaunchKernelGGL(kern, dim3((unsigned)tile_grid(tiles, g.splits), (unsigned)batch),
+    hipLaunchKernelGGL(kern, dim3((unsigned)tile_grid(tiles, g.full, g.splits), (unsigned)batch),
                        dim3(Cfg::kThreads), Cfg::kLds, stream, g);
     return hipGetLastError();
 }
@@ -336,6 +337,7 @@ template <int kProd, bool kTall>
 hipError_t launch_product(OrthoArgs g, int64_t batch, hipStream_t stream) {
     const TilePlan plan = product_plan<kProd>(batch, g.R, g.C);
     g.splits = plan.splits;
+    g.full = plan.full;
     if (plan.tile == TILE_LARGE) return launch_product_cfg<TileLarge, kProd, kTall>(g, batch, stream);
     if constexpr (kProd == PROD_X)
         if (plan.tile == TILE_MID) return launch_product_cfg<TileMid, kProd, kTall>(g, batch, stream);
@@ -393,6 +395,7 @@ hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B,
     g.count = reinterpret_cast<uint32_t*>(ws + L.count);
     g.counters = L.counters;
     g.splits = 1;
+    g.full = 0;
     g.R = R;
     g.C = C;
     g.m = R < C ? R : C;
