@@ -47,11 +47,32 @@ def test_steps(steps):
 
 
 def test_large_tiles():
-    # tiles of 256 x 256 for the outer product (4136 x 2056) and the symmetric ones
+    # tiles of 256 x 256 for the outer product, joined splits of small ones for the symmetric one
     G = gradient(2056, 4136, seed=1).bfloat16().cuda()
     ref.check_orthogonalize(run(G), G, 5, "2056 x 4136")
     Gt = G.t().contiguous()
     ref.check_orthogonalize(run(Gt), Gt, 5, "4136 x 2056")
+
+
+def test_joined_large_tiles():
+    # 3584 rows: the symmetric product takes tiles of 256 x 256 in two joined splits
+    G = gradient(3400, 8200, seed=2, rank=4096).bfloat16().cuda()
+    U = run(G)
+    assert bool(torch_isfinite(U).all())
+    # the fp64 iteration on the GPU: 3400 x 8200 is too long for the host
+    import torch
+    X = G.double() / (torch.linalg.vector_norm(G.double()) + ref.NS_EPS)
+    for _ in range(5):
+        A = X @ X.t().contiguous()
+        X = ref.NS[0] * X + (ref.NS[1] * A + ref.NS[2] * (A @ A)) @ X
+    rel = float(torch.linalg.vector_norm(U.double() - X) / torch.linalg.vector_norm(X))
+    print(f"  3400 x 8200: relative error {rel:.2e}", flush=True)
+    assert rel <= ref.NS_REL
+
+
+def torch_isfinite(t):
+    import torch
+    return torch.isfinite(t.float())
 
 
 @pytest.mark.parametrize("kind", ["rank 1", "rank 16", "orthogonal", "one large direction", "tiny", "huge"])

@@ -55,9 +55,14 @@ def test_shapes(shape, grad_f32):
     ref.check(run(x, out), ref.swiglu_backward(*x.values(), grad_f32=grad_f32), str(shape))
 
 
-def test_large_tiles():
-    # enough tiles of 256 x 256 to choose them, with ragged edges
-    shape = (2056, 2072, 1048, 2056)
+@pytest.mark.parametrize("shape", [
+    (2056, 2072, 1048, 2056),    # tiles of 256 x 128 with ragged edges
+    (3000, 1000, 2800, 1000),    # of 256 x 256; two whole rounds of small ones and a split rest; joins
+    (1013, 2056, 1400, 1992),    # joins
+    (8, 128, 512, 128),          # joins of few rows
+    (20, 2048, 1024, 1536),
+])
+def test_large_shapes(shape):
     print(f"case swiglu backward {shape}", flush=True)
     x, out = make(*shape, seed=3)
     ref.check(run(x, out), ref.swiglu_backward(*x.values()), str(shape))
