@@ -72,8 +72,9 @@ typedef enum { FFN_ACT_NONE = 0, FFN_ACT_RELU = 1, FFN_ACT_GELU_TANH = 2 } ffn_a
  * whole device at once: other kernels that hold CUs meanwhile (another
  * stream, another process) delay it, and two such calls that run at the
  * same time can hold each other's CUs.  Every wait is bounded (about a
- * second): if one expires, or the hardware deals workgroups to XCDs
- * otherwise than round-robin, every element of Y is NaN rather than wrong.
+ * second): if one expires, as it would if the hardware dealt eight
+ * workgroups in a row to other than eight different XCDs, every element of Y
+ * is NaN rather than wrong.
  * Order concurrent decode calls on one stream, or force FFN_VARIANT_SKINNY. */
 typedef enum {
     FFN_VARIANT_AUTO = 0,

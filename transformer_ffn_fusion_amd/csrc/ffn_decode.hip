@@ -6,14 +6,15 @@
 // parallelism"), for M <= 16 token rows.  At this size the call is a stream
 // of W1 and W2 from HBM; what costs time beyond the stream is the chain of
 // dependent steps between the two layers.  MI355X has 8 XCDs of 32 CUs, each
-// XCD with its own L2; workgroups are dealt to the XCDs in turn
-// (workgroup b runs on XCD b mod 8), which every workgroup checks against the
-// hardware's XCC_ID register.  The hidden dimension is cut into 8 slices of
-// O/8 columns, one per XCD, so that everything layer 2 needs from layer 1
-// stays inside one XCD:
+// XCD with its own L2; workgroups are dealt to the XCDs in turn, the first one
+// on XCD 0 or, once the program has used several streams, on another.  Each
+// workgroup takes its XCD from the hardware's XCC_ID register.  The hidden
+// dimension is cut into 8 slices of O/8 columns, one per XCD, so that everything
+// layer 2 needs from layer 1 stays inside one XCD:
 //
-//  * 256 workgroups of 8 waves, one per CU; workgroup (x, j) (x = b mod 8,
-//    j = b / 8) runs on XCD x.  Its waves 0-3 multiply rows [256 (j / 2),
+//  * 256 workgroups of 8 waves, one per CU; workgroup (x, j) (x its XCD,
+//    j = b / 8): every eight workgroups in a row are on eight different XCDs, so
+//    each pair (x, j) is there once.  Its waves 0-3 multiply rows [256 (j / 2),
 //    +256) of X and W1 over one half (j mod 2) of slice x's columns and write
 //    that K block's fp32 partial of the half; once all 16 K blocks of the
 //    slice are in the XCD's L2, the workgroup sums 1/32 of the slice's
@@ -45,9 +46,10 @@
 // this part, serialised within an XCD).  Flags hold the call's epoch (a
 // 64-bit number that is new for every call), so nothing has to be cleared
 // between calls.
-// Every wait is bounded; on expiry, or if a workgroup finds itself on another
-// XCD than its number says, the call records its epoch in a status word and
-// the reduction writes NaN to all of Y instead of a silently wrong result.
+// Every wait is bounded; on expiry (were workgroups dealt otherwise, some pair
+// (x, j) would be missing and its XCD's waits would expire) the call records its
+// epoch in a status word and the reduction writes NaN to all of Y instead of a
+// silently wrong result.
 #include "ffn_device.h"
 #include "ffn_internal.h"
 
@@ -129,8 +131,7 @@ __device__ __forceinline__ void fail(uint64_t* status, uint64_t epoch) {
         __hip_atomic_store(status, epoch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// One workgroup per CU, workgroup b on XCD x = b mod 8 with index j = b / 8
-// there.  The layer-1 waves compute layer 1 of K block j / 2 over half j mod 2
+// One workgroup per CU, workgroup b on XCD x with index j = b / 8 there.  The layer-1 waves compute layer 1 of K block j / 2 over half j mod 2
 // of slice x: wave w of a group of four takes K rows [256 (j / 2) + 64 w,
 // +64) in two 32-row steps; lane (g, c) loads rows +8g .. +8g+7 of each step
 // and the 8 columns 8c .. 8c+7 of the half, transposes them in registers into
@@ -156,14 +157,14 @@ __global__ __launch_bounds__((kGated ? 3 : 2) * kThreads) void decode_stream_ker
     const bool l1 = wave < kL1Waves;     // layer-1 waves; the last four run layer 2
     const bool up = kGated && wave >= 4 && wave < 8;
     const int w = wave & 3;
-    const int x = blockIdx.x % kXcds;
+    const int x = xcc_id() % kXcds;
     const int j = blockIdx.x / kXcds;
     const int ox = a.ox;
     const int nks = ox / 32;    // 32-row K steps of layer 2 (the slice's rows)
     const int64_t O = a.O;
     const int64_t P = a.P;
     float* myred = red + (up ? 4 * 16 * 256 : 0);   // this wave's product's LDS sums
-    if (xcc_id() != x) fail(a.status, a.epoch);    // the exchange would not be coherent
+    if (xcc_id() >= kXcds) fail(a.status, a.epoch);
 
     // the elements of H this workgroup finishes after barrier 1: 1/32 of the
     // row-major [16][ox] slice, four consecutive elements per thread of wave 0
