@@ -39,6 +39,7 @@ struct SwigluBackwardArgs {
     int64_t full;       // tiles of this step that are not split ...
     int splits;         // ... and into how many the others are
     int64_t clear;      // counters that the first step sets to 0
+    uint32_t from[3];   // the last three steps in one launch: first workgroup of each
 };
 
 // The steps above.  GATED's tile holds the gate's columns in its first half and
@@ -63,7 +64,7 @@ struct StepShape {
     }
     static TilePlan plan(int64_t M, int64_t N, int64_t O, int64_t P) {
         return tile_plan(rows(M, N, O), cols(N, O, P), kStep == STEP_GATED ? 2 : 1,
-                         depth(M, N, O, P), 1, false);
+                         depth(M, N, O, P), 1, false, kAS ? 2 : kBS ? 1 : 0);
     }
     template <class Cfg>
     static __host__ __device__ constexpr int width() {
@@ -90,19 +91,20 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8])
     }
 }
 
+// Workgroup w of one step.
 template <class Cfg, int kStep, bool kGradF32>
-__global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBackwardArgs g) {
+__device__ __forceinline__ void run_step(char* smem, const SwigluBackwardArgs& g, uint32_t w,
+                                         uint32_t full, uint32_t splits) {
     using S = StepShape<kStep>;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
     const int64_t M = g.M, N = g.N, O = g.O, P = g.P;
     const int64_t I = S::rows(M, N, O), J = S::cols(N, O, P);
     constexpr int kWidth = S::template width<Cfg>();
     if constexpr (kStep == STEP_DH)   // a later step's counters (this one has no splits then)
-        if (blockIdx.x == 0)
+        if (w == 0)
             for (int64_t k = threadIdx.x; k < g.clear; k += Cfg::kThreads) g.count[k] = 0;
     TilePlace at;
-    if (!tile_place<false>(blockIdx.x, (uint32_t)((I + Cfg::TI - 1) / Cfg::TI),
-                           (uint32_t)((J + kWidth - 1) / kWidth), (uint32_t)g.full, (uint32_t)g.splits, &at))
+    if (!tile_place<false>(w, (uint32_t)((I + Cfg::TI - 1) / Cfg::TI),
+                           (uint32_t)((J + kWidth - 1) / kWidth), full, splits, &at))
         return;
     const int64_t i0 = (int64_t)at.ti * Cfg::TI, j0 = (int64_t)at.tj * kWidth;
 
@@ -196,18 +198,51 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
 }
 
 template <class Cfg, int kStep, bool kGradF32>
-hipError_t launch_step_cfg(const SwigluBackwardArgs& g, hipStream_t stream) {
-    using S = StepShape<kStep>;
-    auto kern = swiglu_backward_kernel<Cfg, kStep, kGradF32>;
-    static std::atomic<bool> lds_set[kMaxDevices] = {};
+__global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBackwardArgs g) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    run_step<Cfg, kStep, kGradF32>(smem, g, blockIdx.x, (uint32_t)g.full, (uint32_t)g.splits);
+}
+
+// dX, dWg and dWu, and dWd in one launch: they do not depend on each other, and where
+// each alone leaves CUs idle, or is over before a launch is, together they fill them
+// (whole calls: 8 x 128 x 512 x 128 28 -> 18 us, 16 x 4096 x 1792 x 4096 67 -> 57,
+// 1013 x 2056 x 1400 x 1992 110 -> 95).  Only dX may be split (few tokens: few tiles
+// of it, each as deep as 2 O).
+template <class Cfg, bool kGradF32>
+__global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_outputs_kernel(SwigluBackwardArgs g) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const uint32_t w = blockIdx.x;
+    // dX first: its tiles are the deep ones where there are few tokens, and a join is
+    // best behind other tiles' work
+    if (w < g.from[1])
+        run_step<Cfg, STEP_DX, false>(smem, g, w, (uint32_t)g.full, (uint32_t)g.splits);
+    else if (w < g.from[2])
+        run_step<Cfg, STEP_DGU, kGradF32>(smem, g, w - g.from[1], 0x7fffffffu, 1);
+    else
+        run_step<Cfg, STEP_DD, kGradF32>(smem, g, w - g.from[2], 0x7fffffffu, 1);
+}
+
+template <class Cfg, class Kernel>
+hipError_t launch_kernel(Kernel kern, std::atomic<bool> (&lds_set)[kMaxDevices],
+                         const SwigluBackwardArgs& g, int64_t grid, hipStream_t stream) {
     hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(kern), Cfg::kLds, lds_set);
     if (e != hipSuccess) return e;
-    const int64_t I = S::rows(g.M, g.N, g.O), J = S::cols(g.N, g.O, g.P);
-    constexpr int kWidth = S::template width<Cfg>();
-    const int64_t tiles = tile_count((I + Cfg::TI - 1) / Cfg::TI, (J + kWidth - 1) / kWidth, false);
-    hipLaunchKernelGGL(kern, dim3((unsigned)tile_grid(tiles, g.full, g.splits)), dim3(Cfg::kThreads),
-                       Cfg::kLds, stream, g);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::kThreads), Cfg::kLds, stream, g);
     return hipGetLastError();
+}
+
+template <int kStep>
+int64_t step_tiles(int kind, int64_t M, int64_t N, int64_t O, int64_t P) {
+    using S = StepShape<kStep>;
+    return tile_tiles(kind, S::rows(M, N, O), S::cols(N, O, P), kStep == STEP_GATED ? 2 : 1, false);
+}
+
+template <class Cfg, int kStep, bool kGradF32>
+hipError_t launch_step_cfg(const SwigluBackwardArgs& g, const TilePlan& plan, hipStream_t stream) {
+    static std::atomic<bool> lds_set[kMaxDevices] = {};
+    const int64_t tiles = step_tiles<kStep>(plan.tile, g.M, g.N, g.O, g.P);
+    return launch_kernel<Cfg>(swiglu_backward_kernel<Cfg, kStep, kGradF32>, lds_set, g,
+                              tile_grid(tiles, g.full, g.splits), stream);
 }
 
 template <int kStep, bool kGradF32>
@@ -215,9 +250,55 @@ hipError_t launch_step(SwigluBackwardArgs g, hipStream_t stream) {
     const TilePlan plan = StepShape<kStep>::plan(g.M, g.N, g.O, g.P);
     g.splits = plan.splits;
     g.full = plan.full;
-    if (plan.tile == TILE_LARGE) return launch_step_cfg<TileLarge, kStep, kGradF32>(g, stream);
-    if (plan.tile == TILE_MID) return launch_step_cfg<TileMid, kStep, kGradF32>(g, stream);
-    return launch_step_cfg<TileSmall, kStep, kGradF32>(g, stream);
+    if (plan.tile == TILE_LARGE) return launch_step_cfg<TileLarge, kStep, kGradF32>(g, plan, stream);
+    if (plan.tile == TILE_MID) return launch_step_cfg<TileMid, kStep, kGradF32>(g, plan, stream);
+    return launch_step_cfg<TileSmall, kStep, kGradF32>(g, plan, stream);
+}
+
+// The last three steps together, in small tiles: bound by all the k-tiles there are at
+// the full chip's rate, or by the deepest tile.
+TilePlan outputs_plan(int64_t M, int64_t N, int64_t O, int64_t P) {
+    TilePlan best{TILE_SMALL, 1, 0, 0, 0, 1e30};
+    constexpr int k = TILE_SMALL;
+    const int64_t nt_x = StepShape<STEP_DX>::depth(M, N, O, P), nt_w = StepShape<STEP_DD>::depth(M, N, O, P);
+    const int64_t slots = kTileKinds[k].slots, tx = step_tiles<STEP_DX>(k, M, N, O, P);
+    const int64_t tw = step_tiles<STEP_DGU>(k, M, N, O, P) + step_tiles<STEP_DD>(k, M, N, O, P);
+    for (int64_t s = 1; s <= 16 && s <= nt_x; ++s) {
+        const int64_t depth = (nt_x + s - 1) / s;
+        if ((nt_x + depth - 1) / depth != s || (s > 1 && tx * s > slots)) continue;
+        const double all = (double)(tx * s * depth + tw * nt_w) / (double)slots * tile_us(k, slots, 2);
+        const double deep = (double)depth * tile_us(k, tx * s + tw, 0) + (s > 1 ? join_us(k, M, tx, s) : 0.0);
+        const double more = (double)(tx * s + tw) / (double)slots - 1.0;   // rounds: each its way in and out
+        const double t = kLaunchUs + (more > 0.0 ? 2.0 * more : 0.0) + (all > deep ? all : deep);
+        if (t < best.us) {
+            best.us = t;
+            best.splits = (int)s;
+            best.full = s == 1 ? tx : 0;
+            best.part_floats = s > 1 ? tx * s * (int64_t)kTileKinds[k].ti * kTileKinds[k].tj : 0;
+            best.counters = s > 1 ? tx : 0;
+        }
+    }
+    return best;
+}
+bool outputs_together(const TilePlan& together, int64_t M, int64_t N, int64_t O, int64_t P) {
+    return together.us < StepShape<STEP_DX>::plan(M, N, O, P).us + StepShape<STEP_DGU>::plan(M, N, O, P).us +
+                             StepShape<STEP_DD>::plan(M, N, O, P).us;
+}
+
+template <bool kGradF32>
+hipError_t launch_outputs(SwigluBackwardArgs g, const TilePlan& plan, hipStream_t stream) {
+    const int64_t M = g.M, N = g.N, O = g.O, P = g.P;
+    g.splits = plan.splits;
+    g.full = plan.full;
+    const int64_t grid_x = tile_grid(step_tiles<STEP_DX>(plan.tile, M, N, O, P), plan.full, plan.splits);
+    const int64_t gu = step_tiles<STEP_DGU>(plan.tile, M, N, O, P), dd = step_tiles<STEP_DD>(plan.tile, M, N, O, P);
+    const int64_t grid_gu = tile_grid(gu, gu, 1), grid_dd = tile_grid(dd, dd, 1);
+    g.from[0] = 0;
+    g.from[1] = (uint32_t)grid_x;
+    g.from[2] = (uint32_t)(grid_x + grid_gu);
+    const int64_t at = grid_x + grid_gu + grid_dd;
+    static std::atomic<bool> lds_set[kMaxDevices] = {};
+    return launch_kernel<TileSmall>(swiglu_backward_outputs_kernel<TileSmall, kGradF32>, lds_set, g, at, stream);
 }
 
 template <bool kGradF32>
@@ -231,17 +312,19 @@ hipError_t launch_all(const SwigluBackwardArgs& g, int64_t counters, hipStream_t
     }
     if ((e = launch_step<STEP_DH, false>(first, stream)) != hipSuccess) return e;
     if ((e = launch_step<STEP_GATED, false>(g, stream)) != hipSuccess) return e;
+    const TilePlan together = outputs_plan(g.M, g.N, g.O, g.P);
+    if (outputs_together(together, g.M, g.N, g.O, g.P)) return launch_outputs<kGradF32>(g, together, stream);
     if ((e = launch_step<STEP_DX, false>(g, stream)) != hipSuccess) return e;
     if ((e = launch_step<STEP_DGU, kGradF32>(g, stream)) != hipSuccess) return e;
     return launch_step<STEP_DD, kGradF32>(g, stream);
 }
 
-// What the five steps' joins need at most: they run one after the other.
+// What the steps' joins need at most: they run one after the other.
 TilePlan join_need(int64_t M, int64_t N, int64_t O, int64_t P) {
-    TilePlan most{0, 1, 0, 0, 0};
+    TilePlan most{0, 1, 0, 0, 0, 0.0};
     const TilePlan plans[] = {StepShape<STEP_DH>::plan(M, N, O, P), StepShape<STEP_GATED>::plan(M, N, O, P),
                               StepShape<STEP_DX>::plan(M, N, O, P), StepShape<STEP_DGU>::plan(M, N, O, P),
-                              StepShape<STEP_DD>::plan(M, N, O, P)};
+                              StepShape<STEP_DD>::plan(M, N, O, P), outputs_plan(M, N, O, P)};
     for (const TilePlan& p : plans) {
         if (p.part_floats > most.part_floats) most.part_floats = p.part_floats;
         if (p.counters > most.counters) most.counters = p.counters;
@@ -259,7 +342,7 @@ SwigluBackwardLayout swiglu_backward_layout(int64_t M, int64_t N, int64_t O, int
         off += (bytes + 255) / 256 * 256;
         return at;
     };
-    const TilePlan join = M > 0 ? join_need(M, N, O, P) : TilePlan{0, 1, 0, 0, 0};
+    const TilePlan join = M > 0 ? join_need(M, N, O, P) : TilePlan{0, 1, 0, 0, 0, 0.0};
     L.dH = take(sizeof(float) * M * O);
     L.H = take(sizeof(uint16_t) * M * O);
     L.dAB = take(sizeof(uint16_t) * M * 2 * O);
@@ -294,6 +377,7 @@ hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream
     g.splits = 1;
     g.full = 0;
     g.clear = 0;
+    for (uint32_t& w : g.from) w = 0;
     return io.grad_f32 ? launch_all<true>(g, L.counters, stream) : launch_all<false>(g, L.counters, stream);
 }
 

@@ -508,7 +508,9 @@ template <bool kTri>
 __device__ __forceinline__ bool tile_place(uint32_t w, uint32_t nI, uint32_t nJ, uint32_t full,
                                            uint32_t splits, TilePlace* at) {
     constexpr uint32_t G = 8;
-    const uint32_t tiles = kTri ? nI * (nI + 1) / 2 : nI * nJ, grid = (full + 7) / 8 * 8;
+    const uint32_t tiles = kTri ? nI * (nI + 1) / 2 : nI * nJ;
+    if (full > tiles) full = tiles;
+    const uint32_t grid = (full + 7) / 8 * 8;
     const bool part = w >= grid;
     if (part) w -= grid;
     const uint32_t n = part ? (tiles - full) * splits : full, per = (n + 7) / 8;
@@ -639,54 +641,63 @@ struct TilePlan {
     int tile, splits;
     int64_t full;                    // of one matrix's tiles: those that are not split
     int64_t part_floats, counters;   // workspace of the join (0 without splits)
+    double us;                       // estimated time
 };
 
-// The plan with the least estimated time, in microseconds, for an I x J output (J
-// in the tile's terms: `share` operand columns of a tile belong to one output
-// column) of `nt` k-tiles, `batch` times.  Measured on 256 CUs, k-contiguous bf16,
-// per k-tile with few and with all CUs at work: large 0.95 to 1.4, mid 0.54 to
-// 0.87, small 0.43 to 0.55 alone on a CU and 0.6 to 0.95 two on one; beside them a
-// launch takes about 4.5.  A join costs (large) 5.5 + 2.7 a split, (mid) 3 + 1.35,
-// (small) 2 + 1 -- the last workgroup reads every split's sums alone, at about 0.1
-// MB/us -- and 0.2 per MB that all tiles' splits write, less where few of a tile's
-// rows are wanted.
-inline TilePlan tile_plan(int64_t I, int64_t J, int share, int64_t nt, int64_t batch, bool tri) {
-    struct Kind { int ti, tj, slots; double join, join_split; };
-    const Kind kinds[3] = {{256, 256, 256, 5.5, 2.7}, {256, 128, 256, 3.0, 1.35}, {128, 128, 512, 2.0, 1.0}};
-    TilePlan best{TILE_LARGE, 1, 0, 0, 0};
-    double best_t = 1e30;
+// Measured on 256 CUs, k-contiguous bf16, in microseconds: per k-tile with few and
+// with all CUs at work (large 0.95 to 1.4, mid 0.54 to 0.87, small 0.43 to 0.55
+// alone on a CU and 0.6 to 0.95 two on one); beside them a launch takes about 4.5.  A
+// join costs (large) 5.5 + 2.7 a split, (mid) 3 + 1.35, (small) 2 + 1 -- the last
+// workgroup reads every split's sums alone, at about 0.1 MB/us -- and 0.2 per MB that
+// all tiles' splits write, less where few of a tile's rows are wanted.
+struct TileKind {
+    int ti, tj, slots;
+    double join, join_split;
+};
+constexpr TileKind kTileKinds[3] = {{256, 256, 256, 5.5, 2.7}, {256, 128, 256, 3.0, 1.35}, {128, 128, 512, 2.0, 1.0}};
+constexpr double kLaunchUs = 4.5;
+// per k-tile, with `units` workgroups at work and `strided` k-strided operands (whose
+// reads are twice as many instructions: the mid tile's short phases do not hide them)
+inline double tile_us(int kind, int64_t units, int strided) {
+    const double slots = kTileKinds[kind].slots, busy = (double)units < slots ? (double)units / slots : 1.0;
+    return kind == TILE_LARGE ? 0.95 + 0.45 * busy
+           : kind == TILE_MID ? (0.54 + 0.33 * busy) * (1.0 + 0.13 * strided)
+           : busy <= 0.5      ? 0.43 + 0.24 * busy
+                              : 0.6 + 0.35 * busy;
+}
+inline int64_t tile_tiles(int kind, int64_t I, int64_t J, int share, bool tri) {
+    const int64_t wi = kTileKinds[kind].ti, wj = kTileKinds[kind].tj / share;
+    return tile_count((I + wi - 1) / wi, (J + wj - 1) / wj, tri);
+}
+inline double join_us(int kind, int64_t I, int64_t tiles, int64_t s) {
+    const TileKind& k = kTileKinds[kind];
+    const double rows = I < k.ti ? (double)((I + 15) / 16 * 16) / k.ti : 1.0;
+    return k.join + rows * ((double)s * k.join_split + 0.2 * (double)(tiles * s) * k.ti * k.tj * 4e-6);
+}
+
+// The plan with the least estimated time for an I x J output (J in the tile's terms:
+// `share` operand columns of a tile belong to one output column) of `nt` k-tiles,
+// `batch` times.
+inline TilePlan tile_plan(int64_t I, int64_t J, int share, int64_t nt, int64_t batch, bool tri,
+                          int strided) {
+    TilePlan best{TILE_LARGE, 1, 0, 0, 0, 1e30};
     for (int k = 0; k < 3; ++k) {
-        if (tri && kinds[k].ti != kinds[k].tj) continue;
-        const int64_t wj = kinds[k].tj / share, slots = kinds[k].slots;
-        const int64_t each = tile_count((I + kinds[k].ti - 1) / kinds[k].ti, (J + wj - 1) / wj, tri);
-        const int64_t tiles = batch * each;
-        const double rows = I < kinds[k].ti ? (double)((I + 15) / 16 * 16) / kinds[k].ti : 1.0;
-        // per k-tile with `units` workgroups at work
-        auto per = [&](int64_t units) {
-            const double busy = units < slots ? (double)units / (double)slots : 1.0;
-            return k == TILE_LARGE ? 0.95 + 0.45 * busy
-                   : k == TILE_MID ? 0.54 + 0.33 * busy
-                   : busy <= 0.5   ? 0.43 + 0.24 * busy
-                                   : 0.6 + 0.35 * busy;
-        };
+        if (tri && kTileKinds[k].ti != kTileKinds[k].tj) continue;
+        const int64_t slots = kTileKinds[k].slots, each = tile_tiles(k, I, J, share, tri), tiles = batch * each;
         for (int64_t s = 1; s <= 16 && s <= nt; ++s) {
             const int64_t depth = (nt + s - 1) / s;
             if ((nt + depth - 1) / depth != s) continue;   // an empty last split
             // whole rounds of the CUs stay unsplit; what is split is one round at most
             const int64_t full = s == 1 ? tiles : tiles / slots * slots, rest = tiles - full;
             if (s > 1 && (rest == 0 || rest * s > slots || (full && batch > 1))) continue;
-            double t = 4.5 + (double)((full + slots - 1) / slots * nt) * per(full);
-            if (s > 1) {
-                const double mb = (double)(rest * s) * kinds[k].ti * kinds[k].tj * 4e-6;
-                t += (double)depth * per(rest * s) + kinds[k].join +
-                     rows * ((double)s * kinds[k].join_split + 0.2 * mb);
-            }
-            if (t < best_t) {
-                best_t = t;
+            double t = kLaunchUs + (double)((full + slots - 1) / slots * nt) * tile_us(k, full, strided);
+            if (s > 1) t += (double)depth * tile_us(k, rest * s, strided) + join_us(k, I, rest, s);
+            if (t < best.us) {
+                best.us = t;
                 best.tile = k;
                 best.splits = (int)s;
                 best.full = s == 1 ? each : full;
-                best.part_floats = s > 1 ? rest * s * (int64_t)kinds[k].ti * kinds[k].tj : 0;
+                best.part_floats = s > 1 ? rest * s * (int64_t)kTileKinds[k].ti * kTileKinds[k].tj : 0;
                 best.counters = s > 1 ? rest : 0;
             }
         }

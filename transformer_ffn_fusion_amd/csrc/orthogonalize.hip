@@ -329,8 +329,9 @@ hipError_t launch_product_cfg(const OrthoArgs& g, int64_t batch, hipStream_t str
 template <int kProd>
 TilePlan product_plan(int64_t B, int64_t R, int64_t C) {
     const int64_t m = R < C ? R : C, K = kProd == PROD_SYM ? (R < C ? C : R) : m;
+    const int strided = kProd == PROD_SYM ? (R > C ? 2 : 0) : kProd == PROD_X && R <= C ? 1 : 0;
     return tile_plan(kProd == PROD_X ? R : m, kProd == PROD_X ? C : m, 1, (K + kTileK - 1) / kTileK,
-                     B, kProd != PROD_X);
+                     B, kProd != PROD_X, strided);
 }
 
 template <int kProd, bool kTall>
