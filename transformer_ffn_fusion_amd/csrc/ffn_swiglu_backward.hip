@@ -268,8 +268,10 @@ TilePlan outputs_plan(int64_t M, int64_t N, int64_t O, int64_t P) {
         if ((nt_x + depth - 1) / depth != s || (s > 1 && tx * s > slots)) continue;
         const double all = (double)(tx * s * depth + tw * nt_w) / (double)slots * tile_us(k, slots, 2);
         const double deep = (double)depth * tile_us(k, tx * s + tw, 0) + (s > 1 ? join_us(k, M, tx, s) : 0.0);
-        const double more = (double)(tx * s + tw) / (double)slots - 1.0;   // rounds: each its way in and out
-        const double t = kLaunchUs + (more > 0.0 ? 2.0 * more : 0.0) + (all > deep ? all : deep);
+        // further rounds pay their way in and out too (tiles of one k-tile hardly)
+        const double more = (double)(tx * s + tw) / (double)slots - 1.0;
+        const double way = nt_w < 12 ? 2.0 + 0.2 * (double)nt_w : kLaunchUs;
+        const double t = kLaunchUs + (more > 0.0 ? way * more : 0.0) + (all > deep ? all : deep);
         if (t < best.us) {
             best.us = t;
             best.splits = (int)s;
