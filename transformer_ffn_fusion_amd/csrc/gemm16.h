@@ -105,6 +105,7 @@ __device__ __forceinline__ void tile_dma(uint64_t base, bool any, uint32_t off, 
     srd.w = kRsrcWord3;
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"   // a wait state between writing M0 and a load to LDS
         "buffer_load_dwordx4 %1, %2, 0 offen lds"
         :
         : "s"(lds), "v"(off), "s"(srd)
