@@ -34,6 +34,12 @@
 //    p + 2.  A wave issues in p + 2 after the barrier that ends its p + 1; by
 //    then the other group has passed the one that ends its p, and every wave
 //    waits for its LDS reads (lgkmcnt 0) before that one.
+//
+// Bound: of a 256 x 256 tile's k-tile the matrix instructions take 2048 clocks
+// and so do the LDS reads (1536) and the loads' writes (512) at 128 B per clock;
+// 2235 measured.  8192 x 8192 x 8192 bf16: 729 us, 1500 TFLOP/s at the 1.9 GHz
+// that the card holds under this load.
+//
 // K past its end reads zeros in both operands (a k-strided operand through the
 // resource's exact size, a k-contiguous one through an offset out of range), so
 // values behind the end of a row never meet a product; indices past I or J read
