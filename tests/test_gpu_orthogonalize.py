@@ -40,6 +40,53 @@ def test_shapes(shape, dtype):
     ref.check_orthogonalize(run(G), G, 5, str(shape))
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("shape", [
+    (8, 512), (512, 8), (16, 32), (40, 96), (96, 40), (104, 456), (456, 104), (128, 128), (512, 128),
+    (128, 504), (504, 120), (128, 520), (520, 128), (136, 512), (512, 136),
+])
+def test_one_workgroup_shapes_and_just_beyond(shape, dtype):
+    import torch
+    print(f"case orthogonalize {shape} {dtype}", flush=True)
+    G = gradient(*shape, seed=sum(shape) + 1).to(getattr(torch, dtype)).cuda()
+    ref.check_orthogonalize(run(G), G, 5, str(shape))
+
+
+@pytest.mark.parametrize("steps", [1, 2, 6])
+@pytest.mark.parametrize("shape", [(72, 200), (200, 72)])
+def test_one_workgroup_steps(shape, steps):
+    G = gradient(*shape, seed=steps).cuda()
+    ref.check_orthogonalize(run(G, steps), G, steps, f"{shape} {steps} steps")
+
+
+@pytest.mark.parametrize("kind", ["rank 1", "rank 16", "orthogonal", "one large direction", "huge"])
+def test_one_workgroup_spectra(kind):
+    import torch
+    R, C = 120, 328
+    if kind == "rank 1":
+        G = gradient(R, C, 13, rank=1)
+    elif kind == "rank 16":
+        G = gradient(R, C, 14, rank=16)
+    elif kind == "orthogonal":
+        G = torch.linalg.qr(torch.randn(C, R, generator=torch.Generator().manual_seed(15)))[0].t().contiguous()
+    elif kind == "one large direction":
+        G = gradient(R, C, 16) + 100 * gradient(R, C, 17, rank=1)
+    else:
+        G = gradient(R, C, 18) * 1e30   # squares leave fp32's range
+    G = G.cuda()
+    ref.check_orthogonalize(run(G), G, 5, kind)
+
+
+def test_one_workgroup_large_stack():
+    import torch
+    G = torch.stack([gradient(72, 40, s) * 10.0 ** (s % 7 - 3) for s in range(20)]).cuda()
+    G = G.repeat(40, 1, 1)   # 800 matrices, more than the CUs
+    U = run(G)
+    assert torch.equal(U, U[:20].repeat(40, 1, 1))
+    for e in range(20):
+        ref.check_orthogonalize(U[e], G[e], 5, f"matrix {e}")
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 6])
 def test_steps(steps):
     G = gradient(136, 264, seed=steps).cuda()

@@ -40,7 +40,11 @@ namespace {
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr double kNsEps = 1e-7;
 constexpr float kScaleX = 64.0f, kScaleSym = 1024.0f;
-constexpr int kNormBlocks = 128;   // partial sums of squares per matrix
+// Partial sums of squares per matrix (3584 x 8192 fp32: 128 of them 60 us, 1024 NORM us).
+inline int norm_blocks(int64_t size) {
+    const int64_t k = size / 8192;
+    return k < 32 ? 32 : k > 1024 ? 1024 : (int)k;
+}
 
 struct OrthoArgs {
     const void* G;
@@ -50,7 +54,8 @@ struct OrthoArgs {
     uint16_t* lo;           // X's low halves, read and written in place
     uint16_t *sym, *poly;   // off-diagonals of A and b A + c A^2, fp16, m x m
     float *diag, *scale;    // diagonals of A and of b A + c A^2
-    double* norm;           // kNormBlocks partial sums per matrix
+    double* norm;           // norm_blocks partial sums per matrix
+    int sums;
     float* part;            // sums of split products, and a counter per tile (tile_join)
     uint32_t* count;
     int64_t counters;
@@ -73,6 +78,15 @@ __device__ __forceinline__ void unpack8_f16(const uint4& w, float (&v)[8]) {
         v[2 * r] = f16_bits(u[r] & 0xffffu);
         v[2 * r + 1] = f16_bits(u[r] >> 16);
     }
+}
+__device__ __forceinline__ uint2 f16x4(const float (&v)[4]) {
+    return make_uint2(bits_f16(v[0]) | bits_f16(v[1]) << 16, bits_f16(v[2]) | bits_f16(v[3]) << 16);
+}
+__device__ __forceinline__ void f32x4(const uint2& w, float (&v)[4]) {
+    v[0] = f16_bits(w.x & 0xffffu);
+    v[1] = f16_bits(w.x >> 16);
+    v[2] = f16_bits(w.y & 0xffffu);
+    v[3] = f16_bits(w.y >> 16);
 }
 __device__ __forceinline__ void store8_f16(uint16_t* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(p) =
@@ -105,6 +119,15 @@ __device__ __forceinline__ void load8_in(const void* p, int64_t at, float (&v)[8
     }
 }
 
+// Sum over the 256 threads, the same in all of them.
+__device__ __forceinline__ double workgroup_sum(double q, double (&s)[4]) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) q += __shfl_xor(q, d);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = q;
+    __syncthreads();
+    return s[0] + s[1] + s[2] + s[3];
+}
+
 // Sums of squares in fp64: an fp32 gradient's squares leave fp32's range.
 template <bool kF32>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs g) {
@@ -113,27 +136,24 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs g) {
     if (blockIdx.x == 0 && blockIdx.y == 0)   // before any product of this call
         for (int64_t k = threadIdx.x; k < g.counters; k += 256) g.count[k] = 0;
     double q = 0.0;
-    for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; k < size; k += kNormBlocks * 2048) {
+#pragma unroll 4
+    for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; k < size; k += (int64_t)g.sums * 2048) {
         float v[8];
         load8_in<kF32>(g.G, base + k, v);
 #pragma unroll
         for (int r = 0; r < 8; ++r) q += (double)v[r] * v[r];
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) q += __shfl_xor(q, d);
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = q;
-    __syncthreads();
-    if (threadIdx.x == 0) g.norm[blockIdx.y * kNormBlocks + blockIdx.x] = s[0] + s[1] + s[2] + s[3];
+    q = workgroup_sum(q, s);
+    if (threadIdx.x == 0) g.norm[(int64_t)blockIdx.y * g.sums + blockIdx.x] = q;
 }
 
 // X = 64 G / (||G|| + eps) as hi + lo.
 template <bool kF32>
 __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoArgs g) {
-    __shared__ double s[kNormBlocks];
-    if (threadIdx.x < kNormBlocks) s[threadIdx.x] = g.norm[blockIdx.y * kNormBlocks + threadIdx.x];
-    __syncthreads();
+    __shared__ double s[4];
     double q = 0.0;
-    for (int k = 0; k < kNormBlocks; ++k) q += s[k];
+    for (int k = threadIdx.x; k < g.sums; k += 256) q += g.norm[(int64_t)blockIdx.y * g.sums + k];
+    q = workgroup_sum(q, s);
     const double by = (double)kScaleX / (sqrt(q) + kNsEps);
     const int64_t size = g.R * g.C, base = (int64_t)blockIdx.y * size;
     for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; k < size;
@@ -345,13 +365,309 @@ hipError_t launch_product(OrthoArgs g, int64_t batch, hipStream_t stream) {
     return launch_product_cfg<TileSmall, kProd, kTall>(g, batch, stream);
 }
 
+// A matrix of at most 128 x 512 (either way round), all steps in one workgroup.  Eight
+// waves own 64 columns of X each (n, the larger dimension, runs over the columns: for a
+// tall G they are its rows) and hold them, hi and lo, in registers as operands of the X
+// product: a lane has column l % 16 of each 16 and, for its group g = l / 16 and each
+// 32 rows, rows 4 g to 4 g + 3 and 16 more -- what the product leaves it with, and as
+// good an order of the contraction as any if P is stored in it as well.  The sum over the
+// columns needs hi the other way round: through LDS, transposed, read by the transposing
+// reads; A and the polynomial then lie where it was.
+//
+// Bound: LDS reads (per step 768 KB for A, 512 KB for X, 128 B a clock) and the matrix
+// instructions behind them.  SMALL_FIGURES
+constexpr int kSmallM = 128, kSmallN = 512, kSmallThreads = 512;
+constexpr int kSquareLd = 2 * kSmallM + 16;   // bytes of a row of A or the polynomial: no conflicts
+constexpr int kSquare = kSmallM * kSquareLd;
+constexpr int kSmallX = 2 * kSmallM * kSmallN;
+constexpr int kSmallLds = kSmallX + 2 * 4 * kSmallM + 64;
+
+inline bool ortho_small(int64_t R, int64_t C) {
+    return (R < C ? R : C) <= kSmallM && (R < C ? C : R) <= kSmallN;
+}
+
+// Where LDS holds X's rows 16 t + 4 c to + 3 of column n.  The 16 rows of t go to one of
+// eight places by n, so that the four columns that each half-wave of a transposing read
+// takes from two groups of eight lie on all banks; the last term does it for the writes.
+__device__ __forceinline__ int small_x_at(int n, int t, int c) {
+    return n * (2 * kSmallM) + ((t ^ ((n & 3) | (n >> 1 & 4))) << 5) + ((c ^ (n >> 1 & 2)) << 3);
+}
+// ... and rows 16 t + 4 g to + 3 of column j of a square matrix.
+__device__ __forceinline__ int small_square_at(int j, int t, int g) {
+    return j * kSquareLd + 64 * (t >> 1) + 16 * g + 8 * (t & 1);
+}
+
+template <bool kF32, bool kTall>
+__global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* G, uint16_t* U, int R,
+                                                                    int C, int steps) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    char* const square = smem;             // A's off-diagonal, after X was read
+    char* const poly = smem + kSquare;
+    float* const diag = reinterpret_cast<float*>(smem + kSmallX);
+    float* const scale = diag + kSmallM;
+    double* const sums = reinterpret_cast<double*>(scale + kSmallM);
+    const int m = kTall ? C : R, n = kTall ? R : C;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int li = lane & 15, g = lane >> 4;
+    const int64_t base = (int64_t)blockIdx.x * R * C;
+    const int col0 = 64 * wave;            // this wave's columns
+
+    // X(i, j) is element i * row + j * col of the matrix; four rows from i at a time
+    auto load4 = [&](int i, int j, float (&v)[4]) {
+        const int64_t at = base + (kTall ? (int64_t)j * C + i : (int64_t)i * C + j);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = 0.f;
+        if (i >= m || j >= n) return;      // (m and n are multiples of 8)
+        if constexpr (kF32) {
+            const float* p = static_cast<const float*>(G) + at;
+            if constexpr (kTall) {
+                const float4 w = *reinterpret_cast<const float4*>(p);
+                v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = p[(int64_t)r * C];
+            }
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(G) + at;
+            if constexpr (kTall) {
+                const uint2 w = *reinterpret_cast<const uint2*>(p);
+                v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = bf16_lo(p[(int64_t)r * C]);
+            }
+        }
+    };
+    auto store4 = [&](int i, int j, const float (&v)[4]) {
+        if (i >= m || j >= n) return;
+        uint16_t* p = U + base + (kTall ? (int64_t)j * C + i : (int64_t)i * C + j);
+        const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+        if constexpr (kTall) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+        } else {
+            p[0] = (uint16_t)a;
+            p[C] = (uint16_t)(a >> 16);
+            p[2 * (int64_t)C] = (uint16_t)b;
+            p[3 * (int64_t)C] = (uint16_t)(b >> 16);
+        }
+    };
+
+    // [16 columns][16 rows]: rows 4 g to 4 g + 3 of them
+    uint2 hi[4][8], lo[4][8];
+    auto split4 = [&](int c, int t, const float (&v)[4]) {
+        float l[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) l[r] = v[r] - (float)(_Float16)v[r];
+        hi[c][t] = f16x4(v);
+        lo[c][t] = f16x4(l);
+    };
+    auto put_x = [&]() {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                *reinterpret_cast<uint2*>(smem + (col0 + 16 * c) * (2 * kSmallM) + small_x_at(li, t, g)) = hi[c][t];
+    };
+
+    {   // X = 64 G / (||G|| + eps)
+        float v[4][8][4];
+        double q = 0.0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) load4(16 * t + 4 * g, col0 + 16 * c + li, v[c][t]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) q += (double)v[c][t][r] * v[c][t][r];
+#pragma unroll
+        for (int d = 32; d; d >>= 1) q += __shfl_xor(q, d);
+        if (lane == 0) sums[wave] = q;
+        __syncthreads();
+        q = 0.0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) q += sums[w];
+        const double by = (double)kScaleX / (sqrt(q) + kNsEps);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    asm volatile("" : "+v"(v[c][t][r]));   // (not 128 doubles from above)
+                    v[c][t][r] = (float)((double)v[c][t][r] * by);
+                }
+                split4(c, t, v[c][t]);
+            }
+    }
+
+    // the square products: rows 64 (wave / 4) and columns 32 (wave % 4) of the output
+    const int ti = 4 * (wave >> 2), tj = 2 * (wave & 3);
+    for (int step = 0; step < steps; ++step) {
+        asm volatile("" : "+v"(li), "+v"(g));   // (addresses anew in each step: no room to keep them)
+        if (step) __syncthreads();   // the polynomial is read
+        put_x();
+        __syncthreads();   // X is written
+        floatx4_t acc[4][2];
+        auto clear = [&]() {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) acc[x][y] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        };
+        auto multiply = [&](const uint4 (&a)[4], const uint4 (&b)[2]) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) acc[x][y] = mfma16<true>(a[x], b[y], acc[x][y]);
+        };
+        clear();
+        {   // A = X X^T, 32 columns of X at a time
+            const int row = 8 * g + (li >> 2), q = li & 3;
+            auto frag = [&](int k, int t) {
+                const uint2 a = lds_read_tr16(smem + 64 * kSmallM * k + small_x_at(row, t, q));
+                const uint2 b = lds_read_tr16(smem + 64 * kSmallM * k + small_x_at(row + 4, t, q));
+                return make_uint4(a.x, a.y, b.x, b.y);
+            };
+            for (int k = 0; 32 * k < n; ++k) {
+                uint4 a[4], b[2];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) a[x] = frag(k, ti + x);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) b[y] = frag(k, tj + y);
+                multiply(a, b);
+            }
+        }
+        __syncthreads();   // X is read
+        // each lane has rows 16 (ti + x) + 4 g to + 3 of column 16 (tj + y) + li
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int j = 16 * (tj + y) + li;
+                const bool on = ti + x == tj + y && g == li >> 2;   // row 4 g + li % 4 is j
+                float v[4], own = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool here = on && r == (li & 3);
+                    own = here ? acc[x][y][r] : own;
+                    v[r] = here ? 0.f : acc[x][y][r] * (kScaleSym / (kScaleX * kScaleX));
+                }
+                if (on) diag[j] = own * (1.0f / (kScaleX * kScaleX));
+                *reinterpret_cast<uint2*>(square + small_square_at(j, ti + x, g)) = f16x4(v);
+            }
+        __syncthreads();   // A is written
+        clear();
+        for (int k = 0; k < 4; ++k) {
+            uint4 a[4], b[2];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                a[x] = ld16(square + (16 * (ti + x) + li) * kSquareLd + 64 * k + 16 * g);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                b[y] = ld16(square + (16 * (tj + y) + li) * kSquareLd + 64 * k + 16 * g);
+            multiply(a, b);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int j = 16 * (tj + y) + li;
+            const float fj = kNsB + kNsC * diag[j];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int at = small_square_at(j, ti + x, g);
+                const bool on = ti + x == tj + y && g == li >> 2;
+                const uint2 e = *reinterpret_cast<const uint2*>(square + at);
+                float o[4];
+                f32x4(e, o);
+                const float4 d4 = *reinterpret_cast<const float4*>(diag + 16 * (ti + x) + 4 * g);
+                const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+                float v[4], own = 0.f, dj = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {   // as PROD_POLY
+                    const bool here = on && r == (li & 3);
+                    own = here ? acc[x][y][r] : own;
+                    dj = here ? d[r] : dj;
+                    v[r] = here ? 0.f : acc[x][y][r] * (kNsC / kScaleSym) + o[r] * (fj + kNsC * d[r]);
+                }
+                if (on) scale[j] = kNsB * dj + kNsC * (own * (1.0f / (kScaleSym * kScaleSym)) + dj * dj);
+                *reinterpret_cast<uint2*>(poly + at) = f16x4(v);
+            }
+        }
+        __syncthreads();   // the polynomial is written
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // 32 columns at a time
+            floatx4_t out[8][2];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) out[t][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const uint4 p = ld16(poly + (16 * t + li) * kSquareLd + 64 * k + 16 * g);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint2 w0 = hi[2 * h + c][2 * k], w1 = hi[2 * h + c][2 * k + 1];
+                        out[t][c] = mfma16<true>(p, make_uint4(w0.x, w0.y, w1.x, w1.y), out[t][c]);
+                    }
+                }
+            tile_fence();   // (one half's sums at a time)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float4 s4 = *reinterpret_cast<const float4*>(scale + 16 * t + 4 * g);
+                const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v[4], x[4], l[4];
+                    f32x4(hi[2 * h + c][t], x);
+                    f32x4(lo[2 * h + c][t], l);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)   // as PROD_X
+                        v[r] = out[t][c][r] * (1.0f / kScaleSym) + (kNsA + s[r]) * x[r] + kNsA * l[r];
+                    split4(2 * h + c, t, v);
+                }
+                tile_fence();
+            }
+        }
+    }
+    // the pair's 22 bits as bf16
+    asm volatile("" : "+v"(li), "+v"(g));
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            float v[4], l[4];
+            f32x4(hi[c][t], v);
+            f32x4(lo[c][t], l);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = (v[r] + l[r]) * (1.0f / kScaleX);
+            store4(16 * t + 4 * g, col0 + 16 * c + li, v);
+        }
+}
+
+template <bool kF32, bool kTall>
+hipError_t launch_small(const void* G, uint16_t* U, int64_t B, int64_t R, int64_t C, int steps,
+                        hipStream_t stream) {
+    auto kern = ortho_small_kernel<kF32, kTall>;
+    static std::atomic<bool> lds_set[kMaxDevices] = {};
+    const hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(kern), kSmallLds, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)B), dim3(kSmallThreads), kSmallLds, stream, G, U, (int)R,
+                       (int)C, steps);
+    return hipGetLastError();
+}
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
 OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C) {
-    OrthogonalizeLayout L;
+    OrthogonalizeLayout L{};
     const int64_t m = R < C ? R : C;
+    if (ortho_small(R, C)) return L;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -365,7 +681,7 @@ OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C) {
     L.poly = take(sizeof(uint16_t) * B * m * m);
     L.diag = take(sizeof(float) * B * m);
     L.scale = take(sizeof(float) * B * m);
-    L.norm = take(sizeof(double) * B * kNormBlocks);
+    L.norm = take(sizeof(double) * B * norm_blocks(R * C));
     const TilePlan plans[] = {product_plan<PROD_SYM>(B, R, C), product_plan<PROD_POLY>(B, R, C),
                               product_plan<PROD_X>(B, R, C)};
     int64_t part = 0;
@@ -382,6 +698,11 @@ OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C) {
 
 hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B, int64_t R,
                                 int64_t C, int steps, char* ws, hipStream_t stream) {
+    if (ortho_small(R, C))
+        return f32 ? R > C ? launch_small<true, true>(G, U, B, R, C, steps, stream)
+                           : launch_small<true, false>(G, U, B, R, C, steps, stream)
+               : R > C ? launch_small<false, true>(G, U, B, R, C, steps, stream)
+                       : launch_small<false, false>(G, U, B, R, C, steps, stream);
     const OrthogonalizeLayout L = orthogonalize_layout(B, R, C);
     OrthoArgs g;
     g.G = G;
@@ -407,13 +728,14 @@ hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B,
     g.hi = hi[1];
     g.hi_next = hi[0];
     hipError_t e;
-    int64_t blocks = (R * C + 2047) / 2048;
-    if (blocks > 2048) blocks = 2048;
+    g.sums = norm_blocks(R * C);
+    int64_t blocks = (R * C + 2047) / 2048, most = 2048 / B;   // a round of workgroups
+    if (blocks > most) blocks = most < 1 ? 1 : most;
     if (f32) {
-        hipLaunchKernelGGL(ortho_norm_kernel<true>, dim3(kNormBlocks, (unsigned)B), dim3(256), 0, stream, g);
+        hipLaunchKernelGGL(ortho_norm_kernel<true>, dim3((unsigned)g.sums, (unsigned)B), dim3(256), 0, stream, g);
         hipLaunchKernelGGL(ortho_start_kernel<true>, dim3((unsigned)blocks, (unsigned)B), dim3(256), 0, stream, g);
     } else {
-        hipLaunchKernelGGL(ortho_norm_kernel<false>, dim3(kNormBlocks, (unsigned)B), dim3(256), 0, stream, g);
+        hipLaunchKernelGGL(ortho_norm_kernel<false>, dim3((unsigned)g.sums, (unsigned)B), dim3(256), 0, stream, g);
         hipLaunchKernelGGL(ortho_start_kernel<false>, dim3((unsigned)blocks, (unsigned)B), dim3(256), 0, stream, g);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
