@@ -28,7 +28,8 @@
 // polynomial's off-diagonal times 1024 (singular values stay below 1.21, so
 // entries stay below 80 and 1.2e4).
 //
-// Bound: the three products of a step, gemm16.h.
+// Bound: the three products of a step, gemm16.h; up to 128 x 512 one workgroup does all
+// (ortho_small_kernel).
 #include "ffn_device.h"
 #include "ffn_internal.h"
 #include "gemm16.h"
@@ -40,7 +41,7 @@ namespace {
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr double kNsEps = 1e-7;
 constexpr float kScaleX = 64.0f, kScaleSym = 1024.0f;
-// Partial sums of squares per matrix (3584 x 8192 fp32: 128 of them 60 us, 1024 NORM us).
+// Partial sums of squares per matrix (3584 x 8192 fp32: 128 of them 60 us, 1024 26 us).
 inline int norm_blocks(int64_t size) {
     const int64_t k = size / 8192;
     return k < 32 ? 32 : k > 1024 ? 1024 : (int)k;
@@ -79,6 +80,7 @@ __device__ __forceinline__ void unpack8_f16(const uint4& w, float (&v)[8]) {
         v[2 * r + 1] = f16_bits(u[r] >> 16);
     }
 }
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint2 f16x4(const float (&v)[4]) {
     return make_uint2(bits_f16(v[0]) | bits_f16(v[1]) << 16, bits_f16(v[2]) | bits_f16(v[3]) << 16);
 }
@@ -147,6 +149,15 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs g) {
     if (threadIdx.x == 0) g.norm[(int64_t)blockIdx.y * g.sums + blockIdx.x] = q;
 }
 
+// v by in fp64, as fp32.  What comes of it is rounded to fp16 next; without the barrier
+// the compiler rounds the double itself, in some forty instructions (a 128 x 512 matrix
+// in one workgroup: 14 us more).
+__device__ __forceinline__ float scaled(float v, double by) {
+    float x = (float)((double)v * by);
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // X = 64 G / (||G|| + eps) as hi + lo.
 template <bool kF32>
 __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoArgs g) {
@@ -161,7 +172,7 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoArgs g) {
         float v[8];
         load8_in<kF32>(g.G, base + k, v);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = (float)((double)v[r] * by);
+        for (int r = 0; r < 8; ++r) v[r] = scaled(v[r], by);
         store8_pair(g.hi_next + base + k, g.lo + base + k, v);
     }
 }
@@ -374,8 +385,11 @@ hipError_t launch_product(OrthoArgs g, int64_t batch, hipStream_t stream) {
 // columns needs hi the other way round: through LDS, transposed, read by the transposing
 // reads; A and the polynomial then lie where it was.
 //
-// Bound: LDS reads (per step 768 KB for A, 512 KB for X, 128 B a clock) and the matrix
-// instructions behind them.  SMALL_FIGURES
+// Against the tiled products of this file (17 launches), fp32: one 128 x 512 113 -> 68 us, 256 of
+// them 777 -> 94 us, 4096 of 32 x 32 5734 -> 633 us.  Bound: one CU.  A step of 128 x 512
+// takes 11 us, about 27000 clocks: LDS reads 768 KB for A (6144 clocks at 128 B) and 512 KB
+// for X, 9200 of matrix instructions and as many of vector instructions per SIMD, six
+// barriers, and little of it at the same time.
 constexpr int kSmallM = 128, kSmallN = 512, kSmallThreads = 512;
 constexpr int kSquareLd = 2 * kSmallM + 16;   // bytes of a row of A or the polynomial: no conflicts
 constexpr int kSquare = kSmallM * kSquareLd;
@@ -453,20 +467,23 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
     };
 
     // [16 columns][16 rows]: rows 4 g to 4 g + 3 of them
-    uint2 hi[4][8], lo[4][8];
-    auto split4 = [&](int c, int t, const float (&v)[4]) {
-        float l[4];
+    f16x4_t hi[4][8], lo[4][8];
+    // ... from w = by^-1 times them: with fp16 results of fp32 multiply-adds, no separate
+    // conversions (they bound the kernel otherwise: 9 instead of 4 instructions an element)
+    auto split4 = [&](int c, int t, const float (&w)[4], float by) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) l[r] = v[r] - (float)(_Float16)v[r];
-        hi[c][t] = f16x4(v);
-        lo[c][t] = f16x4(l);
+        for (int r = 0; r < 4; ++r) {
+            hi[c][t][r] = (_Float16)__builtin_fmaf(w[r], by, -0.f);
+            lo[c][t][r] = (_Float16)__builtin_fmaf(w[r], by, -(float)hi[c][t][r]);
+        }
     };
     auto put_x = [&]() {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int t = 0; t < 8; ++t)
-                *reinterpret_cast<uint2*>(smem + (col0 + 16 * c) * (2 * kSmallM) + small_x_at(li, t, g)) = hi[c][t];
+                *reinterpret_cast<uint2*>(smem + (col0 + 16 * c) * (2 * kSmallM) + small_x_at(li, t, g)) =
+                    __builtin_bit_cast(uint2, hi[c][t]);
     };
 
     {   // X = 64 G / (||G|| + eps)
@@ -497,14 +514,15 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     asm volatile("" : "+v"(v[c][t][r]));   // (not 128 doubles from above)
-                    v[c][t][r] = (float)((double)v[c][t][r] * by);
+                    v[c][t][r] = scaled(v[c][t][r], by);
                 }
-                split4(c, t, v[c][t]);
+                split4(c, t, v[c][t], 1.f);
             }
     }
 
     // the square products: rows 64 (wave / 4) and columns 32 (wave % 4) of the output
     const int ti = 4 * (wave >> 2), tj = 2 * (wave & 3);
+    const bool square_part = 16 * ti < m && 16 * tj < m;   // else zeros
     for (int step = 0; step < steps; ++step) {
         asm volatile("" : "+v"(li), "+v"(g));   // (addresses anew in each step: no room to keep them)
         if (step) __syncthreads();   // the polynomial is read
@@ -524,7 +542,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
                 for (int y = 0; y < 2; ++y) acc[x][y] = mfma16<true>(a[x], b[y], acc[x][y]);
         };
         clear();
-        {   // A = X X^T, 32 columns of X at a time
+        if (square_part) {   // A = X X^T, 32 columns of X at a time
             const int row = 8 * g + (li >> 2), q = li & 3;
             auto frag = [&](int k, int t) {
                 const uint2 a = lds_read_tr16(smem + 64 * kSmallM * k + small_x_at(row, t, q));
@@ -560,7 +578,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
             }
         __syncthreads();   // A is written
         clear();
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < (square_part ? 4 : 0); ++k) {
             uint4 a[4], b[2];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
@@ -591,11 +609,14 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
                     dj = here ? d[r] : dj;
                     v[r] = here ? 0.f : acc[x][y][r] * (kNsC / kScaleSym) + o[r] * (fj + kNsC * d[r]);
                 }
-                if (on) scale[j] = kNsB * dj + kNsC * (own * (1.0f / (kScaleSym * kScaleSym)) + dj * dj);
+                if (on)   // with the linear term and the scale of the products that it joins
+                    scale[j] = kScaleSym * (kNsA + kNsB * dj +
+                                            kNsC * (own * (1.0f / (kScaleSym * kScaleSym)) + dj * dj));
                 *reinterpret_cast<uint2*>(poly + at) = f16x4(v);
             }
         }
         __syncthreads();   // the polynomial is written
+        if (col0 >= n) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {   // 32 columns at a time
             floatx4_t out[8][2];
@@ -604,16 +625,19 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
 #pragma unroll
                 for (int c = 0; c < 2; ++c) out[t][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const uint4 p = ld16(poly + (16 * t + li) * kSquareLd + 64 * k + 16 * g);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint2 w0 = hi[2 * h + c][2 * k], w1 = hi[2 * h + c][2 * k + 1];
+                        const uint2 w0 = __builtin_bit_cast(uint2, hi[2 * h + c][2 * k]);
+                        const uint2 w1 = __builtin_bit_cast(uint2, hi[2 * h + c][2 * k + 1]);
                         out[t][c] = mfma16<true>(p, make_uint4(w0.x, w0.y, w1.x, w1.y), out[t][c]);
                     }
+                    if (t == 3) tile_fence();   // (few operands in flight: the registers are full)
                 }
+            }
             tile_fence();   // (one half's sums at a time)
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -621,13 +645,13 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
                 const float s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float v[4], x[4], l[4];
-                    f32x4(hi[2 * h + c][t], x);
-                    f32x4(lo[2 * h + c][t], l);
+                    float v[4];
+                    const f16x4_t x = hi[2 * h + c][t], l = lo[2 * h + c][t];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)   // as PROD_X
-                        v[r] = out[t][c][r] * (1.0f / kScaleSym) + (kNsA + s[r]) * x[r] + kNsA * l[r];
-                    split4(2 * h + c, t, v);
+                    for (int r = 0; r < 4; ++r)   // as PROD_X, times kScaleSym
+                        v[r] = __builtin_fmaf((float)l[r], kScaleSym * kNsA,
+                                              __builtin_fmaf((float)x[r], s[r], out[t][c][r]));
+                    split4(2 * h + c, t, v, 1.0f / kScaleSym);
                 }
                 tile_fence();
             }
@@ -639,11 +663,9 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
     for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            float v[4], l[4];
-            f32x4(hi[c][t], v);
-            f32x4(lo[c][t], l);
+            float v[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = (v[r] + l[r]) * (1.0f / kScaleX);
+            for (int r = 0; r < 4; ++r) v[r] = ((float)hi[c][t][r] + (float)lo[c][t][r]) * (1.0f / kScaleX);
             store4(16 * t + 4 * g, col0 + 16 * c + li, v);
         }
 }
