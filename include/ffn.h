@@ -41,7 +41,9 @@
  *  - Numerics.  bf16 storage, fp32 accumulation; H is rounded to bf16 once,
  *    Y once (round to nearest even).  No floating-point atomics: repeated
  *    calls with the same inputs give bitwise-identical outputs.
- *  - Aliasing.  Outputs must not overlap any input or the workspace.
+ *  - Aliasing.  Outputs must not overlap any input or the workspace (the
+ *    training operators -- SwiGLU backward, layer norm, orthogonalised update --
+ *    refuse it with FFN_EINVAL; the layer norm may run in place, as it says).
  */
 #ifndef FFN_MI355X_H
 #define FFN_MI355X_H
@@ -270,7 +272,7 @@ int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, con
 
 /* ---------------------------------------------------------------- orthogonalised update
  * The update of a weight matrix by Newton-Schulz steps on its gradient (or
- * momentum), as the Muon optimiser takes it:
+ * momentum):
  *
  *   X = G / (||G||_F + 1e-7), then `steps` times, with A = X X^T:
  *   X <- 3.4445 X - 4.7750 A X + 2.0315 A^2 X;   U = X

@@ -119,6 +119,38 @@ def test_explicit_stream_argument():
     assert torch.equal(n, want["n"]) and torch.equal(U, want["Ug"])
 
 
+def test_explicit_stream_brings_its_own_workspace():
+    """A call on another stream than the current one, with no workspace given, while the current
+    stream is busy: the workspace is filled on the call's stream, not behind that work."""
+    import torch
+    M, N, O = 1024, 2048, 1536
+    g = torch.Generator(device="cuda").manual_seed(8)
+
+    def rand(*shape):
+        return (torch.randn(*shape, generator=g, device="cuda") / shape[-1] ** 0.5).bfloat16()
+
+    args = [rand(M, N), rand(N, O), rand(N, O), rand(O, N), rand(M, N)]
+
+    def grads():
+        return [torch.empty_like(args[k]) for k in (0, 1, 2, 3)]
+    want = grads()
+    ffn.ffn_swiglu_backward(*args, *want)
+    G = torch.randn(512, 1024, generator=g, device="cuda")
+    wantU = torch.empty(512, 1024, dtype=torch.bfloat16, device="cuda")
+    ffn.ffn_orthogonalize(G, wantU)
+    st = torch.cuda.Stream()
+    for sleep in (0, 20000, 60000, 120000, 200000, 400000):
+        got, U = grads(), torch.empty_like(wantU)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(sleep)    # (clocks; the calls take 0.1 to 0.3 ms)
+        ffn.ffn_swiglu_backward(*args, *got, stream=st.cuda_stream)
+        ffn.ffn_orthogonalize(G, U, stream=st.cuda_stream)
+        other = [torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(U, wantU), sleep
+        del other
+
+
 @pytest.mark.parametrize("shape", SHAPES)
 def test_captured_and_replayed(shape):
     """The whole step in a graph, replayed on new inputs with eager work between the replays."""

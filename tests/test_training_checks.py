@@ -174,4 +174,55 @@ def test_workspace_sizes_of_invalid_shapes_are_zero():
     assert ffn.ffn_orthogonalize_workspace_size(1, 64, 12) == 0
     # sizes grow with the shape and cover what the calls keep there
     assert ffn.ffn_swiglu_backward_workspace_size(64, 64, 128, 64) >= 64 * 128 * (4 + 2 + 4)
-    assert ffn.ffn_orthogonalize_workspace_size(3, 64, 128) >= 3 * (3 * 64 * 128 * 2 + 2 * 64 * 64 * 2)
+    assert ffn.ffn_orthogonalize_workspace_size(3, 136, 264) >= 3 * (3 * 136 * 264 * 2 + 2 * 136 * 136 * 2)
+    # up to 128 x 512 a matrix stays in one workgroup
+    for R, C in ((128, 512), (512, 128), (8, 8)):
+        assert ffn.ffn_orthogonalize_workspace_size(3, R, C) == 256
+    assert ffn.ffn_orthogonalize_workspace_size(3, 136, 512) > 256 < ffn.ffn_orthogonalize_workspace_size(3, 128, 520)
+    assert ffn.ffn_orthogonalize_workspace_size(0, 1024, 1024) >= 256
+
+
+# 1 MiB apart, as far as every array below reaches
+def _at(i):
+    return (i + 1) << 20
+
+
+@pytest.mark.parametrize("over,by", [
+    ("dX", "X"), ("dWg", "Wg"), ("dWu", "dWg"), ("dWd", "dY"), ("dX", "dWd"), ("ws", "X"), ("dWu", "ws"),
+])
+@pytest.mark.parametrize("shift", [0, 4096, -4096])
+def test_swiglu_backward_refuses_overlaps(over, by, shift):
+    names = ["X", "Wg", "Wu", "Wd", "dY", "dX", "dWg", "dWu", "dWd", "ws"]
+    at = {n: _at(4 * i) for i, n in enumerate(names)}
+    at[over] = at[by] + shift
+    assert _swiglu(wsb=1 << 20, **at) == E_INVAL and "overlap" in ffn.ffn_last_error()
+
+
+@pytest.mark.parametrize("over,by,shift", [
+    ("Y", "X", 16), ("Y", "X", -16), ("Y", "gamma", 0), ("mean", "X", 0), ("rstd", "mean", 0), ("mean", "beta", 0),
+    ("rstd", "Y", 0),
+])
+def test_layernorm_forward_refuses_overlaps(over, by, shift):
+    at = {n: _at(i) for i, n in enumerate(["X", "gamma", "beta", "Y", "mean", "rstd"])}
+    at[over] = at[by] + shift
+    assert _ln_fwd(**at) == E_INVAL and "overlap" in ffn.ffn_last_error()
+
+
+@pytest.mark.parametrize("over,by,shift", [
+    ("dX", "X", 128), ("dX", "dY", -128), ("dX", "gamma", 0), ("dgamma", "gamma", 0), ("dbeta", "dgamma", 0),
+    ("dbeta", "X", 0), ("dgamma", "mean", 0), ("ws", "dX", 0), ("ws", "rstd", 0),
+])
+def test_layernorm_backward_refuses_overlaps(over, by, shift):
+    names = ["X", "dY", "gamma", "mean", "rstd", "dX", "dgamma", "dbeta", "ws"]
+    at = {n: _at(i) for i, n in enumerate(names)}
+    at[over] = at[by] + shift
+    assert _ln_bwd(wsb=1 << 20, **at) == E_INVAL and "overlap" in ffn.ffn_last_error()
+
+
+@pytest.mark.parametrize("R,C", [(64, 128), (136, 264)])
+def test_orthogonalize_refuses_overlaps(R, C):
+    size = 2 * R * C
+    for kw in (dict(U=_at(0)), dict(U=_at(0) + size - 16), dict(U=_at(0) - size + 16), dict(ws=_at(0)),
+               dict(ws=_at(1)), dict(U=_at(0) + size, dtype=ffn.F32)):
+        args = dict(G=_at(0), U=_at(1), ws=_at(2), wsb=1 << 20, R=R, C=C)
+        assert _ortho(**{**args, **kw}) == E_INVAL and "overlap" in ffn.ffn_last_error()

@@ -248,6 +248,18 @@ def workspace(nbytes: int, device="cuda"):
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _own_workspace(nbytes, device, stream):
+    """The workspace of a call that brings none, allocated and filled on the stream that the call
+    runs on: on another one the fill could come after the kernels' first writes, and the memory
+    could be given to other work before the last ones."""
+    import torch
+    if stream is None or stream == _stream(None):
+        return workspace(nbytes, device)
+    on = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(on):
+        return workspace(nbytes, device)
+
+
 def _dense_args(X, W1, b1, W2, b2, Y, ws=None):
     """Checks the dense call's tensors; returns M, N, O, P and the dtype code."""
     M, N = _dims(X, "X", 2)
@@ -285,7 +297,7 @@ def ffn_forward_ex(X, W1, b1, W2, b2, Y, act1="gelu_tanh", act2="none", variant=
     ``ffn_workspace_size(...)`` bytes (allocated here when None)."""
     M, N, O, P, dt = _dense_args(X, W1, b1, W2, b2, Y, ws)
     if ws is None:
-        ws = workspace(ffn_workspace_size(M, N, O, P, dt, variant), X.device)
+        ws = _own_workspace(ffn_workspace_size(M, N, O, P, dt, variant), X.device, stream)
     _check(lib().ffn_forward_ex(_ptr(X), _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2), _ptr(Y),
                                 M, N, O, P, dt, _act(act1), _act(act2), int(variant),
                                 _ptr(ws), ws.numel(), _stream(stream)))
@@ -322,7 +334,7 @@ def ffn_backward(X, W1, b1, W2, dY, dX, dW1, db1, dW2, db2, act1="gelu_tanh", ws
     _ws_arg(ws)
     _on_device(X, W1, b1, W2, dY, dX, dW1, db1, dW2, db2, ws)
     if ws is None:
-        ws = workspace(ffn_backward_workspace_size(M, N, O, P, dt), X.device)
+        ws = _own_workspace(ffn_backward_workspace_size(M, N, O, P, dt), X.device, stream)
     _check(lib().ffn_backward(_ptr(X), _ptr(W1), _ptr(b1), _ptr(W2), _ptr(dY), _ptr(dX), _ptr(dW1),
                               _ptr(db1), _ptr(dW2), _ptr(db2), M, N, O, P, dt, _act(act1),
                               _ptr(ws), ws.numel(), _stream(stream)))
@@ -347,7 +359,7 @@ def ffn_swiglu_forward(X, Wg, Wu, Wd, Y, variant=VARIANT_AUTO, ws=None, stream=N
     _ws_arg(ws)
     _on_device(X, Wg, Wu, Wd, Y, ws)
     if ws is None:
-        ws = workspace(ffn_swiglu_workspace_size(M, N, O, P, dt, variant), X.device)
+        ws = _own_workspace(ffn_swiglu_workspace_size(M, N, O, P, dt, variant), X.device, stream)
     _check(lib().ffn_swiglu_forward(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(Y), M, N, O, P,
                                     dt, int(variant), _ptr(ws), ws.numel(), _stream(stream)))
     return Y
@@ -379,7 +391,7 @@ def ffn_swiglu_backward(X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, ws=None, stream=No
     _ws_arg(ws)
     _on_device(X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, ws)
     if ws is None:
-        ws = workspace(ffn_swiglu_backward_workspace_size(M, N, O, P), X.device)
+        ws = _own_workspace(ffn_swiglu_backward_workspace_size(M, N, O, P), X.device, stream)
     _check(lib().ffn_swiglu_backward(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(dY), _ptr(dX),
                                      _ptr(dWg), _ptr(dWu), _ptr(dWd), M, N, O, P, BF16, gdt,
                                      _ptr(ws), ws.numel(), _stream(stream)))
@@ -425,7 +437,7 @@ def ffn_layernorm_backward(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws=None,
     _ws_arg(ws)
     _on_device(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws)
     if ws is None:
-        ws = workspace(ffn_layernorm_backward_workspace_size(M, N, dt), X.device)
+        ws = _own_workspace(ffn_layernorm_backward_workspace_size(M, N, dt), X.device, stream)
     _check(lib().ffn_layernorm_backward(_ptr(X), _ptr(dY), _ptr(gamma), _ptr(mean), _ptr(rstd),
                                         _ptr(dX), _ptr(dgamma), _ptr(dbeta), M, N, dt, _ptr(ws),
                                         ws.numel(), _stream(stream)))
@@ -450,7 +462,7 @@ def ffn_orthogonalize(G, U, steps=5, ws=None, stream=None):
     _ws_arg(ws)
     _on_device(G, U, ws)
     if ws is None:
-        ws = workspace(ffn_orthogonalize_workspace_size(B, R, C, dt), G.device)
+        ws = _own_workspace(ffn_orthogonalize_workspace_size(B, R, C, dt), G.device, stream)
     _check(lib().ffn_orthogonalize(_ptr(G), _ptr(U), B, R, C, dt, int(steps), _ptr(ws), ws.numel(),
                                    _stream(stream)))
     return U
@@ -491,7 +503,7 @@ def moe_route(logits, k, topk_ids=None, topk_w=None, expert_offsets=None, sorted
     _ws_arg(ws)
     _on_device(logits, topk_ids, topk_w, expert_offsets, sorted_entries, ws)
     if ws is None:
-        ws = workspace(moe_workspace_size(M, E, k, 8, 8, 8), logits.device)
+        ws = _own_workspace(moe_workspace_size(M, E, k, 8, 8, 8), logits.device, stream)
     _check(lib().moe_route(_ptr(logits), M, E, k, _ptr(topk_ids), _ptr(topk_w),
                            _ptr(expert_offsets), _ptr(sorted_entries), _ptr(ws), ws.numel(),
                            _stream(stream)))
@@ -509,7 +521,7 @@ def moe_ffn_forward(X, logits, k, W1, b1, W2, b2, Y, act1="gelu_tanh", act2="non
     _on_device(X, logits, W1, b1, W2, b2, Y, topk_ids, topk_w, expert_offsets, sorted_entries, ws)
     dt = BF16
     if ws is None:
-        ws = workspace(moe_workspace_size(M, E, k, N, O, P, dt), X.device)
+        ws = _own_workspace(moe_workspace_size(M, E, k, N, O, P, dt), X.device, stream)
     _check(lib().moe_ffn_forward(_ptr(X), _ptr(logits), M, E, k, _ptr(W1), _ptr(b1), _ptr(W2),
                                  _ptr(b2), _ptr(Y), N, O, P, dt, _act(act1), _act(act2),
                                  _ptr(topk_ids), _ptr(topk_w), _ptr(expert_offsets),
@@ -531,7 +543,7 @@ def moe_router(X, Wr, br, k, logits_out=None, topk_ids=None, topk_w=None, expert
     _ws_arg(ws)
     _on_device(X, Wr, br, logits_out, topk_ids, topk_w, expert_offsets, sorted_entries, ws)
     if ws is None:
-        ws = workspace(moe_workspace_size(M, E, k, N, 8, 8), X.device)
+        ws = _own_workspace(moe_workspace_size(M, E, k, N, 8, 8), X.device, stream)
     _check(lib().moe_router(_ptr(X), _ptr(Wr), _ptr(br), M, N, E, k, _ptr(logits_out),
                             _ptr(topk_ids), _ptr(topk_w), _ptr(expert_offsets),
                             _ptr(sorted_entries), _ptr(ws), ws.numel(), _stream(stream)))
@@ -552,7 +564,7 @@ def moe_ffn_forward_router(X, Wr, br, k, W1, b1, W2, b2, Y, act1="gelu_tanh", ac
                sorted_entries, ws)
     dt = BF16
     if ws is None:
-        ws = workspace(moe_workspace_size(M, E, k, N, O, P, dt), X.device)
+        ws = _own_workspace(moe_workspace_size(M, E, k, N, O, P, dt), X.device, stream)
     _check(lib().moe_ffn_forward_router(_ptr(X), _ptr(Wr), _ptr(br), M, E, k, _ptr(W1), _ptr(b1),
                                         _ptr(W2), _ptr(b2), _ptr(Y), N, O, P, dt, _act(act1),
                                         _act(act2), _ptr(logits_out), _ptr(topk_ids), _ptr(topk_w),

@@ -610,6 +610,32 @@ int ffn_swiglu_forward_traced(const void* X, const void* Wg, const void* Wu, con
                           workspace_bytes, stream, events, n_events);
 }
 
+// An array of a call, for the training operators' check of overlaps.
+struct Span {
+    const void* p;
+    int64_t bytes;
+    const char* name;
+};
+
+// Refuses outputs (the workspace among them) that overlap an input or one another; the
+// first output may be the very array of one of the first `same` inputs.
+static int check_overlaps(const Span* out, int outs, const Span* in, int ins, int same) {
+    auto overlap = [](const Span& a, const Span& b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
+    };
+    for (int i = 0; i < outs; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return fail(FFN_EINVAL, "%s and %s overlap", out[j].name, out[i].name);
+        for (int j = 0; j < ins; ++j)
+            if (overlap(out[i], in[j]) &&
+                !(j < same && i == 0 && out[i].p == in[j].p && out[i].bytes == in[j].bytes))
+                return fail(FFN_EINVAL, "%s and %s overlap", in[j].name, out[i].name);
+    }
+    return FFN_OK;
+}
+
 // ---------------------------------------------------------------- SwiGLU backward
 
 size_t ffn_swiglu_backward_workspace_size(int64_t M, int64_t N, int64_t O, int64_t P, int dtype) {
@@ -643,6 +669,12 @@ int ffn_swiglu_backward(const void* X, const void* Wg, const void* Wu, const voi
     const size_t need = ffn::swiglu_backward_layout(M, N, O, P).total;
     if (workspace_bytes < need)
         return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    const int64_t gb = grad_dtype == FFN_F32 ? 4 : 2;
+    const Span out[] = {{dX, 2 * M * N, "dX"}, {dWg, gb * N * O, "dWg"}, {dWu, gb * N * O, "dWu"},
+                        {dWd, gb * O * P, "dWd"}, {workspace, (int64_t)need, "the workspace"}};
+    const Span in[] = {{X, 2 * M * N, "X"}, {Wg, 2 * N * O, "Wg"}, {Wu, 2 * N * O, "Wu"},
+                       {Wd, 2 * O * P, "Wd"}, {dY, 2 * M * P, "dY"}};
+    if ((rc = check_overlaps(out, 5, in, 5, 0))) return rc;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (M == 0) {
         const int64_t words = grad_dtype == FFN_F32 ? 1 : 2;   // gradients per 4-byte word
@@ -697,6 +729,10 @@ int ffn_layernorm_forward(const void* X, const void* gamma, const void* beta, vo
     const char* nm[] = {"X", "gamma", "beta", "Y", "mean", "rstd"};
     for (int i = 0; i < 6; ++i)
         if (ps[i] && !aligned16(ps[i])) return fail(FFN_EALIGN, "%s is not 16-byte aligned", nm[i]);
+    const int64_t eb = dtype == FFN_F32 ? 4 : 2;
+    const Span out[] = {{Y, eb * M * N, "Y"}, {mean, 4 * M, "mean"}, {rstd, 4 * M, "rstd"}};
+    const Span in[] = {{X, eb * M * N, "X"}, {gamma, eb * N, "gamma"}, {beta, eb * N, "beta"}};
+    if ((rc = check_overlaps(out, 3, in, 3, 1))) return rc;
     if (M == 0) return ok();
     rc = launched(ffn::launch_layernorm_forward(X, gamma, beta, Y, mean, rstd, M, N,
                                                 dtype == FFN_F32, eps,
@@ -730,6 +766,12 @@ int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, con
     const size_t need = ffn_layernorm_backward_workspace_size(M, N, dtype);
     if (workspace_bytes < need)
         return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    const int64_t eb = dtype == FFN_F32 ? 4 : 2;
+    const Span out[] = {{dX, eb * M * N, "dX"}, {dgamma, 4 * N, "dgamma"}, {dbeta, 4 * N, "dbeta"},
+                        {workspace, (int64_t)need, "the workspace"}};
+    const Span in[] = {{X, eb * M * N, "X"}, {dY, eb * M * N, "dY"}, {gamma, eb * N, "gamma"},
+                       {mean, 4 * M, "mean"}, {rstd, 4 * M, "rstd"}};
+    if ((rc = check_overlaps(out, 4, in, 5, 2))) return rc;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (M == 0) {
         if ((rc = launched(ffn::launch_zero_f32(dgamma, N, st), "zero fill"))) return rc;
@@ -785,6 +827,9 @@ int ffn_orthogonalize(const void* G, void* U, int64_t B, int64_t R, int64_t C, i
     const size_t need = ffn_orthogonalize_workspace_size(B, R, C, dtype);
     if (workspace_bytes < need)
         return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    const Span out[] = {{U, 2 * B * R * C, "U"}, {workspace, (int64_t)need, "the workspace"}};
+    const Span in[] = {{G, (dtype == FFN_F32 ? 4 : 2) * B * R * C, "G"}};
+    if ((rc = check_overlaps(out, 2, in, 1, 0))) return rc;
     if (B == 0) return ok();
     rc = launched(ffn::launch_orthogonalize(G, dtype == FFN_F32, static_cast<uint16_t*>(U), B, R, C,
                                             steps, static_cast<char*>(workspace),
