@@ -289,6 +289,7 @@ __device__ __forceinline__ void dma16(const int32x4_t& srd, uint32_t byte_off, c
     const uint32_t m0 = (uint32_t)(uintptr_t)((lds_void_t*)lds_base);
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"   // a wait state between writing M0 and a load to LDS
         "buffer_load_dwordx4 %1, %2, 0 offen lds"
         :
         : "s"(__builtin_amdgcn_readfirstlane((int)m0)), "v"(byte_off), "s"(srd)
