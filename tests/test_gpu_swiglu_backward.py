@@ -61,6 +61,10 @@ def test_shapes(shape, grad_f32):
     (1013, 2056, 1400, 1992),    # joins
     (8, 128, 512, 128),          # joins of few rows
     (20, 2048, 1024, 1536),
+    (70, 2056, 264, 2000),       # few tiles, deep: dh and the gated step apart, split
+    (2100, 72, 4104, 88),        # many tiles, shallow: dh and the gated step together, in rounds
+    (2100, 1032, 4104, 1000),    # ... and a shape where they are apart
+    (1030, 264, 1096, 200),
 ])
 def test_large_shapes(shape):
     print(f"case swiglu backward {shape}", flush=True)

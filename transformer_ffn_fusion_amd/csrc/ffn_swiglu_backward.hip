@@ -3,7 +3,7 @@
 // With a = X Wg, b = X Wu, h = silu(a) * b, Y = h Wd, s = sigmoid(a) and the
 // output gradient dY:
 //
-//   1. dh = dY Wd^T                                            (M x O, fp32)
+//   1. dh = dY Wd^T                           (M x O, fp32; small calls: inside 2.)
 //   2. a, b, recomputed together; epilogue: h = a s b,
 //      da = dh b s (1 + a (1 - s)), db = dh a s                (M x O each, bf16)
 //   3. dX = da Wg^T + db Wu^T, one sum over both products      (M x N, bf16)
@@ -91,15 +91,15 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8])
     }
 }
 
-// Workgroup w of one step.
-template <class Cfg, int kStep, bool kGradF32>
+// Workgroup w of one step; kOwnDh: the gated step computes its tile of dh itself.
+template <class Cfg, int kStep, bool kGradF32, bool kOwnDh = false>
 __device__ __forceinline__ void run_step(char* smem, const SwigluBackwardArgs& g, uint32_t w,
                                          uint32_t full, uint32_t splits) {
     using S = StepShape<kStep>;
     const int64_t M = g.M, N = g.N, O = g.O, P = g.P;
     const int64_t I = S::rows(M, N, O), J = S::cols(N, O, P);
     constexpr int kWidth = S::template width<Cfg>();
-    if constexpr (kStep == STEP_DH)   // a later step's counters (this one has no splits then)
+    if constexpr (kStep == STEP_DH || kOwnDh)   // a later step's counters (this one has no splits then)
         if (w == 0)
             for (int64_t k = threadIdx.x; k < g.clear; k += Cfg::kThreads) g.count[k] = 0;
     TilePlace at;
@@ -146,7 +146,29 @@ __device__ __forceinline__ void run_step(char* smem, const SwigluBackwardArgs& g
     auto before = [&](int off, auto& d) {
         if constexpr (kStep == STEP_GATED) load8_f32(g.dH + first + (int64_t)off * O, d.v);
     };
-    if (at.splits == 1) states.load(t, rows, before);   // (the join needs the registers)
+    if constexpr (kOwnDh) {
+        // dY Wd^T of the tile's rows and hidden columns, through LDS to the threads that use it
+        using Own = TileCfg<Cfg::TI, Cfg::HJ, Cfg::WI, Cfg::WJ>;
+        static_assert(states.kEarly && PartOf<Own>::kParts == PartOf<Cfg>::kParts, "one part, kept");
+        TileOperand C = A, D = B;
+        C.p = g.dY;
+        D.p = g.Wd;
+        C.ld = D.ld = P;
+        D.at[1] = j0 + Own::HJ;
+        TileAcc<Own> dh;
+        tile_clear<Own>(dh);
+        tile_product<Own, false, false, false, 1>(smem, C, D, P, nullptr, nullptr, nullptr, 0,
+                                                  (int)((P + kTileK - 1) / kTileK), dh);
+        part_put<Own>(smem, dh, 0);
+        __syncthreads();
+        const PartThread<Own, kCols> own;
+#pragma unroll
+        for (int k = 0; k < own.kUnits; ++k) own.get(smem, own.place(2 * own.c), k, states.early[0][k].v);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __syncthreads();   // the next product's loads take the place
+    } else if (at.splits == 1) {
+        states.load(t, rows, before);   // (the join needs the registers)
+    }
 
     TileAcc<Cfg> acc;
     tile_clear<Cfg>(acc);
@@ -203,11 +225,19 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_kernel(SwigluBa
     run_step<Cfg, kStep, kGradF32>(smem, g, blockIdx.x, (uint32_t)g.full, (uint32_t)g.splits);
 }
 
+// dh and the gated step in one launch, where that is faster (hidden_together).  The same sums in
+// the same order as apart in 128 x 128 tiles: dh stays fp32 and goes through LDS only.
+template <class Cfg>
+__global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_hidden_kernel(SwigluBackwardArgs g) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    run_step<Cfg, STEP_GATED, false, true>(smem, g, blockIdx.x, 0x7fffffffu, 1);
+}
+
 // dX, dWg and dWu, and dWd in one launch: they do not depend on each other, and where
 // each alone leaves CUs idle, or is over before a launch is, together they fill them
 // (whole calls: 8 x 128 x 512 x 128 28 -> 18 us, 16 x 4096 x 1792 x 4096 67 -> 57,
-// 1013 x 2056 x 1400 x 1992 110 -> 95).  Only dX may be split (few tokens: few tiles
-// of it, each as deep as 2 O).
+// 1013 x 2056 x 1400 x 1992 110 -> 95; dh still apart).  Only dX may be split (few
+// tokens: few tiles of it, each as deep as 2 O).
 template <class Cfg, bool kGradF32>
 __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_outputs_kernel(SwigluBackwardArgs g) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -303,17 +333,43 @@ hipError_t launch_outputs(SwigluBackwardArgs g, const TilePlan& plan, hipStream_
     return launch_kernel<TileSmall>(swiglu_backward_outputs_kernel<TileSmall, kGradF32>, lds_set, g, at, stream);
 }
 
+// Whether dh and the gated step go together: few k-tiles on few tiles, where a launch and
+// dh's way to memory and back count, against each in the tile and splits that suit it.  The
+// way there and back is at 5 TB/s; a k-tile of 128 x 64 is taken as 0.6 of one of 128 x 128.
+// Whole calls, apart -> together (* as chosen): 8 x 128 x 512 x 128 18.1 -> 15.3 us *,
+// 1013 x 2056 x 1400 x 1992 95.7 -> 87.7 *, 4096 x 256 x 4096 x 256 128 -> 106 *,
+// 2048 x 4096 x 1792 x 4096 233 -> 230 *; 1500 x 1000 x 3000 x 1000 120 * -> 123,
+// 512 x 4096 x 1792 x 4096 97 * -> 103, 16 x 4096 x 1792 x 4096 55.6 * -> 78.
+bool hidden_together(int64_t M, int64_t N, int64_t O, int64_t P) {
+    constexpr int k = TILE_SMALL;
+    const int64_t tiles = step_tiles<STEP_GATED>(k, M, N, O, P), slots = kTileKinds[k].slots;
+    const double each = 0.6 * StepShape<STEP_DH>::depth(M, N, O, P) * tile_us(k, tiles, 0) +
+                        StepShape<STEP_GATED>::depth(M, N, O, P) * tile_us(k, tiles, 1);
+    return kLaunchUs + 1.0 + (double)((tiles + slots - 1) / slots) * each <
+           StepShape<STEP_DH>::plan(M, N, O, P).us + StepShape<STEP_GATED>::plan(M, N, O, P).us +
+               (double)M * (double)O * 8e-6 / 5.0;
+}
+
 template <bool kGradF32>
 hipError_t launch_all(const SwigluBackwardArgs& g, int64_t counters, hipStream_t stream) {
     hipError_t e;
     SwigluBackwardArgs first = g;
-    if (StepShape<STEP_DH>::plan(g.M, g.N, g.O, g.P).splits == 1) {
+    const bool hidden = hidden_together(g.M, g.N, g.O, g.P);
+    if (hidden || StepShape<STEP_DH>::plan(g.M, g.N, g.O, g.P).splits == 1) {
         first.clear = counters;
     } else if ((e = launch_zero_f32(reinterpret_cast<float*>(g.count), counters, stream)) != hipSuccess) {
         return e;
     }
-    if ((e = launch_step<STEP_DH, false>(first, stream)) != hipSuccess) return e;
-    if ((e = launch_step<STEP_GATED, false>(g, stream)) != hipSuccess) return e;
+    if (hidden) {
+        static std::atomic<bool> lds_set[kMaxDevices] = {};
+        const int64_t tiles = step_tiles<STEP_GATED>(TILE_SMALL, g.M, g.N, g.O, g.P);
+        e = launch_kernel<TileSmall>(swiglu_backward_hidden_kernel<TileSmall>, lds_set, first,
+                                     tile_grid(tiles, tiles, 1), stream);
+    } else {
+        if ((e = launch_step<STEP_DH, false>(first, stream)) != hipSuccess) return e;
+        e = launch_step<STEP_GATED, false>(g, stream);
+    }
+    if (e != hipSuccess) return e;
     const TilePlan together = outputs_plan(g.M, g.N, g.O, g.P);
     if (outputs_together(together, g.M, g.N, g.O, g.P)) return launch_outputs<kGradF32>(g, together, stream);
     if ((e = launch_step<STEP_DX, false>(g, stream)) != hipSuccess) return e;

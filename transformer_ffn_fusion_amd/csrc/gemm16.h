@@ -77,7 +77,6 @@ struct TileCfg {
     static constexpr int kBuf = 2 * (kHalfA + kHalfB);
     static constexpr int kLds = 2 * kBuf;
     static constexpr int UA = kHalfA / 1024 / kWaves, UB = kHalfB / 1024 / kWaves;  // loads a wave
-    static_assert(HI % 64 == 0 && HJ % 64 == 0, "k-strided operands stage 64-index blocks");
     static_assert(FI * 16 * WI == HI && FJ * 16 * WJ == HJ, "whole fragments per wave");
     static_assert(UA * 1024 * kWaves == kHalfA && UB * 1024 * kWaves == kHalfB,
                   "every wave issues the same loads");
@@ -125,7 +124,7 @@ __device__ __forceinline__ void tile_dma(uint64_t base, bool any, uint32_t off, 
 //  the 8-deep k-group c of index r lies in slot 8r + (c ^ r).  A fragment read
 //  takes k-group 4 kh + lane / 16 of index lane % 16 = 8q + r: 8 lanes with the
 //  same k-group fill the 8 slots' columns, no bank conflicts.  (Units of 16
-//  indices x 32 k read half lines: 8192^3 734 us against 6xx.)
+//  indices x 32 k, which read half lines, measured the same.)
 //
 //  k-strided: unit (kh, g, c) holds k-rows 32 kh + 8 g .. + 7 and indices 64 c ..
 //  64 c + 63, 128 contiguous bytes a row; the 8-index group u of row r lies in
@@ -137,6 +136,7 @@ __device__ __forceinline__ int strided_swizzle(int r, int g) { return 2 * (r ^ (
 // What a wave loads of a half-tile: units wave, wave + W, ...
 template <bool kStrided, int H, int W, int U>
 struct HalfLoads {
+    static_assert(!kStrided || H % 64 == 0, "k-strided operands stage 64-index blocks");
     uint32_t off[2][U];   // this lane's byte offset from the k-tile, per half; kOOB past the indices
     bool past[U];         // in the last k-tile: past K
     uint64_t base[2];     // where each half's next k-tile starts
