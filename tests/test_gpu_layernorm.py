@@ -56,6 +56,16 @@ def test_forward_and_backward(shape, dtype):
               f"{shape} backward")
 
 
+@pytest.mark.parametrize("M,N", [(256, 16384), (257, 16384), (300, 16376), (511, 8200), (512, 8192), (513, 8192)])
+def test_backward_one_two_and_three_turns(M, N):
+    """Around one, two and three rows a workgroup, where the number of workgroups changes."""
+    import torch
+    x = make(M, N, torch.float32, seed=M)
+    f = forward(x)
+    b = backward(x, f["mean"], f["rstd"])
+    ref.check(b, ref.layernorm_backward(x["X"], x["dY"], x["gamma"], f["mean"], f["rstd"]), f"{M} x {N}")
+
+
 def test_statistics_are_optional_and_calls_repeat_bitwise():
     import torch
     x = make(301, 1288, torch.bfloat16, seed=2)

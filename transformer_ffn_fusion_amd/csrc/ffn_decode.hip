@@ -131,8 +131,9 @@ __device__ __forceinline__ void fail(uint64_t* status, uint64_t epoch) {
         __hip_atomic_store(status, epoch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// One workgroup per CU, workgroup b on XCD x with index j = b / 8 there.  The layer-1 waves compute layer 1 of K block j / 2 over half j mod 2
-// of slice x: wave w of a group of four takes K rows [256 (j / 2) + 64 w,
+// One workgroup per CU, workgroup b on XCD x with index j = b / 8 there.  The
+// layer-1 waves compute layer 1 of K block j / 2 over half j mod 2 of slice x:
+// wave w of a group of four takes K rows [256 (j / 2) + 64 w,
 // +64) in two 32-row steps; lane (g, c) loads rows +8g .. +8g+7 of each step
 // and the 8 columns 8c .. 8c+7 of the half, transposes them in registers into
 // the MFMA's k-contiguous operand and multiplies the matching X fragment (a
