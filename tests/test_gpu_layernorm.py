@@ -151,3 +151,21 @@ def test_differences():
         slack = 300 * ref.U_F32 * float((ref.d(b[grad]).abs() * v.abs()).sum() + 30)
         print(f"  {grad}: {got:.7f}, by differences {num:.7f}", flush=True)
         assert abs(got - num) <= slack + 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("N", [72, 520, 1544, 8200, 12296])
+def test_backward_where_mean_times_rstd_leaves_fp32(N, dtype):
+    """Constant rows far from 0: z is 0 and dX finite, although mean * rstd is past fp32's largest
+    value (2^112 * 1e6); N that does not fill the waves' columns.  (The sum of N times 2^112 is a
+    whole multiple of it and within fp32: the mean is exact.)"""
+    import torch
+    print(f"case layer norm backward, constant rows, N = {N} {dtype}", flush=True)
+    x = make(21, N, getattr(torch, dtype), seed=N)
+    x["X"][4] = 2.0 ** 112
+    x["X"][17] = -2.0 ** 112
+    f = forward(x, eps=1e-12)
+    assert float(f["mean"][4]) == 2.0 ** 112 and float(f["mean"][17]) == -2.0 ** 112
+    assert torch.equal(f["Y"][4], x["beta"]) and torch.equal(f["Y"][17], x["beta"])
+    b = backward(x, f["mean"], f["rstd"])
+    ref.check(b, ref.layernorm_backward(x["X"], x["dY"], x["gamma"], f["mean"], f["rstd"]), f"N = {N}")

@@ -209,7 +209,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_backward_kernel(
             if (on && column(v) < N) {
                 xr[set][v].load(X, row * N + column(v));
                 dr[set][v].load(dY, row * N + column(v));
-            } else {   // z = 0 then, whatever mean is: the sums below take no part of it
+            } else {
                 xr[set][v].zero();
                 dr[set][v].zero();
             }
@@ -225,8 +225,11 @@ __global__ __launch_bounds__(kLnThreads) void ln_backward_kernel(
         auto split = [&](int v, float (&zz)[8], float (&tt)[8]) {
             xr[set][v].get(zz);
             dr[set][v].get(tt);
+            // Columns past N hold x = 0, and mean * rstd may leave fp32 where no column's z does (a
+            // constant row); with 0 for rstd their z is 0 and adds nothing to the sums.
+            const float by = column(v) < N ? rstd : 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) zz[e] = (zz[e] - mean) * rstd;
+            for (int e = 0; e < 8; ++e) zz[e] = (zz[e] - mean) * by;
         };
 #pragma unroll
         for (int v = 0; v < V; ++v) {
