@@ -280,8 +280,9 @@ int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, con
  * G: a stack of B matrices R x C in `dtype` (FFN_BF16 or FFN_F32), for instance
  * the experts' gradients; each is treated by itself.  U: B x R x C bf16.  (With
  * R > C the same polynomial is applied from the right.)  The norm is summed in
- * fp64; products take fp16 operands with fp32 sums, X is carried in 22 bits, so U
- * is within a few bf16 half steps of the exact iteration.  A matrix of zeros gives
+ * fp64; products take fp16 operands with fp32 sums, X is carried in 22 bits under
+ * a scale of each matrix's own, so U is within a few bf16 half steps of the exact
+ * iteration whatever ||G|| is.  A matrix of zeros gives
  * zeros; a NaN or infinity in a matrix makes that matrix's U NaN.  R and C
  * multiples of 8 below 2^22, R * C and min(R, C)^2 below 2^31, B up to 65535,
  * 1 <= steps <= 32.  U must not overlap G.  With B == 0 nothing is done. */

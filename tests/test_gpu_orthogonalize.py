@@ -180,3 +180,32 @@ def test_zeros_nan_and_infinity():
 def test_empty_stack():
     import torch
     ffn.ffn_orthogonalize(torch.empty(0, 8, 8, device="cuda"), torch.empty(0, 8, 8, dtype=torch.bfloat16, device="cuda"))
+
+
+SMALL_NORMS = [1e-7, 1e-10, 1e-12, 1e-16, 1e-25, 1e-36]
+
+
+@pytest.mark.parametrize("norm", SMALL_NORMS)
+@pytest.mark.parametrize("shape", [(120, 328), (512, 128), (200, 328), (1032, 264)])
+def test_small_norms(shape, norm):
+    """||G|| around the norm's epsilon and far below it: X = G / (||G|| + 1e-7) is small then, and as
+    accurate as any other, in one workgroup and in tiles."""
+    import torch
+    print(f"case orthogonalize {shape} of norm {norm}", flush=True)
+    G = gradient(*shape, seed=21).double()
+    G = (G * (norm / torch.linalg.vector_norm(G))).float().cuda()
+    for steps in (1, 5, 8):
+        ref.check_orthogonalize(run(G, steps), G, steps, f"{shape} norm {norm} {steps} steps")
+
+
+@pytest.mark.parametrize("shape", [(72, 136), (136, 264)])
+def test_stack_of_unlike_norms_is_each_alone_bitwise(shape):
+    import torch
+    G = torch.stack([gradient(*shape, seed=30 + s) * 10.0 ** p for s, p in enumerate((0, -12, -30, 20, -9))])
+    G = torch.cat([G, torch.zeros_like(G[:1]), G[:1]]).cuda()
+    G[2, 3, 5] = float("nan")
+    U = run(G)
+    assert bool(torch.isnan(U[2].float()).all()) and not bool(U[5].any())
+    for e in (0, 1, 3, 4, 6):
+        ref.check_orthogonalize(U[e], G[e], 5, f"matrix {e}")
+        assert torch.equal(run(G[e].contiguous()), U[e])

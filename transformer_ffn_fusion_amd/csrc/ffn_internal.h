@@ -227,7 +227,7 @@ hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream
 // ---- orthogonalised updates (orthogonalize.hip)
 
 struct OrthogonalizeLayout {   // workspace byte offsets, 256-byte aligned
-    size_t hi[2], lo, sym, poly, diag, scale, norm, part, count, total;
+    size_t hi[2], lo, sym, poly, diag, scale, norm, scale_x, part, count, total;
     int64_t counters;
 };
 OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C);

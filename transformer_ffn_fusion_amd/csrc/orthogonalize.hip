@@ -24,12 +24,18 @@
 //    They multiply hi alone, as the products do: with hi + lo there, D X and E X
 //    would see two different X, and the difference is again noise in directions
 //    that G does not have (a rank-1 G: 3.3e-3 instead of 1.7e-3).
-// Scales keep fp16 clear of its subnormals: X is held times 64, E and the
-// polynomial's off-diagonal times 1024 (singular values stay below 1.21, so
-// entries stay below 80 and 1.2e4).
+// Scales keep fp16 clear of its subnormals.  X's singular values stay below 1.21 and
+// it is held times 2^15 (entries below 4e4): the pair has its 22 bits down to entries of
+// 2^-18, which the largest matrices' are in the mean.  Where ||G|| is small against
+// 1e-7, X is, and it grows by a in each step: it is held times a larger power of two then,
+// one that its growth cannot overflow (x_scale).  (Times 64 for all, emulated, 1024 x 1536:
+// 4e-3 off at ||G|| = 1e-11, 0.3 at 1e-13.)  E and the polynomial's off-diagonal are held
+// times 1024 (entries below 1.2e4).
 //
 // Bound: the three products of a step, gemm16.h; up to 128 x 512 one workgroup does all
 // (ortho_small_kernel).
+#include <cmath>
+
 #include "ffn_device.h"
 #include "ffn_internal.h"
 #include "gemm16.h"
@@ -40,7 +46,9 @@ namespace {
 
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr double kNsEps = 1e-7;
-constexpr float kScaleX = 64.0f, kScaleSym = 1024.0f;
+constexpr int kScaleX = 15;         // X is held times 2^15 at least,
+constexpr int kScaleSymBits = 10;   // the square matrices' off-diagonals times 2^10
+constexpr float kScaleSym = 1 << kScaleSymBits;
 // Partial sums of squares per matrix (3584 x 8192 fp32: 128 of them 60 us, 1024 26 us).
 inline int norm_blocks(int64_t size) {
     const int64_t k = size / 8192;
@@ -57,6 +65,8 @@ struct OrthoArgs {
     float *diag, *scale;    // diagonals of A and of b A + c A^2
     double* norm;           // norm_blocks partial sums per matrix
     int sums;
+    double growth;          // a^steps: what a small X grows by
+    int* scale_x;           // X's scale, per matrix: the power of two
     float* part;            // sums of split products, and a counter per tile (tile_join)
     uint32_t* count;
     int64_t counters;
@@ -158,14 +168,31 @@ __device__ __forceinline__ float scaled(float v, double by) {
     return x;
 }
 
-// X = 64 G / (||G|| + eps) as hi + lo.
+// 2^k, 0 below fp32's normal numbers.
+__device__ __forceinline__ float pow2(int k) {
+    return __uint_as_float(k < -126 ? 0u : (uint32_t)(127 + k) << 23);
+}
+// What G is multiplied by to be X = G / (||G|| + eps) times its scale 2^*e; q: G's sum of
+// squares, the same in all lanes.  No singular value grows by more than a in a step, so X stays
+// below a^steps times its norm here.  (Zeros, NaN and infinities take the plain scale.)
+__device__ __forceinline__ double x_scale(double q, double growth, int* e) {
+    const double norm = sqrt(q), grown = norm / (norm + kNsEps) * growth;
+    int up = 0;
+    if (grown > 0.0 && grown < 1.0) up = -ilogb(grown) - 1;   // grown 2^up is in [0.5, 1)
+    *e = kScaleX + __builtin_amdgcn_readfirstlane(up < 110 ? up : 110);   // (2^-e stays normal)
+    return ldexp(1.0, *e) / (norm + kNsEps);
+}
+
+// X as hi + lo.
 template <bool kF32>
 __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoArgs g) {
     __shared__ double s[4];
     double q = 0.0;
     for (int k = threadIdx.x; k < g.sums; k += 256) q += g.norm[(int64_t)blockIdx.y * g.sums + k];
     q = workgroup_sum(q, s);
-    const double by = (double)kScaleX / (sqrt(q) + kNsEps);
+    int e;
+    const double by = x_scale(q, g.growth, &e);
+    if (blockIdx.x == 0 && threadIdx.x == 0) g.scale_x[blockIdx.y] = e;
     const int64_t size = g.R * g.C, base = (int64_t)blockIdx.y * size;
     for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; k < size;
          k += (int64_t)gridDim.x * 2048) {
@@ -199,6 +226,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
     const uint16_t* sym = g.sym + at_m;
     float* diag = g.diag + blockIdx.y * m;
     float* scale = g.scale + blockIdx.y * m;
+    const int ex = kProd == PROD_POLY ? 0 : g.scale_x[blockIdx.y];
 
     TileOperand A, B;
     int64_t K;
@@ -288,7 +316,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
                 const int64_t at_e = first + (int64_t)off * ld;
                 if (g.last) {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] *= 1.0f / kScaleX;
+                    for (int r = 0; r < 8; ++r) v[r] *= pow2(-ex);
                     *reinterpret_cast<uint4*>(g.U + at_e) =
                         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -298,7 +326,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
             } else {
                 if constexpr (kProd == PROD_SYM) {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] *= kScaleSym / (kScaleX * kScaleX);
+                    for (int r = 0; r < 8; ++r) v[r] *= pow2(kScaleSymBits - 2 * ex);
                 } else {
                     // b E + c (E^2 + (D_i + D_j) E), E and the result times kScaleSym
                     float o[8];
@@ -317,7 +345,7 @@ __global__ __launch_bounds__(Cfg::kThreads) void ortho_kernel(OrthoArgs g) {
                     }
                     const int64_t i = i0 + t.row0 + off;
                     if constexpr (kProd == PROD_SYM)
-                        diag[i] = own * (1.0f / (kScaleX * kScaleX));
+                        diag[i] = own * pow2(-2 * ex);
                     else   // b D + c (E^2 + D^2)
                         scale[i] = kNsB * e.d + kNsC * (own * (1.0f / (kScaleSym * kScaleSym)) + e.d * e.d);
                 }
@@ -413,7 +441,7 @@ __device__ __forceinline__ int small_square_at(int j, int t, int g) {
 
 template <bool kF32, bool kTall>
 __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* G, uint16_t* U, int R,
-                                                                    int C, int steps) {
+                                                                    int C, int steps, double growth) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     char* const square = smem;             // A's off-diagonal, after X was read
     char* const poly = smem + kSquare;
@@ -486,7 +514,8 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
                     __builtin_bit_cast(uint2, hi[c][t]);
     };
 
-    {   // X = 64 G / (||G|| + eps)
+    int ex;
+    {   // X = G / (||G|| + eps), scaled
         float v[4][8][4];
         double q = 0.0;
 #pragma unroll
@@ -506,7 +535,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
         q = 0.0;
 #pragma unroll
         for (int w = 0; w < 8; ++w) q += sums[w];
-        const double by = (double)kScaleX / (sqrt(q) + kNsEps);
+        const double by = x_scale(q, growth, &ex);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -571,9 +600,9 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
                 for (int r = 0; r < 4; ++r) {
                     const bool here = on && r == (li & 3);
                     own = here ? acc[x][y][r] : own;
-                    v[r] = here ? 0.f : acc[x][y][r] * (kScaleSym / (kScaleX * kScaleX));
+                    v[r] = here ? 0.f : acc[x][y][r] * pow2(kScaleSymBits - 2 * ex);
                 }
-                if (on) diag[j] = own * (1.0f / (kScaleX * kScaleX));
+                if (on) diag[j] = own * pow2(-2 * ex);
                 *reinterpret_cast<uint2*>(square + small_square_at(j, ti + x, g)) = f16x4(v);
             }
         __syncthreads();   // A is written
@@ -665,7 +694,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
         for (int t = 0; t < 8; ++t) {
             float v[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = ((float)hi[c][t][r] + (float)lo[c][t][r]) * (1.0f / kScaleX);
+            for (int r = 0; r < 4; ++r) v[r] = ((float)hi[c][t][r] + (float)lo[c][t][r]) * pow2(-ex);
             store4(16 * t + 4 * g, col0 + 16 * c + li, v);
         }
 }
@@ -678,7 +707,7 @@ hipError_t launch_small(const void* G, uint16_t* U, int64_t B, int64_t R, int64_
     const hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(kern), kSmallLds, lds_set);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3((unsigned)B), dim3(kSmallThreads), kSmallLds, stream, G, U, (int)R,
-                       (int)C, steps);
+                       (int)C, steps, std::pow((double)kNsA, steps));
     return hipGetLastError();
 }
 
@@ -704,6 +733,7 @@ OrthogonalizeLayout orthogonalize_layout(int64_t B, int64_t R, int64_t C) {
     L.diag = take(sizeof(float) * B * m);
     L.scale = take(sizeof(float) * B * m);
     L.norm = take(sizeof(double) * B * norm_blocks(R * C));
+    L.scale_x = take(sizeof(int) * B);
     const TilePlan plans[] = {product_plan<PROD_SYM>(B, R, C), product_plan<PROD_POLY>(B, R, C),
                               product_plan<PROD_X>(B, R, C)};
     int64_t part = 0;
@@ -735,6 +765,8 @@ hipError_t launch_orthogonalize(const void* G, bool f32, uint16_t* U, int64_t B,
     g.diag = reinterpret_cast<float*>(ws + L.diag);
     g.scale = reinterpret_cast<float*>(ws + L.scale);
     g.norm = reinterpret_cast<double*>(ws + L.norm);
+    g.scale_x = reinterpret_cast<int*>(ws + L.scale_x);
+    g.growth = std::pow((double)kNsA, steps);
     g.part = reinterpret_cast<float*>(ws + L.part);
     g.count = reinterpret_cast<uint32_t*>(ws + L.count);
     g.counters = L.counters;
