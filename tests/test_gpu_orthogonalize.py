@@ -209,3 +209,29 @@ def test_stack_of_unlike_norms_is_each_alone_bitwise(shape):
     for e in (0, 1, 3, 4, 6):
         ref.check_orthogonalize(U[e], G[e], 5, f"matrix {e}")
         assert torch.equal(run(G[e].contiguous()), U[e])
+
+
+# Directions that G does not have: what a step rounds there is multiplied by a = 3.4445 in each
+# later one.  A rounding of X's pair is 2^-24 of an element at most; one of the product's fp32 sum
+# over m terms (m / 32 additions of the matrix instruction, 2^-23 each, truncated; taken as
+# independent, 1 / sqrt 3 in the mean, of partial sums that grow to |b + c| = 2.74 times an
+# element): 2^-23 * 2.74 / 3 * sqrt(m / 32), 2.3 * 2^-23 at m = 200.  After the first step's rounding
+# `steps` - 1 more multiply it, and the later ones' add 1 / sqrt(1 - 1 / 3.4445^2) = 1.05 and the
+# pair's own: below 2.5 * 1.41 * 2^-23 * sqrt(m / 200) * 3.4445^(steps - 1) of a U of rank 1.
+def low_rank_bound(m, steps):
+    noise = 2.5 * 1.41 * 2.0 ** -23 * max(1.0, (m / 200) ** 0.5) * ref.NS[0] ** (steps - 1)
+    return (ref.NS_REL ** 2 + noise ** 2) ** 0.5
+
+
+@pytest.mark.parametrize("steps", [5, 8])
+@pytest.mark.parametrize("rank", [1, 4, 16])
+@pytest.mark.parametrize("shape", [(120, 328), (512, 128), (200, 328), (1032, 264), (1024, 1536), (2056, 4136)])
+def test_low_rank_up_to_the_most_steps(shape, rank, steps):
+    import torch
+    print(f"case orthogonalize {shape} rank {rank} {steps} steps", flush=True)
+    G = gradient(*shape, seed=40 + rank, rank=rank).cuda()
+    want, got = ref.orthogonalize(G, steps), ref.d(run(G, steps))
+    rel = float(torch.linalg.vector_norm(got - want) / torch.linalg.vector_norm(want))
+    bound = low_rank_bound(min(shape), steps)
+    print(f"  relative error {rel:.2e} (bound {bound:.1e})", flush=True)
+    assert rel <= bound

@@ -226,3 +226,12 @@ def test_orthogonalize_refuses_overlaps(R, C):
                dict(ws=_at(1)), dict(U=_at(0) + size, dtype=ffn.F32)):
         args = dict(G=_at(0), U=_at(1), ws=_at(2), wsb=1 << 20, R=R, C=C)
         assert _ortho(**{**args, **kw}) == E_INVAL and "overlap" in ffn.ffn_last_error()
+
+
+@pytest.mark.parametrize("R,C", [(64, 128), (136, 264)])
+@pytest.mark.parametrize("steps", [9, 12, 16, 32])
+def test_orthogonalize_refuses_steps_that_grow_noise_past_the_answer(R, C, steps):
+    """A gradient of low rank: what is rounded in directions that it does not have grows by 3.4445 a step."""
+    assert _ortho(R=R, C=C, steps=steps) == E_UNSUP and "steps" in ffn.ffn_last_error()
+    # the most steps that are taken reach the next check
+    assert _ortho(R=R, C=C, steps=8, wsb=0) == E_WS

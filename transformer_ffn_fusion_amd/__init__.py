@@ -449,7 +449,7 @@ def ffn_orthogonalize_workspace_size(B, R, C, dtype=BF16) -> int:
 
 def ffn_orthogonalize(G, U, steps=5, ws=None, stream=None):
     """Newton-Schulz orthogonalisation of a gradient ``G`` (R x C, or a stack B x R x C; bf16 or
-    fp32); ``U`` (the same shape, bf16) is written in place."""
+    fp32) in ``steps`` (1 to 8) steps; ``U`` (the same shape, bf16) is written in place."""
     import torch
     if G is None:
         raise ValueError("G must not be None")

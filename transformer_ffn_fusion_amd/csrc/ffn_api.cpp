@@ -817,7 +817,10 @@ int ffn_orthogonalize(const void* G, void* U, int64_t B, int64_t R, int64_t C, i
                       int steps, void* workspace, size_t workspace_bytes, void* stream) {
     int rc = check_orthogonalize(B, R, C, dtype);
     if (rc) return rc;
-    if (steps < 1 || steps > 32) return fail(FFN_EINVAL, "steps must be 1 to 32 (got %d)", steps);
+    if (steps < 1 || steps > 32) return fail(FFN_EINVAL, "steps must be 1 to %d (got %d)", ffn::kOrthogonalizeSteps, steps);
+    if (steps > ffn::kOrthogonalizeSteps)
+        return fail(FFN_EUNSUPPORTED, "the orthogonalised update takes up to %d steps (got %d)",
+                    ffn::kOrthogonalizeSteps, steps);
     if (B > 0 && (!G || !U)) return fail(FFN_EINVAL, "G and U must not be NULL");
     if (!workspace) return fail(FFN_EINVAL, "workspace must not be NULL");
     if (G && !aligned16(G)) return fail(FFN_EALIGN, "G is not 16-byte aligned");
