@@ -195,3 +195,23 @@ def test_shapes_with_joined_splits_repeat_bitwise():
         torch.cuda.synchronize()
         first = U.clone() if first is None else first
         assert torch.equal(U, first)
+
+
+def test_stream_given_as_a_ctypes_handle():
+    """A handle as C programs pass it around, with and without a workspace of the caller's."""
+    import ctypes
+    import torch
+    M, N, O, P = 40, 72, 136, 104
+    s = Step(M, N, O, P, seed=9)
+    s.run()
+    want = s.take()
+    st = torch.cuda.Stream()
+    for handle in (ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p(None), ctypes.c_void_p(0)):
+        for ws in (None, s.ws):
+            y, dn = torch.full_like(want["y"], float("nan")), torch.full_like(want["dn"], float("nan"))
+            torch.cuda.synchronize()
+            ffn.ffn_swiglu_forward(want["n"], *s.w, y, ws=ws and ws["fwd"], stream=handle)
+            ffn.ffn_swiglu_backward(want["n"], *s.w, s.dy, dn, s.out["dWg"], s.out["dWu"], s.out["dWd"],
+                                    ws=ws and ws["bwd"], stream=handle)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want["y"]) and torch.equal(dn, want["dn"])

@@ -253,6 +253,8 @@ def _own_workspace(nbytes, device, stream):
     runs on: on another one the fill could come after the kernels' first writes, and the memory
     could be given to other work before the last ones."""
     import torch
+    if stream is not None:
+        stream = getattr(stream, "value", stream) or 0   # (a ctypes handle; NULL's value is None)
     if stream is None or stream == _stream(None):
         return workspace(nbytes, device)
     on = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
