@@ -44,3 +44,30 @@ def test_decode_stream_after_side_streams(gated):
         assert torch.equal(Y, first)
         assert torch.equal(call(st.cuda_stream), first)
     assert not bool(torch.isnan(first).any())
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_decode_stream_after_side_streams_ordered(gated):
+    """Y's fill has ended before a call on another stream than the current one begins."""
+    import torch
+    M, N, O, P = 4, 4096, 512, 4096
+    X, W, Wd = _operands(M, N, O, P, gated)
+
+    def call(stream=None):
+        Y = torch.full((M, P), float("nan"), dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        if gated:
+            ffn.ffn_swiglu_forward(X, *W, Wd, Y, variant=ffn.VARIANT_DECODE, stream=stream)
+        else:
+            ffn.ffn_forward_ex(X, W[0], None, Wd, None, Y, variant=ffn.VARIANT_DECODE, stream=stream)
+        torch.cuda.synchronize()
+        return Y
+    first = call()
+    assert not bool(torch.isnan(first).any())
+    for k in range(1, 6):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            torch.zeros(8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(call(), first), k
+        assert torch.equal(call(st.cuda_stream), first), k
