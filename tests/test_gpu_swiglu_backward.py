@@ -147,3 +147,18 @@ def test_infinite_and_nan_inputs_stay_in_their_rows():
     keep = torch.arange(70, device="cuda") != 33
     assert torch.equal(out["dX"][keep], clean["dX"][keep]) and bool(torch.isnan(out["dX"][33]).all())
     assert bool(torch.isnan(out["dWg"]).all())
+
+
+@pytest.mark.parametrize("shape", [
+    (9, 4296, 3776, 3896),       # dWg | dWu and dWd in tiles of 256 x 256
+    (898, 4296, 3936, 4072),     # ... dWg | dWu with a split rest
+    (5393, 144, 3192, 4792),     # dWg | dWu in tiles of 256 x 128, in five joined splits
+    (3163, 8, 3464, 4504),       # ... of 128 x 128, in nine
+    (1697, 4528, 1488, 208),     # dWd of 128 x 128, in three
+    (542, 4264, 3728, 4552),     # ... with a split rest
+    (1013, 2056, 1400, 1992),    # the three output products in one launch
+])
+def test_fp32_gradients_of_every_tile(shape):
+    print(f"case swiglu backward {shape} fp32 gradients", flush=True)
+    x, out = make(*shape, seed=4, grad_f32=True)
+    ref.check(run(x, out), ref.swiglu_backward(*x.values(), grad_f32=True), str(shape))
