@@ -169,3 +169,23 @@ def test_backward_where_mean_times_rstd_leaves_fp32(N, dtype):
     assert torch.equal(f["Y"][4], x["beta"]) and torch.equal(f["Y"][17], x["beta"])
     b = backward(x, f["mean"], f["rstd"])
     ref.check(b, ref.layernorm_backward(x["X"], x["dY"], x["gamma"], f["mean"], f["rstd"]), f"N = {N}")
+
+
+@pytest.mark.parametrize("M,N,dtype", [
+    (1100, 4104, "bfloat16"), (2053, 520, "float32"), (5000, 24, "bfloat16"),   # many rows, the next rows in flight
+    (1030, 12296, "bfloat16"), (1030, 12296, "float32"),                        # ... of eight waves
+    (5, 12296, "float32"), (300, 16384, "float32"), (520, 8200, "float32"),     # x and dy read again for dx
+])
+def test_in_place_many_and_wide_rows(M, N, dtype):
+    import torch
+    print(f"case layer norm in place {M} x {N} {dtype}", flush=True)
+    x = make(M, N, getattr(torch, dtype), seed=M + N)
+    f = forward(x)
+    y = x["X"].clone()
+    again = forward({**x, "X": y}, Y=y)
+    assert all(torch.equal(again[k], f[k]) for k in f)
+    b = backward(x, f["mean"], f["rstd"])
+    for name in ("X", "dY"):
+        z = {**x, name: x[name].clone()}
+        again = backward(z, f["mean"], f["rstd"], dX=z[name])
+        assert all(torch.equal(again[k], b[k]) for k in b), name
