@@ -17,8 +17,10 @@
 // rounding of the same size to dX and the weight gradients.
 //
 // Bound: the eight products, 12 M N O + 4 M O P operations (gemm16.h).  Every
-// output element is one workgroup's sum over the whole depth in a fixed order: no
-// atomics, bitwise reproducible.
+// output element is a sum in a fixed order: one workgroup's over the whole depth, or,
+// where a tile's depth is split, of up to 16 workgroups' parts, which the last to
+// arrive adds in ascending order (tile_join; an integer counter per tile tells who is
+// last).  No floating-point atomics, bitwise reproducible.
 #include "ffn_device.h"
 #include "ffn_internal.h"
 #include "gemm16.h"
@@ -39,7 +41,7 @@ struct SwigluBackwardArgs {
     int64_t full;       // tiles of this step that are not split ...
     int splits;         // ... and into how many the others are
     int64_t clear;      // counters that the first step sets to 0
-    uint32_t from[3];   // the last three steps in one launch: first workgroup of each
+    uint32_t from_gu, from_dd;   // dX, dWg | dWu and dWd in one launch: first workgroups of the latter
 };
 
 // The steps above.  GATED's tile holds the gate's columns in its first half and
@@ -244,12 +246,12 @@ __global__ __launch_bounds__(Cfg::kThreads) void swiglu_backward_outputs_kernel(
     const uint32_t w = blockIdx.x;
     // dX first: its tiles are the deep ones where there are few tokens, and a join is
     // best behind other tiles' work
-    if (w < g.from[1])
+    if (w < g.from_gu)
         run_step<Cfg, STEP_DX, false>(smem, g, w, (uint32_t)g.full, (uint32_t)g.splits);
-    else if (w < g.from[2])
-        run_step<Cfg, STEP_DGU, kGradF32>(smem, g, w - g.from[1], 0x7fffffffu, 1);
+    else if (w < g.from_dd)
+        run_step<Cfg, STEP_DGU, kGradF32>(smem, g, w - g.from_gu, 0x7fffffffu, 1);
     else
-        run_step<Cfg, STEP_DD, kGradF32>(smem, g, w - g.from[2], 0x7fffffffu, 1);
+        run_step<Cfg, STEP_DD, kGradF32>(smem, g, w - g.from_dd, 0x7fffffffu, 1);
 }
 
 template <class Cfg, class Kernel>
@@ -325,9 +327,8 @@ hipError_t launch_outputs(SwigluBackwardArgs g, const TilePlan& plan, hipStream_
     const int64_t grid_x = tile_grid(step_tiles<STEP_DX>(plan.tile, M, N, O, P), plan.full, plan.splits);
     const int64_t gu = step_tiles<STEP_DGU>(plan.tile, M, N, O, P), dd = step_tiles<STEP_DD>(plan.tile, M, N, O, P);
     const int64_t grid_gu = tile_grid(gu, gu, 1), grid_dd = tile_grid(dd, dd, 1);
-    g.from[0] = 0;
-    g.from[1] = (uint32_t)grid_x;
-    g.from[2] = (uint32_t)(grid_x + grid_gu);
+    g.from_gu = (uint32_t)grid_x;
+    g.from_dd = (uint32_t)(grid_x + grid_gu);
     const int64_t at = grid_x + grid_gu + grid_dd;
     static std::atomic<bool> lds_set[kMaxDevices] = {};
     return launch_kernel<TileSmall>(swiglu_backward_outputs_kernel<TileSmall, kGradF32>, lds_set, g, at, stream);
@@ -435,7 +436,7 @@ hipError_t launch_swiglu_backward(const SwigluBackwardIO& io, hipStream_t stream
     g.splits = 1;
     g.full = 0;
     g.clear = 0;
-    for (uint32_t& w : g.from) w = 0;
+    g.from_gu = g.from_dd = 0;
     return io.grad_f32 ? launch_all<true>(g, L.counters, stream) : launch_all<false>(g, L.counters, stream);
 }
 

@@ -40,10 +40,11 @@
 // 2235 measured.  8192 x 8192 x 8192 bf16: 729 us, 1500 TFLOP/s at the 1.9 GHz
 // that the card holds under this load.
 //
-// K past its end reads zeros in both operands (a k-strided operand through the
-// resource's exact size, a k-contiguous one through an offset out of range), so
-// values behind the end of a row never meet a product; indices past I or J read
-// zeros or other rows and only reach outputs that are not stored.
+// K past its end reads zeros in both operands, of either kind: in the last k-tile the
+// lanes whose k lies past K (HalfLoads::past) load from an offset out of range, so
+// values behind the end of a row or a matrix never meet a product.  Indices past I or
+// J read zeros in the same way (HalfLoads::off) and only reach outputs that are not
+// stored.
 #pragma once
 
 #include <type_traits>

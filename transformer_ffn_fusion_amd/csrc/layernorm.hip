@@ -376,8 +376,10 @@ int64_t ln_backward_blocks(int64_t M, int64_t N) {
     const LnShape s = ln_shape(N, kLnThreads);
     const int64_t need = (M + s.G - 1) / s.G;
     // Two turns: as many workgroups as take two each, for fewer partial rows and no
-    // workgroup that is done after one (fp32: 300 x 16384 28.5 -> 24.2 us, 1013 x 2056 12.8
-    // -> 12.5).  With more turns the loads of all CUs count (5000 x 2048 26.5, balanced 28.3).
+    // workgroup that is done after one.  Whole calls, unbalanced -> balanced, bf16: 300 x 16384
+    // 21.4 -> 18.6 us, 600 x 4096 13.0 -> 12.3, 1013 x 2056 11.8 -> 11.6, 384 x 8192 14.1 -> 14.6,
+    // 8000 x 512 11.8 -> 12.6; fp32: 31.7 -> 23.8, 14.6 -> 14.0, 13.0 -> 13.1, 16.5 -> 16.9, 13.2 ->
+    // 14.8.  With more turns the loads of all CUs count (5000 x 2048 fp32 26.5, balanced 28.3).
     if (need > kLnBackwardBlocks && need <= 2 * kLnBackwardBlocks) return (need + 1) / 2;
     return need < kLnBackwardBlocks ? need : kLnBackwardBlocks;
 }

@@ -414,10 +414,11 @@ hipError_t launch_product(OrthoArgs g, int64_t batch, hipStream_t stream) {
 // reads; A and the polynomial then lie where it was.
 //
 // Against the tiled products of this file (17 launches), fp32: one 128 x 512 113 -> 68 us, 256 of
-// them 777 -> 94 us, 4096 of 32 x 32 5734 -> 633 us.  Bound: one CU.  A step of 128 x 512
-// takes 11 us, about 27000 clocks: LDS reads 768 KB for A (6144 clocks at 128 B) and 512 KB
-// for X, 9200 of matrix instructions and as many of vector instructions per SIMD, six
-// barriers, and little of it at the same time.
+// them 777 -> 86 us, 4096 of 32 x 32 5734 -> 633 us.  What bounds it is that little of its work
+// overlaps: a step of 128 x 512 takes 11 us, about 27000 clocks, for LDS reads of 768 KB for A
+// (6144 clocks at 128 B) and 512 KB for X (4096), 9200 clocks of matrix instructions and as many
+// of vector instructions per SIMD, one after the other between six barriers.  A and A^2 are
+// computed in full, although they are symmetric.
 constexpr int kSmallM = 128, kSmallN = 512, kSmallThreads = 512;
 constexpr int kSquareLd = 2 * kSmallM + 16;   // bytes of a row of A or the polynomial: no conflicts
 constexpr int kSquare = kSmallM * kSquareLd;
@@ -686,7 +687,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const void* 
             }
         }
     }
-    // the pair's 22 bits as bf16
+    // the pair as bf16 (its 22 bits are a rounding of 2^-14 of bf16's)
     asm volatile("" : "+v"(li), "+v"(g));
 #pragma unroll
     for (int c = 0; c < 4; ++c)
