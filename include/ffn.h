@@ -43,7 +43,8 @@
  *    calls with the same inputs give bitwise-identical outputs.
  *  - Aliasing.  Outputs must not overlap any input or the workspace (the
  *    training operators -- SwiGLU backward, layer norm, orthogonalised update --
- *    refuse it with FFN_EINVAL; the layer norm may run in place, as it says).
+ *    and those around an expert sub-layer -- RMS norm, dispatch, combine, 4-bit
+ *    products -- refuse it with FFN_EINVAL; some may run in place, as they say).
  */
 #ifndef FFN_MI355X_H
 #define FFN_MI355X_H
@@ -55,7 +56,7 @@
 extern "C" {
 #endif
 
-typedef enum { FFN_F32 = 0, FFN_BF16 = 1 } ffn_dtype_t;
+typedef enum { FFN_F32 = 0, FFN_BF16 = 1, FFN_E4M3 = 2 } ffn_dtype_t;   /* E4M3: moe_dispatch alone */
 
 /* act1 / act2.  GELU_TANH is 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))). */
 typedef enum { FFN_ACT_NONE = 0, FFN_ACT_RELU = 1, FFN_ACT_GELU_TANH = 2 } ffn_act_t;
@@ -270,6 +271,46 @@ int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, con
                            int64_t N, int dtype, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* ---------------------------------------------------------------- RMS norm
+ * The norm in front of the FFN without a mean, with the residual's addition in
+ * front of it, and its gradients:
+ *
+ *   s = x + r, rounded once to the data's type (s = x where R is NULL)
+ *   rstd = 1 / sqrt(sum_j s_j^2 / N + eps),  y_j = s_j rstd gamma_j
+ *
+ *   z = s rstd, t = dy gamma
+ *   dx = rstd (t - z sum_j t_j z_j / N) + ds        (the gradient of x and of r)
+ *   dgamma = column sums of dy z
+ *
+ * X, R, S, Y, dY, dS, dX: M x N; gamma: N; all in `dtype` (FFN_BF16 or FFN_F32).
+ * rstd: M fp32 (the forward writes it unless it is NULL; the backward reads it).
+ * S is written where R is given and must be NULL where it is not; the backward
+ * takes S (X without a residual), and in dS, which may be NULL, the gradient that
+ * reaches S by the residual path.  dgamma: N fp32.  Statistics and sums are fp32 in
+ * a fixed order: squares whose sum leaves fp32 (|s| from about 1e18 on) give y = 0 or
+ * NaN.  A NaN in a row makes the row NaN.  N a multiple of 8 up to 16384; eps > 0 (so
+ * that rows of zeros, as padding leaves them, give zeros).
+ *
+ * 8-bit output: Q holds y / scale as OCP e4m3 codes (round to nearest even; M x N
+ * bytes), from y before any rounding, with one fp32 scale per row and `group`
+ * columns: scale = max(max |y|, 2^-100) / 448.  group is 128 (scale: M x
+ * ceil(N / 128)) or 0 for whole rows (scale: M).
+ *
+ * S may be X or R itself, Y may be X where there is no R, and dX may be S, dY or
+ * dS.  With M == 0 the forward does nothing and the backward zero-fills dgamma. */
+int ffn_rmsnorm_forward(const void* X, const void* R, const void* gamma, void* S, void* Y,
+                        float* rstd, int64_t M, int64_t N, int dtype, float eps, void* stream);
+
+int ffn_rmsnorm_q8_forward(const void* X, const void* R, const void* gamma, void* S, void* Q,
+                           float* scale, float* rstd, int64_t M, int64_t N, int dtype, int group,
+                           float eps, void* stream);
+
+size_t ffn_rmsnorm_backward_workspace_size(int64_t M, int64_t N, int dtype);
+
+int ffn_rmsnorm_backward(const void* S, const void* dY, const void* dS, const void* gamma,
+                         const float* rstd, void* dX, float* dgamma, int64_t M, int64_t N, int dtype,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- orthogonalised update
  * The update of a weight matrix by Newton-Schulz steps on its gradient (or
  * momentum):
@@ -361,6 +402,126 @@ int moe_ffn_forward_router(const void* X, const void* Wr, const float* br, int64
                            int act2, float* logits_out, int32_t* topk_ids, float* topk_w,
                            int32_t* expert_offsets, int32_t* sorted_entries, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- MoE: rows by expert and back
+ * The steps around the experts by themselves, for experts that are computed
+ * elsewhere (the SwiGLU form and its gradients per expert, the 4-bit products
+ * below).  Entry t*k+s is token t's s-th choice, topk_ids[t][s] its expert; an
+ * entry whose id is not in [0, E) is dropped (a choice beyond an expert's
+ * capacity, an expert of another process).  A token may name an expert more than once.
+ *
+ * Dispatch: the kept entries by expert, within an expert in ascending order of the
+ * entries.  positions[t][s] is entry t*k+s's place (-1 where it is dropped),
+ * sorted_entries[p] the entry at place p, expert_offsets (E+1) the first place of each
+ * expert ([E] = number of kept entries K), Xs[p] = X[sorted_entries[p] / k].
+ * sorted_entries, Xs and scale_sorted have M*k rows; those from K on are left as they
+ * were.  X, Xs: M x N and M*k x N in `dtype` (FFN_BF16, FFN_F32 or FFN_E4M3); scale,
+ * scale_sorted: M x scale_cols and M*k x scale_cols fp32, carried along with the rows
+ * (both may be NULL).  N a multiple of 8 below 2^23.
+ *
+ * Combine: Y[t] = R[t] + sum over s, ascending, of topk_w[t][s] Ys[positions[t][s]],
+ * summed in fp32 and rounded once; Ys: `rows` x N, R (M x N) may be NULL, topk_w may be
+ * NULL for weights of 1 (which makes it the dispatch's gradient, moe_dispatch_backward).
+ * Positions outside [0, rows) are dropped entries: they add nothing.
+ *
+ * Combine's gradients: dYs[positions[t][s]] = topk_w[t][s] dY[t] (topk_w NULL: dY[t]),
+ * dw[t][s] = <Ys[positions[t][s]], dY[t]> in fp32 (0 for dropped entries; dw and Ys may
+ * both be NULL).  Rows of dYs that no position names are left as they were; positions
+ * that name one row twice leave either's value there.
+ *
+ * Routing's gradient: with w the softmax over a token's k chosen logits,
+ * dlogits[t][topk_ids[t][s]] = w_s (dw_s - sum_j w_j dw_j), all else 0.  Takes the ids that
+ * the router gave: an id outside [0, E) is in the sum, but has no logit.
+ *
+ * Data in `dtype` (FFN_BF16 or FFN_F32 but for dispatch), row-major; 1 <= E <= 256,
+ * 1 <= k <= 8, M*k below 2^31.  Y may be R itself and dYs may be Ys.  With M == 0 the
+ * dispatch zero-fills expert_offsets; the others do nothing. */
+size_t moe_dispatch_workspace_size(int64_t M, int64_t E, int k);
+
+int moe_dispatch(const void* X, const int32_t* topk_ids, const float* scale, int64_t M, int64_t N,
+                 int64_t E, int k, int dtype, int64_t scale_cols, void* Xs, float* scale_sorted,
+                 int32_t* expert_offsets, int32_t* sorted_entries, int32_t* positions,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+int moe_dispatch_backward(const void* dXs, const int32_t* positions, void* dX, int64_t M, int64_t N,
+                          int k, int64_t rows, int dtype, void* stream);
+
+int moe_combine(const void* Ys, const int32_t* positions, const float* topk_w, const void* R, void* Y,
+                int64_t M, int64_t N, int k, int64_t rows, int dtype, void* stream);
+
+int moe_combine_backward(const void* dY, const void* Ys, const int32_t* positions,
+                         const float* topk_w, void* dYs, float* dw, int64_t M, int64_t N, int k,
+                         int64_t rows, int dtype, void* stream);
+
+int moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* dw, float* dlogits,
+                       int64_t M, int64_t E, int k, void* stream);
+
+/* ---------------------------------------------------------------- 4-bit weights
+ * Products of few rows with weights of 4 bits and group scales, for single-token
+ * decoding (K x C weights; bf16 X and Y, fp32 sums, one rounding):
+ *
+ *     Y = act(X W + b)                       ffn_q4_matvec
+ *     H = silu(X Wg) * (X Wu)                ffn_q4_swiglu
+ *
+ *   FFN_Q4_INT:  W[k][c] = (q[k][c] - z) s, z and s of column c and k's group; z = 8
+ *                without zero points
+ *   FFN_Q4_E2M1: W[k][c] = e2m1(q[k][c]) s (OCP FP4: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and sign)
+ *
+ * `group` consecutive k (32, 64 or 128) share s and z, both bf16.
+ *
+ * Packed layout (ffn_q4_quantize and ffn_q4_pack write it), in tiles of 16 columns x
+ * 128 k, ct = c / 16 of ceil(C / 16), kt = k / 128 of ceil(K / 128):
+ *   codes    uint8 [ct][kt][1024]: 32-bit word (l, j), l < 64, j < 4, at byte 16 l + 4 j,
+ *            holds column c % 16 = l % 16 and k % 128 = 32 j + 8 (l / 16) + e, e < 8, at bits
+ *            4 p .. 4 p + 3: p = e for FFN_Q4_E2M1, p = e / 2 + 4 (e % 2) for FFN_Q4_INT
+ *   scale, zero   bf16 [ct][kt][16][128 / group]: column c % 16, group (k % 128) / group
+ * Codes past K or C may be anything, and so may scales and zeros of whole groups past K
+ * and of columns past C.
+ *
+ * The moe_ forms take E matrices ([E] in front of the layout and of a bias of E x C) and
+ * the rows sorted by expert: rows expert_offsets[e] .. expert_offsets[e + 1] of X go
+ * through matrix e (as moe_dispatch gives them); rows outside the lists are left as they
+ * were in Y.  Offsets are read on the device and kept inside [0, rows].
+ *
+ * K, C multiples of 8 below 2^22, K * C below 2^31; M <= 16, and up to 4096 rows in the
+ * moe_ forms, whose weights are read once per 16 rows of an expert.  A row with an
+ * infinity, or whose integers' partial sums leave fp32 (|x| from about 1e36 on), gives
+ * NaN or infinity.  With no rows nothing is done. */
+typedef enum { FFN_Q4_INT = 0, FFN_Q4_E2M1 = 1 } ffn_q4_t;
+
+/* Bytes of the packed codes of one matrix (0 if the shape is invalid). */
+size_t ffn_q4_bytes(int64_t K, int64_t C);
+
+int ffn_q4_matvec(const void* X, const void* Wq, const void* scale, const void* zero,
+                  const void* bias, void* Y, int64_t M, int64_t K, int64_t C, int code, int group,
+                  int act, void* stream);
+
+int ffn_q4_swiglu(const void* X, const void* Wg, const void* scale_g, const void* zero_g,
+                  const void* Wu, const void* scale_u, const void* zero_u, void* H, int64_t M,
+                  int64_t K, int64_t C, int code, int group, void* stream);
+
+int moe_q4_matvec(const void* X, const int32_t* expert_offsets, const void* Wq, const void* scale,
+                  const void* zero, const void* bias, void* Y, int64_t rows, int64_t E, int64_t K,
+                  int64_t C, int code, int group, int act, void* stream);
+
+int moe_q4_swiglu(const void* X, const int32_t* expert_offsets, const void* Wg, const void* scale_g,
+                  const void* zero_g, const void* Wu, const void* scale_u, const void* zero_u,
+                  void* H, int64_t rows, int64_t E, int64_t K, int64_t C, int code, int group,
+                  void* stream);
+
+/* Codes, scales and (zero != NULL, FFN_Q4_INT) zero points of W (K x C, `dtype`: FFN_BF16 or
+ * FFN_F32), rounding to nearest under the scale as it is kept in bf16:
+ *   FFN_Q4_INT   s = max |w| / 7, q = round(w / s) + 8; with zero points s = (hi - lo) / 15 with
+ *                lo = min(w, 0), hi = max(w, 0), z = round(-lo / s), q = round(w / s) + z in 0..15
+ *   FFN_Q4_E2M1  s = max |w| / 6, q the nearest code to w / s, ties to the even one
+ * A group whose largest magnitude is below 2^-100 becomes zeros with s = 0.  W is finite. */
+int ffn_q4_quantize(const void* W, void* Wq, void* scale, void* zero, int64_t K, int64_t C,
+                    int dtype, int code, int group, void* stream);
+
+/* Codes (uint8, K x C, the low four bits), scales and zeros (bf16, ceil(K / group) x C; zero_in
+ * and zero NULL together) of another quantiser into the packed layout. */
+int ffn_q4_pack(const void* codes, const void* scale_in, const void* zero_in, void* Wq, void* scale,
+                void* zero, int64_t K, int64_t C, int code, int group, void* stream);
 
 /* Text describing the last non-zero return on this host thread ("" if none). */
 const char* ffn_last_error(void);

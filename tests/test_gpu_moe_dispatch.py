@@ -1,0 +1,224 @@
+"""GPU parity of the dispatch of tokens to experts, the combine, their gradients and the routing's
+gradient: the sort and the copies bit for bit, sums within the bounds of sublayer_ref."""
+from __future__ import annotations
+
+import pytest
+
+import transformer_ffn_fusion_amd as ffn
+
+import sublayer_ref as ref
+
+pytestmark = pytest.mark.gpu
+# (M, N, E, k): one token; few tokens; around 1024 entries, where the sort becomes launches of its
+# own; many entries, more than one turn of a sort workgroup; every k
+CASES = [(1, 8, 1, 1), (1, 4096, 8, 2), (16, 4096, 8, 2), (3, 72, 5, 5), (128, 24, 256, 8), (341, 136, 24, 3),
+         (342, 136, 24, 3), (513, 264, 7, 2), (1013, 2056, 64, 6), (257, 8200, 100, 4), (4099, 16, 33, 7),
+         (40000, 8, 256, 8), (140001, 8, 3, 2)]
+
+
+def route(M, E, k, seed, drop=0.2):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    logits = torch.randn(M, E, generator=g) + torch.randn(E, generator=g)
+    top, ids = logits.topk(k, dim=1)
+    ids[torch.rand(M, k, generator=g) < drop] = -1
+    return ids.to(torch.int32).cuda(), torch.softmax(top, 1).cuda()
+
+
+def rows(M, N, dtype, seed):
+    import torch
+    x = torch.randn(M, N, generator=torch.Generator().manual_seed(seed))
+    return (100 * x).clamp(-448, 448).to(dtype).cuda() if dtype == torch.float8_e4m3fn else x.to(dtype).cuda()
+
+
+def dispatch(X, ids, E, scale=None, ws=None):
+    import torch
+    M, k = ids.shape
+    o = dict(Xs=torch.full((M * k, X.shape[1]), 7.0, device="cuda").to(X.dtype),
+             off=torch.full((E + 1,), -9, dtype=torch.int32, device="cuda"),
+             entries=torch.full((M * k,), -9, dtype=torch.int32, device="cuda"),
+             pos=torch.full((M, k), -9, dtype=torch.int32, device="cuda"),
+             scale=None if scale is None else torch.full((M * k, scale.shape[1]), 7.0, device="cuda"))
+    ffn.moe_dispatch(X, ids, o["Xs"], o["off"], o["entries"], o["pos"], scale=scale, scale_sorted=o["scale"], ws=ws)
+    torch.cuda.synchronize()
+    return o
+
+
+def check_dispatch(o, X, ids, E, scale=None):
+    import torch
+    k = ids.shape[1]
+    pos, off, entries = ref.sort(ids, E)
+    n = entries.numel()
+    assert torch.equal(o["off"].cpu(), off) and torch.equal(o["pos"].cpu(), pos)
+    assert torch.equal(o["entries"][:n].cpu(), entries) and bool((o["entries"][n:] == -9).all())
+    bits = torch.int32 if X.dtype == torch.float32 else torch.int16 if X.dtype == torch.bfloat16 else torch.uint8
+    got, src = o["Xs"].view(bits), X.view(bits)
+    token = (entries // k).long().cuda()
+    assert torch.equal(got[:n], src[token])
+    assert bool((o["Xs"][n:].float() == 7.0).all()), "rows behind the last kept entry"
+    if scale is not None:
+        assert torch.equal(o["scale"][:n], scale[token]) and bool((o["scale"][n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32", "float8_e4m3fn"])
+@pytest.mark.parametrize("case", CASES)
+def test_dispatch(case, dtype):
+    import torch
+    M, N, E, k = case
+    print(f"case dispatch {case} {dtype}", flush=True)
+    ids, _ = route(M, E, k, seed=M + N)
+    X = rows(M, N, getattr(torch, dtype), seed=M)
+    check_dispatch(dispatch(X, ids, E), X, ids, E)
+    scale = torch.rand(M, -(-N // 128), device="cuda")
+    check_dispatch(dispatch(X, ids, E, scale), X, ids, E, scale)
+
+
+@pytest.mark.parametrize("M", [100, 3000])
+def test_dispatch_of_unusual_ids(M):
+    """All dropped, all to one expert, the same expert twice in a token, ids far outside."""
+    import torch
+    E, k = 6, 3
+    X = rows(M, 40, torch.bfloat16, seed=M)
+    g = torch.Generator().manual_seed(5)
+    wild = torch.randint(-2 ** 31, 2 ** 31 - 1, (M, k), generator=g).to(torch.int32)
+    wild[::7] = E
+    for what, ids in (("none", torch.full((M, k), -1)), ("one", torch.full((M, k), E - 1)),
+                      ("any", torch.randint(0, E, (M, k), generator=g)), ("wild", wild),
+                      ("both ends", torch.randint(-1, E + 1, (M, k), generator=g))):
+        print(f"case dispatch of unusual ids: {what}", flush=True)
+        ids = ids.to(torch.int32).cuda()
+        check_dispatch(dispatch(X, ids, E), X, ids, E)
+
+
+def test_dispatch_agrees_with_the_router():
+    """On the router's ids the lists are the router's own."""
+    import torch
+    for M, E, k in ((16, 8, 2), (2000, 32, 4)):
+        logits = torch.randn(M, E, generator=torch.Generator().manual_seed(M)).cuda()
+        i32 = dict(dtype=torch.int32, device="cuda")
+        ids, w = torch.empty(M, k, **i32), torch.empty(M, k, device="cuda")
+        off, entries = torch.empty(E + 1, **i32), torch.empty(M * k, **i32)
+        ffn.moe_route(logits, k, ids, w, off, entries)
+        o = dispatch(rows(M, 16, torch.bfloat16, 1), ids, E)
+        assert torch.equal(o["off"], off) and torch.equal(o["entries"], entries)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("case", CASES)
+def test_combine_and_gradients(case, dtype):
+    import torch
+    M, N, E, k = case
+    print(f"case combine {case} {dtype}", flush=True)
+    dt = getattr(torch, dtype)
+    ids, w = route(M, E, k, seed=M + 2 * N)
+    pos, _, entries = ref.sort(ids, E)
+    n = max(entries.numel(), 1)
+    w[pos.cuda() < 0] = float("nan")       # a dropped entry's weight is not looked at
+    pos = pos.cuda()
+    Ys, R, dY = rows(n, N, dt, 1), rows(M, N, dt, 2), rows(M, N, dt, 3)
+    for weights, res in ((w, R), (w, None), (None, R), (None, None)):
+        Y = torch.full((M, N), float("nan"), device="cuda", dtype=dt)
+        ffn.moe_combine(Ys, pos, Y, topk_w=weights, R=res)
+        ref.check({"Y": Y}, ref.combine(Ys, pos, weights, res), f"{case} combine")
+    dX = torch.full((M, N), float("nan"), device="cuda", dtype=dt)
+    ffn.moe_dispatch_backward(Ys, pos, dX)
+    assert torch.equal(dX, Y)
+    for weights in (w, None):
+        dYs = torch.full((n, N), 7.0, device="cuda", dtype=dt)
+        dw = torch.full((M, k), float("nan"), device="cuda")
+        ffn.moe_combine_backward(dY, Ys, pos, weights, dYs, dw)
+        want, (drow, bound, kept) = ref.combine_backward(dY, Ys, pos, weights)
+        ref.check({"dw": dw}, want, f"{case} backward")
+        at = torch.where(kept, pos.cpu().long(), 0)
+        if bool(kept.any()):
+            over = ((ref.d(dYs)[at] - drow).abs() / bound)[kept]
+            print(f"  {case} dYs: worst error {float(over.max()):.3f} of its bound", flush=True)
+            assert float(over.max()) <= 1.0
+        else:
+            assert bool((dYs == 7.0).all())
+        only = torch.full((n, N), 7.0, device="cuda", dtype=dt)
+        ffn.moe_combine_backward(dY, None, pos, weights, only, None)
+        assert torch.equal(only, dYs)
+
+
+def test_positions_outside_the_rows_are_dropped():
+    import torch
+    M, N, k, n = 50, 72, 4, 60
+    g = torch.Generator().manual_seed(3)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (M, k), generator=g).to(torch.int32)
+    pos[:, 1] = torch.arange(M)
+    pos[3, 2], pos[4, 2] = n, n - 1
+    pos = pos.cuda()
+    Ys, dY = rows(n, N, torch.float32, 1), rows(M, N, torch.float32, 2)
+    w = torch.rand(M, k, generator=g).cuda()
+    Y, dYs, dw = torch.empty_like(dY), torch.full_like(Ys, 7.0), torch.empty_like(w)
+    ffn.moe_combine(Ys, pos, Y, topk_w=w)
+    ffn.moe_combine_backward(dY, Ys, pos, w, dYs, dw)
+    ref.check({"Y": Y}, ref.combine(Ys, pos, w), "wild positions")
+    ref.check({"dw": dw}, ref.combine_backward(dY, Ys, pos, w)[0], "wild positions")
+    untouched = torch.ones(n, dtype=torch.bool)
+    untouched[:M] = False
+    untouched[n - 1] = False
+    assert bool((dYs[untouched.cuda()] == 7.0).all())
+
+
+def test_in_place():
+    import torch
+    M, N, E, k = 300, 1032, 12, 3
+    ids, w = route(M, E, k, seed=1)
+    pos = ref.sort(ids, E)[0].cuda()
+    for dt in (torch.bfloat16, torch.float32):
+        Ys, R, dY = rows(M * k, N, dt, 1), rows(M, N, dt, 2), rows(M, N, dt, 3)
+        Y, dYs, dw = torch.empty_like(R), Ys.clone(), torch.empty_like(w)
+        ffn.moe_combine(Ys, pos, Y, topk_w=w, R=R)
+        over = R.clone()
+        ffn.moe_combine(Ys, pos, over, topk_w=w, R=over)
+        assert torch.equal(over, Y)
+        ffn.moe_combine_backward(dY, Ys, pos, w, dYs, dw)
+        over, dw2 = Ys.clone(), torch.empty_like(dw)
+        ffn.moe_combine_backward(dY, over, pos, w, over, dw2)
+        assert torch.equal(over, dYs) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("M,E,k", [(1, 1, 1), (1, 8, 2), (77, 24, 3), (1013, 256, 8), (20000, 300 - 44, 8)])
+def test_route_backward(M, E, k):
+    import torch
+    print(f"case routing backward {M} {E} {k}", flush=True)
+    ids, w = route(M, E, k, seed=M, drop=0.1)
+    ids[0, 0] = E                                    # outside: has no logit
+    if k > 1:
+        ids[-1, 1] = ids[-1, 0]                      # the same expert twice
+    dw = torch.randn(M, k, generator=torch.Generator().manual_seed(2)).cuda()
+    dl = torch.full((M, E), float("nan"), device="cuda")
+    ffn.moe_route_backward(ids, w, dw, dl)
+    ref.check({"dlogits": dl}, ref.route_backward(ids, w, dw, E), f"{M} {E} {k}")
+
+
+def test_no_tokens_and_no_rows():
+    import torch
+    ids = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    X = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    o = dispatch(X, ids, 5)
+    assert not bool(o["off"].any())
+    ffn.moe_combine(X, ids, X)
+    w = torch.empty(0, 2, device="cuda")
+    ffn.moe_combine_backward(X, X, ids, w, X, w)
+    ffn.moe_route_backward(ids, w, w, torch.empty(0, 5, device="cuda"))
+    pos = torch.full((4, 2), -1, dtype=torch.int32, device="cuda")        # every entry dropped, no rows
+    R = rows(4, 64, torch.bfloat16, 1)
+    Y = torch.empty_like(R)
+    ffn.moe_combine(X, pos, Y, topk_w=torch.ones(4, 2, device="cuda"), R=R)
+    assert torch.equal(Y, R)
+    dw = torch.full((4, 2), 7.0, device="cuda")
+    ffn.moe_combine_backward(R, X, pos, torch.ones(4, 2, device="cuda"), X, dw)
+    assert not bool(dw.any())
+
+
+def test_workspace_contents_do_not_matter():
+    import torch
+    M, E, k = 5000, 64, 4
+    ids, _ = route(M, E, k, seed=9)
+    X = rows(M, 24, torch.bfloat16, 1)
+    ws = ffn.workspace(ffn.moe_dispatch_workspace_size(M, E, k))
+    ws.fill_(0xFF)
+    check_dispatch(dispatch(X, ids, E, ws=ws), X, ids, E)

@@ -1,0 +1,224 @@
+"""GPU parity of the products with 4-bit weights, of the quantiser and of the packed layout against
+their fp64 forms, within the bounds of sublayer_ref."""
+from __future__ import annotations
+
+import pytest
+
+import transformer_ffn_fusion_amd as ffn
+
+import sublayer_ref as ref
+
+pytestmark = pytest.mark.gpu
+SHAPES = [(8, 8), (64, 16), (128, 16), (136, 24), (264, 4104), (1992, 1400), (2056, 200), (4096, 48), (4104, 264),
+          (520, 32)]     # K, C
+KINDS = [("int4", 128, False), ("int4", 64, True), ("int4", 32, False), ("int4", 128, True), ("e2m1", 32, False),
+         ("e2m1", 64, False), ("e2m1", 128, False)]
+
+
+def weight(K, C, kind, seed, experts=None):
+    """Random codes, scales of either sign and zero points; NaN in scales that nothing may look at."""
+    import torch
+    code, group, zero = kind
+    g = torch.Generator().manual_seed(seed)
+    Wq, s, z = ffn.ffn_q4_empty(K, C, group, zero, experts, device="cpu")
+    Wq = torch.randint(0, 256, Wq.shape, generator=g, dtype=torch.uint8)
+    s = (torch.exp(0.3 * torch.randn(s.shape, generator=g)) / (4 * K ** 0.5)).to(torch.bfloat16)
+    s = torch.where(torch.rand(s.shape, generator=g) < 0.1, -s, s)
+    if zero:
+        z = torch.randint(0, 16, z.shape, generator=g).to(torch.bfloat16)
+    per, kt = 128 // group, -(-K // 128)
+    for p in range(per):
+        if (kt - 1) * 128 + p * group >= K:
+            s[..., kt - 1, :, p] = float("nan")
+            if zero:
+                z[..., kt - 1, :, p] = float("nan")
+    if C % 16:
+        s[..., -1, :, C % 16:, :] = float("nan")
+    return Wq.cuda(), s.cuda(), None if z is None else z.cuda()
+
+
+def inputs(M, K, seed):
+    import torch
+    return torch.randn(M, K, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+
+
+def empty(M, C):
+    import torch
+    return torch.full((M, C), float("nan"), dtype=torch.bfloat16, device="cuda")
+
+
+def cpu(w):
+    return [None if t is None else t.cpu() for t in w]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_matvec(shape, kind):
+    import torch
+    K, C = shape
+    code = kind[0]
+    print(f"case 4-bit product {shape} {kind}", flush=True)
+    w = weight(K, C, kind, seed=K + C)
+    bias = torch.randn(C, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    for M, act, b in ((1, "none", None), (5, "gelu_tanh", bias), (16, "relu", bias), (13, "none", bias)):
+        X, Y = inputs(M, K, M), empty(M, C)
+        ffn.ffn_q4_matvec(X, w[0], w[1], Y, zero=w[2], bias=b, act=act, code=code)
+        ref.check({"Y": Y}, ref.q4_matvec(X, *cpu(w), b, act, C, code), f"{shape} {kind} {M} rows")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_swiglu(shape, kind):
+    K, C = shape
+    print(f"case 4-bit gated pair {shape} {kind}", flush=True)
+    wg, wu = weight(K, C, kind, 1), weight(K, C, kind, 2)
+    for M in (1, 16, 7):
+        X, H = inputs(M, K, M), empty(M, C)
+        ffn.ffn_q4_swiglu(X, wg[0], wg[1], wu[0], wu[1], H, zero_g=wg[2], zero_u=wu[2], code=kind[0])
+        ref.check({"H": H}, ref.q4_swiglu(X, *cpu(wg), *cpu(wu), C, kind[0]), f"{shape} {kind} {M} rows")
+
+
+# rows per expert: none, one, a full tile, more than one tile, more than two
+LISTS = [[1], [0, 0, 3, 0], [1, 0, 16, 17, 2], [5, 40, 0, 33, 1, 0, 16], [0, 0, 0]]
+
+
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[1], KINDS[4]])
+@pytest.mark.parametrize("counts", LISTS)
+@pytest.mark.parametrize("shape", [(136, 24), (1032, 200), (512, 64)])
+def test_experts(shape, counts, kind):
+    import torch
+    K, C = shape
+    code, E = kind[0], len(counts)
+    print(f"case 4-bit experts {shape} {counts} {kind}", flush=True)
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    n = int(off[-1])
+    X, Y, H = inputs(n + 3, K, 4), empty(n + 3, C), empty(n + 3, C)     # three rows of no expert
+    wg, wu = weight(K, C, kind, 1, E), weight(K, C, kind, 2, E)
+    bias = torch.randn(E, C, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    Y.fill_(7.0)
+    H.fill_(7.0)
+    ffn.moe_q4_matvec(X, off, wg[0], wg[1], Y, zero=wg[2], bias=bias, act="gelu_tanh", code=code)
+    ffn.moe_q4_swiglu(X, off, wg[0], wg[1], wu[0], wu[1], H, zero_g=wg[2], zero_u=wu[2], code=code)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            continue
+        g, u = ([None if t is None else t[e].cpu() for t in w] for w in (wg, wu))
+        ref.check({"Y": Y[lo:hi]}, ref.q4_matvec(X[lo:hi], *g, bias[e], "gelu_tanh", C, code), f"expert {e}")
+        ref.check({"H": H[lo:hi]}, ref.q4_swiglu(X[lo:hi], *g, *u, C, code), f"expert {e}")
+    assert bool((Y[n:] == 7.0).all()) and bool((H[n:] == 7.0).all())
+
+
+def test_offsets_outside_the_rows():
+    """Offsets that decrease or leave the rows: every row that is written belongs to the list as it is
+    kept inside the rows."""
+    import torch
+    K, C, kind = 136, 24, KINDS[0]
+    w = weight(K, C, kind, 1, 3)
+    X, Y = inputs(20, K, 4), empty(20, C)
+    Y.fill_(7.0)
+    off = torch.tensor([-5, 4, 2, 2 ** 31 - 1], dtype=torch.int32, device="cuda")    # 0..4, none, 2..20
+    ffn.moe_q4_matvec(X, off[:2].clone(), w[0][:1].contiguous(), w[1][:1].contiguous(), Y)
+    ref.check({"Y": Y[:4]}, ref.q4_matvec(X[:4], w[0][0].cpu(), w[1][0].cpu(), None, None, "none", C, "int4"), "first")
+    assert bool((Y[4:] == 7.0).all())
+    Z = empty(20, C)
+    Z.fill_(7.0)
+    ffn.moe_q4_matvec(X, off[1:].clone(), w[0][1:].contiguous(), w[1][1:].contiguous(), Z)
+    ref.check({"Y": Z[2:]}, ref.q4_matvec(X[2:], w[0][2].cpu(), w[1][2].cpu(), None, None, "none", C, "int4"), "last")
+    assert bool((Z[:2] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", [(8, 8), (136, 24), (300 * 8, 72), (520, 200)])
+def test_quantize(shape, kind, dtype):
+    """Scales, zero points and codes are what the same fp32 steps give on the CPU."""
+    import torch
+    K, C = shape
+    code, group, zero = kind
+    print(f"case quantise {shape} {kind} {dtype}", flush=True)
+    g = torch.Generator().manual_seed(K)
+    W = (torch.randn(K, C, generator=g) * torch.exp(torch.randn(1, C, generator=g))).to(getattr(torch, dtype))
+    W[:, 1] = 0
+    W[:, 2] = W[:, 2].abs()
+    W[:, 3] *= 2.0 ** -120
+    Wq, s, z = ffn.ffn_q4_empty(K, C, group, zero)
+    ffn.ffn_q4_quantize(W.cuda(), Wq, s, zero=z, code=code)
+    G = -(-K // group)
+    w = torch.nn.functional.pad(W.float(), (0, 0, 0, G * group - K)).reshape(G, group, C)
+    lo, hi = w.amin(1).clamp(max=0), w.amax(1).clamp(min=0)
+    top = torch.maximum(-lo, hi)
+    want = top / 6 if code == "e2m1" else (hi - lo) / 15 if zero else top / 7
+    want = torch.where(top < 2.0 ** -100, 0.0, want).to(torch.bfloat16).float()
+    got = ref.q4_groups(s, K, C)[::group].float()
+    assert torch.equal(got, want)
+    wz = torch.full_like(want, 8.0)
+    if zero:
+        wz = torch.where(want > 0, torch.round(-lo / want).clamp(0, 15), 8.0)
+        assert torch.equal(ref.q4_groups(z, K, C)[::group].float(), wz)
+    v = torch.where(want[:, None] > 0, w / want[:, None], 0.0)
+    q = ref.q4_codes(Wq, K, C, code)
+    if code == "e2m1":
+        v = v.reshape(-1, C)[:K].double()
+        near = (ref.E2M1[q] - v).abs()
+        best = (ref.E2M1[None, None, :8] - v.abs()[:, :, None]).abs().amin(2)
+        assert torch.equal(near, best) and bool((ref.E2M1[q] * v >= 0).all())
+        tie = ((ref.E2M1[None, None, :8] - v.abs()[:, :, None]).abs() == best[:, :, None]).sum(2) > 1
+        assert not bool((q[tie] & 1).any())
+    else:
+        want_q = (torch.round(v) + wz[:, None]).clamp(0, 15).reshape(-1, C)[:K]
+        assert torch.equal(q.float(), want_q)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", [(8, 8), (136, 24), (520, 200)])
+def test_pack(shape, kind):
+    import torch
+    K, C = shape
+    code, group, zero = kind
+    g = torch.Generator().manual_seed(K)
+    q = torch.randint(0, 16, (K, C), generator=g).to(torch.uint8)
+    G = -(-K // group)
+    sin = torch.randn(G, C, generator=g).to(torch.bfloat16)
+    zin = torch.randint(0, 16, (G, C), generator=g).to(torch.bfloat16) if zero else None
+    Wq, s, z = ffn.ffn_q4_empty(K, C, group, zero)
+    Wq.fill_(0xFF)
+    ffn.ffn_q4_pack(q.cuda() | 0xF0, sin.cuda(), Wq, s, zero_in=None if zin is None else zin.cuda(), zero=z, code=code)
+    assert torch.equal(ref.q4_codes(Wq, K, C, code), q.long())
+    k = torch.arange(K) // group
+    assert torch.equal(ref.q4_groups(s, K, C), sin.double()[k])
+    if zero:
+        assert torch.equal(ref.q4_groups(z, K, C), zin.double()[k])
+    want = ref.q4_pack(q, torch.zeros_like(Wq).cpu(), code)
+    assert torch.equal(ref.q4_codes(want, K, C, code), q.long())
+
+
+def test_rows_with_nan_and_infinity_stay_alone():
+    import torch
+    K, C = 264, 40
+    for kind in (KINDS[1], KINDS[4]):
+        w = weight(K, C, kind, 3)
+        X, Y, Z = inputs(9, K, 1), empty(9, C), empty(9, C)
+        ffn.ffn_q4_matvec(X, w[0], w[1], Y, zero=w[2], code=kind[0])
+        X[2, 5], X[8, 263] = float("nan"), float("inf")
+        ffn.ffn_q4_matvec(X, w[0], w[1], Z, zero=w[2], code=kind[0])
+        keep = [0, 1, 3, 4, 5, 6, 7]
+        assert torch.equal(Y[keep], Z[keep])
+        assert bool(torch.isnan(Z[2].float()).all()) and not bool(torch.isfinite(Z[8].float()).any())
+
+
+def test_no_rows_and_repeated_calls():
+    import torch
+    K, C = 520, 72
+    w = weight(K, C, KINDS[0], 3)
+    ffn.ffn_q4_matvec(inputs(0, K, 1), w[0], w[1], empty(0, C))
+    X, Y = inputs(16, K, 1), empty(16, C)
+    ffn.ffn_q4_matvec(X, w[0], w[1], Y)
+    for _ in range(20):
+        Z = empty(16, C)
+        ffn.ffn_q4_matvec(X, w[0], w[1], Z)
+        assert torch.equal(Y, Z)
+    for m in range(1, 16):         # a row's result does not depend on the rows beside it
+        Z = empty(m, C)
+        ffn.ffn_q4_matvec(X[:m], w[0], w[1], Z)
+        assert torch.equal(Y[:m], Z)

@@ -23,11 +23,18 @@ __all__ = [
     "ffn_forward_noalloc", "NOALLOC_SCRATCH_BYTES",
     "ffn_swiglu_workspace_size", "ffn_swiglu_forward", "ffn_swiglu_backward_workspace_size",
     "ffn_swiglu_backward", "ffn_layernorm_forward", "ffn_layernorm_backward_workspace_size",
-    "ffn_layernorm_backward", "ffn_orthogonalize_workspace_size", "ffn_orthogonalize",
+    "ffn_layernorm_backward", "ffn_rmsnorm_forward", "ffn_rmsnorm_q8_forward",
+    "ffn_rmsnorm_backward_workspace_size", "ffn_rmsnorm_backward",
+    "ffn_orthogonalize_workspace_size", "ffn_orthogonalize",
     "moe_workspace_size", "moe_route", "moe_ffn_forward", "ffn_last_error", "workspace",
+    "moe_dispatch_workspace_size", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
+    "moe_combine_backward", "moe_route_backward", "Q4_INT", "Q4_E2M1", "ffn_q4_bytes", "ffn_q4_empty",
+    "ffn_q4_quantize", "ffn_q4_pack", "ffn_q4_matvec", "ffn_q4_swiglu", "moe_q4_matvec", "moe_q4_swiglu",
 ]
 
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
+Q4_INT, Q4_E2M1 = 0, 1
+Q4_CODES = {"int4": Q4_INT, "e2m1": Q4_E2M1}
 ACT_NONE, ACT_RELU, ACT_GELU_TANH = 0, 1, 2
 VARIANT_AUTO, VARIANT_FUSED, VARIANT_SKINNY, VARIANT_F32, VARIANT_DECODE = 0, 1, 2, 3, 4
 ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu_tanh": ACT_GELU_TANH}
@@ -111,6 +118,40 @@ def lib():
         L.ffn_layernorm_backward_workspace_size.restype = sz
         L.ffn_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, vp, sz, vp]
         L.ffn_layernorm_backward.restype = i32
+        L.ffn_rmsnorm_forward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, ctypes.c_float, vp]
+        L.ffn_rmsnorm_forward.restype = i32
+        L.ffn_rmsnorm_q8_forward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, ctypes.c_float, vp]
+        L.ffn_rmsnorm_q8_forward.restype = i32
+        L.ffn_rmsnorm_backward_workspace_size.argtypes = [i64, i64, i32]
+        L.ffn_rmsnorm_backward_workspace_size.restype = sz
+        L.ffn_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, vp, sz, vp]
+        L.ffn_rmsnorm_backward.restype = i32
+        L.moe_dispatch_workspace_size.argtypes = [i64, i64, i32]
+        L.moe_dispatch_workspace_size.restype = sz
+        L.moe_dispatch.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_dispatch.restype = i32
+        L.moe_dispatch_backward.argtypes = [vp, vp, vp, i64, i64, i32, i64, i32, vp]
+        L.moe_dispatch_backward.restype = i32
+        L.moe_combine.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i64, i32, vp]
+        L.moe_combine.restype = i32
+        L.moe_combine_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i64, i32, vp]
+        L.moe_combine_backward.restype = i32
+        L.moe_route_backward.argtypes = [vp, vp, vp, vp, i64, i64, i32, vp]
+        L.moe_route_backward.restype = i32
+        L.ffn_q4_bytes.argtypes = [i64, i64]
+        L.ffn_q4_bytes.restype = sz
+        L.ffn_q4_matvec.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp]
+        L.ffn_q4_matvec.restype = i32
+        L.ffn_q4_swiglu.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp]
+        L.ffn_q4_swiglu.restype = i32
+        L.moe_q4_matvec.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, i32, vp]
+        L.moe_q4_matvec.restype = i32
+        L.moe_q4_swiglu.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, vp]
+        L.moe_q4_swiglu.restype = i32
+        L.ffn_q4_quantize.argtypes = [vp, vp, vp, vp, i64, i64, i32, i32, i32, vp]
+        L.ffn_q4_quantize.restype = i32
+        L.ffn_q4_pack.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, vp]
+        L.ffn_q4_pack.restype = i32
         L.ffn_orthogonalize_workspace_size.argtypes = [i64, i64, i64, i32]
         L.ffn_orthogonalize_workspace_size.restype = sz
         L.ffn_orthogonalize.argtypes = [vp, vp, i64, i64, i64, i32, i32, vp, sz, vp]
@@ -445,6 +486,73 @@ def ffn_layernorm_backward(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws=None,
                                         ws.numel(), _stream(stream)))
 
 
+def _rmsnorm_args(X, gamma, R, S, rstd):
+    import torch
+    M, N = _dims(X, "X", 2)
+    dt = _dtype_code(X)
+    _arg(X, "X", (M, N), X.dtype)
+    _arg(gamma, "gamma", (N,), X.dtype)
+    _arg(R, "R", (M, N), X.dtype, optional=True)
+    _arg(S, "S", (M, N), X.dtype, optional=True)
+    _arg(rstd, "rstd", (M,), torch.float32, optional=True)
+    if (R is None) != (S is None):
+        raise ValueError("S is written with R alone: give both or neither")
+    return M, N, dt
+
+
+def ffn_rmsnorm_forward(X, gamma, Y, R=None, S=None, rstd=None, eps=1e-5, stream=None):
+    """``S = X + R`` (where a residual ``R`` is given) and ``Y = S rstd gamma`` over the last dimension
+    (M x N, bf16 or fp32); ``S``, ``Y`` and, when given, ``rstd`` (M, fp32) are written in place."""
+    M, N, dt = _rmsnorm_args(X, gamma, R, S, rstd)
+    _arg(Y, "Y", (M, N), X.dtype)
+    _on_device(X, gamma, Y, R, S, rstd)
+    _check(lib().ffn_rmsnorm_forward(_ptr(X), _ptr(R), _ptr(gamma), _ptr(S), _ptr(Y), _ptr(rstd), M, N, dt,
+                                     float(eps), _stream(stream)))
+    return Y
+
+
+def ffn_rmsnorm_q8_forward(X, gamma, Q, scale, R=None, S=None, rstd=None, group=128, eps=1e-5, stream=None):
+    """As ``ffn_rmsnorm_forward`` with the output as e4m3 codes ``Q`` (M x N, float8_e4m3fn) and fp32
+    ``scale``: M x ceil(N / 128) for groups of 128 columns, M x 1 for whole rows (``group=0``)."""
+    import torch
+    M, N, dt = _rmsnorm_args(X, gamma, R, S, rstd)
+    if group not in (0, 128):
+        raise ValueError(f"group must be 128, or 0 for whole rows (got {group})")
+    _arg(Q, "Q", (M, N), torch.float8_e4m3fn)
+    _arg(scale, "scale", (M, -(-N // group) if group else 1), torch.float32)
+    _on_device(X, gamma, Q, scale, R, S, rstd)
+    _check(lib().ffn_rmsnorm_q8_forward(_ptr(X), _ptr(R), _ptr(gamma), _ptr(S), _ptr(Q), _ptr(scale), _ptr(rstd),
+                                        M, N, dt, group, float(eps), _stream(stream)))
+    return Q
+
+
+def ffn_rmsnorm_backward_workspace_size(M, N, dtype=BF16) -> int:
+    return lib().ffn_rmsnorm_backward_workspace_size(M, N, dtype)
+
+
+def ffn_rmsnorm_backward(S, dY, gamma, rstd, dX, dgamma, dS=None, ws=None, stream=None):
+    """Gradients of ``ffn_rmsnorm_forward``: dX (of X and of R alike) in S's type, dgamma (N, fp32),
+    written in place.  ``S`` is the normed sum (X without a residual), ``rstd`` what the forward wrote,
+    ``dS`` the gradient that reaches S by the residual path."""
+    import torch
+    M, N = _dims(S, "S", 2)
+    dt = _dtype_code(S)
+    f32 = torch.float32
+    _arg(S, "S", (M, N), S.dtype)
+    _arg(dY, "dY", (M, N), S.dtype)
+    _arg(gamma, "gamma", (N,), S.dtype)
+    _arg(rstd, "rstd", (M,), f32)
+    _arg(dX, "dX", (M, N), S.dtype)
+    _arg(dgamma, "dgamma", (N,), f32)
+    _arg(dS, "dS", (M, N), S.dtype, optional=True)
+    _ws_arg(ws)
+    _on_device(S, dY, gamma, rstd, dX, dgamma, dS, ws)
+    if ws is None:
+        ws = _own_workspace(ffn_rmsnorm_backward_workspace_size(M, N, dt), S.device, stream)
+    _check(lib().ffn_rmsnorm_backward(_ptr(S), _ptr(dY), _ptr(dS), _ptr(gamma), _ptr(rstd), _ptr(dX), _ptr(dgamma),
+                                      M, N, dt, _ptr(ws), ws.numel(), _stream(stream)))
+
+
 def ffn_orthogonalize_workspace_size(B, R, C, dtype=BF16) -> int:
     return lib().ffn_orthogonalize_workspace_size(B, R, C, dtype)
 
@@ -573,6 +681,264 @@ def moe_ffn_forward_router(X, Wr, br, k, W1, b1, W2, b2, Y, act1="gelu_tanh", ac
                                         _ptr(expert_offsets), _ptr(sorted_entries), _ptr(ws),
                                         ws.numel(), _stream(stream)))
     return Y
+
+
+# ---------------------------------------------------------------- rows by expert and back
+
+def moe_dispatch_workspace_size(M, E, k) -> int:
+    return lib().moe_dispatch_workspace_size(M, E, k)
+
+
+def moe_dispatch(X, topk_ids, Xs, expert_offsets, sorted_entries, positions, scale=None, scale_sorted=None,
+                 ws=None, stream=None):
+    """Tokens sorted by expert: entry ``t * k + s`` of ``topk_ids`` (M x k, int32; ids outside [0, E) are
+    dropped) goes to row ``positions[t, s]`` (-1: dropped) of ``Xs`` (M*k x N), whose rows of expert e are
+    ``expert_offsets[e]`` to ``expert_offsets[e + 1]`` (E + 1, int32) and come from ``sorted_entries``
+    (M*k, int32).  X is bf16, fp32 or float8_e4m3fn; ``scale`` (M x G, fp32) travels with the rows.  Rows
+    behind the last kept entry are left as they were."""
+    import torch
+    M, N = _dims(X, "X", 2)
+    k = _dims(topk_ids, "topk_ids", 2)[1]
+    E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
+    i32 = torch.int32
+    dt = E4M3 if X.dtype == torch.float8_e4m3fn else _dtype_code(X)
+    _arg(X, "X", (M, N), X.dtype)
+    _arg(topk_ids, "topk_ids", (M, k), i32)
+    _arg(Xs, "Xs", (M * k, N), X.dtype)
+    _arg(expert_offsets, "expert_offsets", (E + 1,), i32)
+    _arg(sorted_entries, "sorted_entries", (M * k,), i32)
+    _arg(positions, "positions", (M, k), i32)
+    if (scale is None) != (scale_sorted is None):
+        raise ValueError("give scale and scale_sorted together or neither")
+    G = 0
+    if scale is not None:
+        G = _dims(scale, "scale", 2)[1]
+        if G < 1:
+            raise ValueError("scale must have columns")
+        _arg(scale, "scale", (M, G), torch.float32)
+        _arg(scale_sorted, "scale_sorted", (M * k, G), torch.float32)
+    _ws_arg(ws)
+    _on_device(X, topk_ids, Xs, expert_offsets, sorted_entries, positions, scale, scale_sorted, ws)
+    if ws is None:
+        ws = _own_workspace(moe_dispatch_workspace_size(M, E, k), X.device, stream)
+    _check(lib().moe_dispatch(_ptr(X), _ptr(topk_ids), _ptr(scale), M, N, E, k, dt, G, _ptr(Xs), _ptr(scale_sorted),
+                              _ptr(expert_offsets), _ptr(sorted_entries), _ptr(positions), _ptr(ws), ws.numel(),
+                              _stream(stream)))
+    return Xs
+
+
+def moe_dispatch_backward(dXs, positions, dX, stream=None):
+    """``dX[t] = sum_s dXs[positions[t, s]]``, the gradient of ``moe_dispatch``; written in place."""
+    import torch
+    M, N = _dims(dX, "dX", 2)
+    k = _dims(positions, "positions", 2)[1]
+    dt = _dtype_code(dX)
+    rows = _dims(dXs, "dXs", 2)[0]
+    _arg(dXs, "dXs", (rows, N), dX.dtype)
+    _arg(positions, "positions", (M, k), torch.int32)
+    _arg(dX, "dX", (M, N), dX.dtype)
+    _on_device(dXs, positions, dX)
+    _check(lib().moe_dispatch_backward(_ptr(dXs), _ptr(positions), _ptr(dX), M, N, k, rows, dt, _stream(stream)))
+    return dX
+
+
+def moe_combine(Ys, positions, Y, topk_w=None, R=None, stream=None):
+    """``Y[t] = R[t] + sum_s topk_w[t, s] Ys[positions[t, s]]`` (weights of 1 and no residual where they are
+    None; dropped entries add nothing); ``Y`` is written in place."""
+    import torch
+    M, N = _dims(Y, "Y", 2)
+    k = _dims(positions, "positions", 2)[1]
+    dt = _dtype_code(Y)
+    rows = _dims(Ys, "Ys", 2)[0]
+    _arg(Ys, "Ys", (rows, N), Y.dtype)
+    _arg(positions, "positions", (M, k), torch.int32)
+    _arg(topk_w, "topk_w", (M, k), torch.float32, optional=True)
+    _arg(R, "R", (M, N), Y.dtype, optional=True)
+    _arg(Y, "Y", (M, N), Y.dtype)
+    _on_device(Ys, positions, topk_w, R, Y)
+    _check(lib().moe_combine(_ptr(Ys), _ptr(positions), _ptr(topk_w), _ptr(R), _ptr(Y), M, N, k, rows, dt,
+                             _stream(stream)))
+    return Y
+
+
+def moe_combine_backward(dY, Ys, positions, topk_w, dYs, dw, stream=None):
+    """Gradients of ``moe_combine``: ``dYs[positions[t, s]] = topk_w[t, s] dY[t]`` and
+    ``dw[t, s] = <Ys[positions[t, s]], dY[t]>`` (fp32; ``dw`` and ``Ys`` may both be None), written in place."""
+    import torch
+    M, N = _dims(dY, "dY", 2)
+    k = _dims(positions, "positions", 2)[1]
+    dt = _dtype_code(dY)
+    rows = _dims(dYs, "dYs", 2)[0]
+    if (Ys is None) != (dw is None):
+        raise ValueError("dw takes Ys: give both or neither")
+    _arg(dY, "dY", (M, N), dY.dtype)
+    _arg(Ys, "Ys", (rows, N), dY.dtype, optional=True)
+    _arg(positions, "positions", (M, k), torch.int32)
+    _arg(topk_w, "topk_w", (M, k), torch.float32, optional=True)
+    _arg(dYs, "dYs", (rows, N), dY.dtype)
+    _arg(dw, "dw", (M, k), torch.float32, optional=True)
+    _on_device(dY, Ys, positions, topk_w, dYs, dw)
+    _check(lib().moe_combine_backward(_ptr(dY), _ptr(Ys), _ptr(positions), _ptr(topk_w), _ptr(dYs), _ptr(dw), M, N,
+                                      k, rows, dt, _stream(stream)))
+
+
+def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None):
+    """The gradient of the gate's softmax over the chosen logits: ``dlogits`` (M x E, fp32), written in place."""
+    import torch
+    M, E = _dims(dlogits, "dlogits", 2)
+    k = _dims(topk_ids, "topk_ids", 2)[1]
+    f32 = torch.float32
+    _arg(topk_ids, "topk_ids", (M, k), torch.int32)
+    _arg(topk_w, "topk_w", (M, k), f32)
+    _arg(dw, "dw", (M, k), f32)
+    _arg(dlogits, "dlogits", (M, E), f32)
+    _on_device(topk_ids, topk_w, dw, dlogits)
+    _check(lib().moe_route_backward(_ptr(topk_ids), _ptr(topk_w), _ptr(dw), _ptr(dlogits), M, E, k, _stream(stream)))
+    return dlogits
+
+
+# ---------------------------------------------------------------- 4-bit weights
+
+def ffn_q4_bytes(K, C) -> int:
+    return lib().ffn_q4_bytes(K, C)
+
+
+def ffn_q4_empty(K, C, group=128, zero=False, experts=None, device="cuda"):
+    """Buffers ``(Wq, scale, zero or None)`` of the packed layout of a K x C matrix, or of ``experts`` of them."""
+    import torch
+    lead = () if experts is None else (experts,)
+    ct, kt = -(-C // 16), -(-K // 128)
+    scale = torch.zeros(*lead, ct, kt, 16, 128 // group, dtype=torch.bfloat16, device=device)
+    return (torch.zeros(*lead, ct, kt, 1024, dtype=torch.uint8, device=device), scale,
+            torch.zeros_like(scale) if zero else None)
+
+
+def _q4_code(code):
+    if isinstance(code, str) and code not in Q4_CODES:
+        raise ValueError(f"code must be one of {sorted(Q4_CODES)} (got {code!r})")
+    return Q4_CODES[code] if isinstance(code, str) else int(code)
+
+
+def _q4_weight(Wq, scale, zero, lead, K, C, names):
+    """Checks one packed weight; returns its group size."""
+    import torch
+    ct, kt = -(-C // 16), -(-K // 128)
+    _arg(Wq, names[0], (*lead, ct, kt, 1024), torch.uint8)
+    per = _dims(scale, names[1], 4 + len(lead))[-1]
+    if per not in (1, 2, 4):
+        raise ValueError(f"{names[1]} must have 1, 2 or 4 groups per 128 rows (got {per})")
+    _arg(scale, names[1], (*lead, ct, kt, 16, per), torch.bfloat16)
+    _arg(zero, names[2], scale.shape, torch.bfloat16, optional=True)
+    return 128 // per
+
+
+def ffn_q4_quantize(W, Wq, scale, zero=None, code="int4", stream=None):
+    """4-bit codes, scales and, when given, zero points of ``W`` (K x C, bf16 or fp32) in the packed layout
+    (``ffn_q4_empty`` makes the buffers; the group size is the scales'), written in place."""
+    K, C = _dims(W, "W", 2)
+    dt = _dtype_code(W)
+    _arg(W, "W", (K, C), W.dtype)
+    group = _q4_weight(Wq, scale, zero, (), K, C, ("Wq", "scale", "zero"))
+    _on_device(W, Wq, scale, zero)
+    _check(lib().ffn_q4_quantize(_ptr(W), _ptr(Wq), _ptr(scale), _ptr(zero), K, C, dt, _q4_code(code), group,
+                                 _stream(stream)))
+    return Wq
+
+
+def ffn_q4_pack(codes, scale_in, Wq, scale, zero_in=None, zero=None, code="int4", stream=None):
+    """Another quantiser's codes (K x C, uint8), scales and zero points (groups x C, bf16) into the packed
+    layout, written in place."""
+    import torch
+    K, C = _dims(codes, "codes", 2)
+    _arg(codes, "codes", (K, C), torch.uint8)
+    group = _q4_weight(Wq, scale, zero, (), K, C, ("Wq", "scale", "zero"))
+    if (zero_in is None) != (zero is None):
+        raise ValueError("give zero_in and zero together or neither")
+    _arg(scale_in, "scale_in", (-(-K // group), C), torch.bfloat16)
+    _arg(zero_in, "zero_in", (-(-K // group), C), torch.bfloat16, optional=True)
+    _on_device(codes, scale_in, Wq, scale, zero_in, zero)
+    _check(lib().ffn_q4_pack(_ptr(codes), _ptr(scale_in), _ptr(zero_in), _ptr(Wq), _ptr(scale), _ptr(zero), K, C,
+                             _q4_code(code), group, _stream(stream)))
+    return Wq
+
+
+def ffn_q4_matvec(X, Wq, scale, Y, zero=None, bias=None, act="none", code="int4", stream=None):
+    """``Y = act(X W + bias)`` for up to 16 rows of X (bf16) and a K x C matrix of packed 4-bit weights;
+    ``Y`` (bf16) is written in place."""
+    import torch
+    M, K = _dims(X, "X", 2)
+    C = _dims(Y, "Y", 2)[1]
+    bf = torch.bfloat16
+    _arg(X, "X", (M, K), bf)
+    group = _q4_weight(Wq, scale, zero, (), K, C, ("Wq", "scale", "zero"))
+    _arg(bias, "bias", (C,), bf, optional=True)
+    _arg(Y, "Y", (M, C), bf)
+    _on_device(X, Wq, scale, zero, bias, Y)
+    _check(lib().ffn_q4_matvec(_ptr(X), _ptr(Wq), _ptr(scale), _ptr(zero), _ptr(bias), _ptr(Y), M, K, C,
+                               _q4_code(code), group, _act(act), _stream(stream)))
+    return Y
+
+
+def _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, lead, K, C):
+    group = _q4_weight(Wg, scale_g, zero_g, lead, K, C, ("Wg", "scale_g", "zero_g"))
+    if _q4_weight(Wu, scale_u, zero_u, lead, K, C, ("Wu", "scale_u", "zero_u")) != group:
+        raise ValueError("both matrices must have the same group size")
+    if (zero_g is None) != (zero_u is None):
+        raise ValueError("give both zero points or neither")
+    return group
+
+
+def ffn_q4_swiglu(X, Wg, scale_g, Wu, scale_u, H, zero_g=None, zero_u=None, code="int4", stream=None):
+    """``H = silu(X Wg) * (X Wu)`` for up to 16 rows of X (bf16) and two K x C matrices of packed 4-bit
+    weights; ``H`` (bf16) is written in place."""
+    import torch
+    M, K = _dims(X, "X", 2)
+    C = _dims(H, "H", 2)[1]
+    _arg(X, "X", (M, K), torch.bfloat16)
+    group = _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, (), K, C)
+    _arg(H, "H", (M, C), torch.bfloat16)
+    _on_device(X, Wg, scale_g, zero_g, Wu, scale_u, zero_u, H)
+    _check(lib().ffn_q4_swiglu(_ptr(X), _ptr(Wg), _ptr(scale_g), _ptr(zero_g), _ptr(Wu), _ptr(scale_u), _ptr(zero_u),
+                               _ptr(H), M, K, C, _q4_code(code), group, _stream(stream)))
+    return H
+
+
+def moe_q4_matvec(X, expert_offsets, Wq, scale, Y, zero=None, bias=None, act="none", code="int4", stream=None):
+    """``ffn_q4_matvec`` over the experts' row lists: rows ``expert_offsets[e]`` to ``expert_offsets[e + 1]``
+    of X go through matrix e (Wq, scale, zero, bias: one per expert in front); other rows of ``Y`` are
+    left as they were."""
+    import torch
+    rows, K = _dims(X, "X", 2)
+    C = _dims(Y, "Y", 2)[1]
+    E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
+    bf = torch.bfloat16
+    _arg(X, "X", (rows, K), bf)
+    _arg(expert_offsets, "expert_offsets", (E + 1,), torch.int32)
+    group = _q4_weight(Wq, scale, zero, (E,), K, C, ("Wq", "scale", "zero"))
+    _arg(bias, "bias", (E, C), bf, optional=True)
+    _arg(Y, "Y", (rows, C), bf)
+    _on_device(X, expert_offsets, Wq, scale, zero, bias, Y)
+    _check(lib().moe_q4_matvec(_ptr(X), _ptr(expert_offsets), _ptr(Wq), _ptr(scale), _ptr(zero), _ptr(bias), _ptr(Y),
+                               rows, E, K, C, _q4_code(code), group, _act(act), _stream(stream)))
+    return Y
+
+
+def moe_q4_swiglu(X, expert_offsets, Wg, scale_g, Wu, scale_u, H, zero_g=None, zero_u=None, code="int4",
+                  stream=None):
+    """``ffn_q4_swiglu`` over the experts' row lists, as ``moe_q4_matvec`` is ``ffn_q4_matvec`` over them."""
+    import torch
+    rows, K = _dims(X, "X", 2)
+    C = _dims(H, "H", 2)[1]
+    E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
+    _arg(X, "X", (rows, K), torch.bfloat16)
+    _arg(expert_offsets, "expert_offsets", (E + 1,), torch.int32)
+    group = _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, (E,), K, C)
+    _arg(H, "H", (rows, C), torch.bfloat16)
+    _on_device(X, expert_offsets, Wg, scale_g, zero_g, Wu, scale_u, zero_u, H)
+    _check(lib().moe_q4_swiglu(_ptr(X), _ptr(expert_offsets), _ptr(Wg), _ptr(scale_g), _ptr(zero_g), _ptr(Wu),
+                               _ptr(scale_u), _ptr(zero_u), _ptr(H), rows, E, K, C, _q4_code(code), group,
+                               _stream(stream)))
+    return H
 
 
 # ---------------------------------------------------------------- measurement support

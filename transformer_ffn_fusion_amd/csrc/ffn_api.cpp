@@ -17,6 +17,7 @@
 #include "ffn_device.h"
 
 #include "ffn_internal.h"
+#include "sublayer.h"
 
 namespace {
 
@@ -610,30 +611,45 @@ int ffn_swiglu_forward_traced(const void* X, const void* Wg, const void* Wu, con
                           workspace_bytes, stream, events, n_events);
 }
 
-// An array of a call, for the training operators' check of overlaps.
+// An array of a call, for the checks of null pointers, alignment and overlaps.
 struct Span {
     const void* p;
     int64_t bytes;
     const char* name;
 };
 
-// Refuses outputs (the workspace among them) that overlap an input or one another; the
-// first output may be the very array of one of the first `same` inputs.
-static int check_overlaps(const Span* out, int outs, const Span* in, int ins, int same) {
+// Null and alignment of the given arrays (a null one must be among those that may be).
+static int check_arrays(const Span* a, int n, uint32_t optional, uintptr_t align = 16) {
+    for (int i = 0; i < n; ++i) {
+        if (!a[i].p && !((optional >> i) & 1)) return fail(FFN_EINVAL, "%s must not be NULL", a[i].name);
+        if ((reinterpret_cast<uintptr_t>(a[i].p) & (align - 1)) != 0)
+            return fail(FFN_EALIGN, "%s is not %d-byte aligned", a[i].name, (int)align);
+    }
+    return FFN_OK;
+}
+
+// Refuses outputs (the workspace among them) that overlap an input or one another; same[i] has a bit for each input
+// that output i may be the very array of.
+static int check_apart(const Span* out, const uint32_t* same, int outs, const Span* in, int ins) {
     auto overlap = [](const Span& a, const Span& b) {
         const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
         return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
     };
     for (int i = 0; i < outs; ++i) {
         for (int j = 0; j < i; ++j)
-            if (overlap(out[i], out[j]))
-                return fail(FFN_EINVAL, "%s and %s overlap", out[j].name, out[i].name);
+            if (overlap(out[i], out[j])) return fail(FFN_EINVAL, "%s and %s overlap", out[j].name, out[i].name);
         for (int j = 0; j < ins; ++j)
             if (overlap(out[i], in[j]) &&
-                !(j < same && i == 0 && out[i].p == in[j].p && out[i].bytes == in[j].bytes))
+                !(((same[i] >> j) & 1) && out[i].p == in[j].p && out[i].bytes == in[j].bytes))
                 return fail(FFN_EINVAL, "%s and %s overlap", in[j].name, out[i].name);
     }
     return FFN_OK;
+}
+
+// The same where only the first output may be the very array of one of the first `same` inputs.
+static int check_overlaps(const Span* out, int outs, const Span* in, int ins, int same) {
+    uint32_t may[8] = {(1u << same) - 1u};
+    return check_apart(out, may, outs, in, ins);
 }
 
 // ---------------------------------------------------------------- SwiGLU backward
@@ -783,6 +799,106 @@ int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, con
                                                  dtype == FFN_F32, st),
                   "layer norm backward kernels");
     if (rc) return rc;
+    return ok();
+}
+
+// ---------------------------------------------------------------- RMS norm
+
+static int check_rmsnorm(int64_t M, int64_t N, int dtype) {
+    if (dtype != FFN_F32 && dtype != FFN_BF16) return fail(FFN_EINVAL, "unknown dtype %d", dtype);
+    if (M < 0) return fail(FFN_EINVAL, "M must be >= 0 (got %lld)", (long long)M);
+    if (N < 1) return fail(FFN_EINVAL, "N must be >= 1 (got %lld)", (long long)N);
+    if (N % 8 || N > ffn::kLnMaxN)
+        return fail(FFN_EUNSUPPORTED, "the RMS norm takes N a multiple of 8 up to %lld (got %lld)",
+                    (long long)ffn::kLnMaxN, (long long)N);
+    if (M >= ((int64_t)1 << 31)) return fail(FFN_EUNSUPPORTED, "M must be below 2^31");
+    return FFN_OK;
+}
+
+static int rmsnorm_forward(const void* X, const void* R, const void* gamma, void* S, void* Y, float* scale,
+                           float* rstd, int64_t M, int64_t N, int dtype, bool q8, int group, float eps,
+                           void* stream) {
+    int rc = check_rmsnorm(M, N, dtype);
+    if (rc) return rc;
+    if (!(eps > 0.0f)) return fail(FFN_EINVAL, "eps must be > 0");
+    if (q8 && group != 0 && group != 128)
+        return fail(FFN_EUNSUPPORTED, "group must be 128, or 0 for whole rows (got %d)", group);
+    if (M > 0 && !R != !S) return fail(FFN_EINVAL, "S is written with R alone: give both or neither");
+    const int64_t eb = dtype == FFN_F32 ? 4 : 2;
+    const int64_t scales = group ? (N + group - 1) / group : 1;
+    const Span in[] = {{X, eb * M * N, "X"}, {R, eb * M * N, "R"}, {gamma, eb * N, "gamma"}};
+    const Span out[] = {{S, eb * M * N, "S"}, {Y, (q8 ? 1 : eb) * M * N, q8 ? "Q" : "Y"}, {rstd, 4 * M, "rstd"},
+                       {scale, q8 ? 4 * M * scales : 0, "scale"}};
+    const uint32_t none = M == 0 ? 15u : 0u;   // an empty tensor's pointer
+    if ((rc = check_arrays(in, 3, none | 2u))) return rc;
+    if ((rc = check_arrays(out, 4, none | 1u | 4u | (q8 ? 0u : 8u)))) return rc;
+    // a lane reads its columns of a row before it writes them
+    const uint32_t same[] = {3u, q8 || R ? 0u : 1u, 0u, 0u};
+    if ((rc = check_apart(out, same, 4, in, 3))) return rc;
+    if (M == 0) return ok();
+    ffn::RmsForwardIO io;
+    io.X = X;
+    io.R = R;
+    io.gamma = gamma;
+    io.S = S;
+    io.Y = Y;
+    io.scale = scale;
+    io.rstd = rstd;
+    io.M = M;
+    io.N = N;
+    io.f32 = dtype == FFN_F32;
+    io.q8 = q8;
+    io.group = group;
+    io.eps = eps;
+    if ((rc = launched(ffn::launch_rmsnorm_forward(io, reinterpret_cast<hipStream_t>(stream)), "RMS norm kernel")))
+        return rc;
+    return ok();
+}
+
+int ffn_rmsnorm_forward(const void* X, const void* R, const void* gamma, void* S, void* Y,
+                        float* rstd, int64_t M, int64_t N, int dtype, float eps, void* stream) {
+    return rmsnorm_forward(X, R, gamma, S, Y, nullptr, rstd, M, N, dtype, false, 0, eps, stream);
+}
+
+int ffn_rmsnorm_q8_forward(const void* X, const void* R, const void* gamma, void* S, void* Q,
+                           float* scale, float* rstd, int64_t M, int64_t N, int dtype, int group,
+                           float eps, void* stream) {
+    return rmsnorm_forward(X, R, gamma, S, Q, scale, rstd, M, N, dtype, true, group, eps, stream);
+}
+
+size_t ffn_rmsnorm_backward_workspace_size(int64_t M, int64_t N, int dtype) {
+    if (check_rmsnorm(M, N, dtype) != FFN_OK) return 0;
+    const size_t n = align_up(sizeof(float) * ffn::rmsnorm_partial_floats(M, N));
+    return n ? n : kAlign;
+}
+
+int ffn_rmsnorm_backward(const void* S, const void* dY, const void* dS, const void* gamma,
+                         const float* rstd, void* dX, float* dgamma, int64_t M, int64_t N, int dtype,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_rmsnorm(M, N, dtype);
+    if (rc) return rc;
+    const int64_t eb = dtype == FFN_F32 ? 4 : 2;
+    const size_t need = ffn_rmsnorm_backward_workspace_size(M, N, dtype);
+    const Span in[] = {{S, eb * M * N, "S"}, {dY, eb * M * N, "dY"}, {dS, eb * M * N, "dS"},
+                      {rstd, 4 * M, "rstd"}, {gamma, eb * N, "gamma"}};
+    const Span out[] = {{dX, eb * M * N, "dX"}, {dgamma, 4 * N, "dgamma"},
+                       {workspace, (int64_t)need, "the workspace"}};
+    if ((rc = check_arrays(in, 5, M == 0 ? 15u : 4u))) return rc;
+    if ((rc = check_arrays(out, 2, M == 0 ? 1u : 0u))) return rc;
+    if ((rc = check_arrays(out + 2, 1, 0, kAlign))) return rc;
+    if (workspace_bytes < need)
+        return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    const uint32_t same[] = {7u, 0u, 0u};
+    if ((rc = check_apart(out, same, 3, in, 5))) return rc;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (M == 0) {
+        if ((rc = launched(ffn::launch_zero_f32(dgamma, N, st), "zero fill"))) return rc;
+        return ok();
+    }
+    if ((rc = launched(ffn::launch_rmsnorm_backward(S, dY, dS, gamma, rstd, dX, dgamma,
+                                                    static_cast<float*>(workspace), M, N, dtype == FFN_F32, st),
+                       "RMS norm backward kernels")))
+        return rc;
     return ok();
 }
 
@@ -1075,6 +1191,289 @@ int moe_ffn_forward_traced(const void* X, const float* logits, int64_t M, int64_
 }
 
 // ---------------------------------------------------------------- self-check
+
+// ---------------------------------------------------------------- MoE: rows by expert and back
+
+// Sizes of the calls around the experts; rows: of the sorted side.
+static int check_rows(int64_t M, int64_t N, int64_t E, int k, int64_t rows, int dtype, bool e4m3) {
+    if (dtype != FFN_F32 && dtype != FFN_BF16 && dtype != FFN_E4M3) return fail(FFN_EINVAL, "unknown dtype %d", dtype);
+    if (dtype == FFN_E4M3 && !e4m3) return fail(FFN_EUNSUPPORTED, "e4m3 rows are taken by moe_dispatch alone");
+    if (M < 0 || rows < 0) return fail(FFN_EINVAL, "M and rows must be >= 0");
+    if (E < 1 || E > 256) return fail(FFN_EUNSUPPORTED, "E must be in [1, 256] (got %lld)", (long long)E);
+    if (k < 1 || k > 8) return fail(FFN_EUNSUPPORTED, "k must be in [1, 8] (got %d)", k);
+    const int64_t lim = (int64_t)1 << 31;
+    if (M >= lim || M * k >= lim || rows >= lim) return fail(FFN_EUNSUPPORTED, "M*k and rows must be below 2^31");
+    if (N < 1) return fail(FFN_EINVAL, "N must be >= 1 (got %lld)", (long long)N);
+    if (N % 8 || N >= ((int64_t)1 << 23))
+        return fail(FFN_EUNSUPPORTED, "N must be a multiple of 8 below 2^23 (got %lld)", (long long)N);
+    return FFN_OK;
+}
+
+size_t moe_dispatch_workspace_size(int64_t M, int64_t E, int k) {
+    if (check_rows(M, 8, E, k, 0, FFN_BF16, false) != FFN_OK) return 0;
+    const size_t n = align_up(sizeof(int32_t) * ffn::dispatch_count_ints(M, E, k));
+    return n ? n : kAlign;
+}
+
+int moe_dispatch(const void* X, const int32_t* topk_ids, const float* scale, int64_t M, int64_t N,
+                 int64_t E, int k, int dtype, int64_t scale_cols, void* Xs, float* scale_sorted,
+                 int32_t* expert_offsets, int32_t* sorted_entries, int32_t* positions,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_rows(M, N, E, k, 0, dtype, true);
+    if (rc) return rc;
+    if (scale_cols < 0 || scale_cols >= ((int64_t)1 << 23))
+        return fail(FFN_EINVAL, "scale_cols must be in [0, 2^23) (got %lld)", (long long)scale_cols);
+    if (M > 0 && (!scale != !scale_sorted || !scale != (scale_cols == 0)))
+        return fail(FFN_EINVAL, "give scale, scale_sorted and scale_cols together or none of them");
+    const int64_t eb = dtype == FFN_F32 ? 4 : dtype == FFN_BF16 ? 2 : 1, n = M * k;
+    const size_t need = moe_dispatch_workspace_size(M, E, k);
+    const Span in[] = {{X, eb * M * N, "X"}, {topk_ids, 4 * n, "topk_ids"}, {scale, 4 * M * scale_cols, "scale"}};
+    const Span out[] = {{Xs, eb * n * N, "Xs"}, {sorted_entries, 4 * n, "sorted_entries"},
+                       {positions, 4 * n, "positions"}, {scale_sorted, 4 * n * scale_cols, "scale_sorted"},
+                       {expert_offsets, 4 * (E + 1), "expert_offsets"}, {workspace, (int64_t)need, "the workspace"}};
+    if ((rc = check_arrays(in, 3, M == 0 ? 7u : 4u))) return rc;
+    if ((rc = check_arrays(out, 5, M == 0 ? 15u : 8u))) return rc;
+    if ((rc = check_arrays(out + 5, 1, 0, kAlign))) return rc;
+    if (workspace_bytes < need)
+        return fail(FFN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    const uint32_t same[6] = {};
+    if ((rc = check_apart(out, same, 6, in, 3))) return rc;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (M == 0) {   // (words of zeros, whatever their type)
+        if ((rc = launched(ffn::launch_zero_f32(reinterpret_cast<float*>(expert_offsets), E + 1, st), "zero fill")))
+            return rc;
+        return ok();
+    }
+    ffn::DispatchIO io;
+    io.X = X;
+    io.ids = topk_ids;
+    io.scale = scale;
+    io.Xs = Xs;
+    io.scale_sorted = scale_sorted;
+    io.offsets = expert_offsets;
+    io.entries = sorted_entries;
+    io.positions = positions;
+    io.M = M;
+    io.row_bytes = eb * N;
+    io.scale_cols = scale_cols;
+    io.E = (int)E;
+    io.k = k;
+    io.counts = static_cast<int32_t*>(workspace);
+    if ((rc = launched(ffn::launch_moe_dispatch(io, st), "dispatch kernels"))) return rc;
+    return ok();
+}
+
+int moe_combine(const void* Ys, const int32_t* positions, const float* topk_w, const void* R, void* Y,
+                int64_t M, int64_t N, int k, int64_t rows, int dtype, void* stream) {
+    int rc = check_rows(M, N, 1, k, rows, dtype, false);
+    if (rc) return rc;
+    const int64_t eb = dtype == FFN_F32 ? 4 : 2;
+    const Span in[] = {{R, eb * M * N, "R"}, {Ys, eb * rows * N, "Ys"}, {positions, 4 * M * k, "positions"},
+                      {topk_w, 4 * M * k, "topk_w"}};
+    const Span out[] = {{Y, eb * M * N, "Y"}};
+    if ((rc = check_arrays(in, 4, M == 0 ? 15u : 1u | 8u | (rows == 0 ? 2u : 0u)))) return rc;
+    if ((rc = check_arrays(out, 1, M == 0 ? 1u : 0u))) return rc;
+    const uint32_t same[] = {1u};
+    if ((rc = check_apart(out, same, 1, in, 4))) return rc;
+    if (M == 0) return ok();
+    if ((rc = launched(ffn::launch_moe_combine_rows(Ys, rows, positions, topk_w, R, Y, M, N, k, dtype == FFN_F32,
+                                                    reinterpret_cast<hipStream_t>(stream)),
+                       "combine kernel")))
+        return rc;
+    return ok();
+}
+
+int moe_dispatch_backward(const void* dXs, const int32_t* positions, void* dX, int64_t M, int64_t N,
+                          int k, int64_t rows, int dtype, void* stream) {
+    return moe_combine(dXs, positions, nullptr, nullptr, dX, M, N, k, rows, dtype, stream);
+}
+
+int moe_combine_backward(const void* dY, const void* Ys, const int32_t* positions,
+                         const float* topk_w, void* dYs, float* dw, int64_t M, int64_t N, int k,
+                         int64_t rows, int dtype, void* stream) {
+    int rc = check_rows(M, N, 1, k, rows, dtype, false);
+    if (rc) return rc;
+    const bool empty = M == 0 || rows == 0;
+    if (!empty && !Ys != !dw) return fail(FFN_EINVAL, "dw takes Ys: give both or neither");
+    const int64_t eb = dtype == FFN_F32 ? 4 : 2;
+    const Span in[] = {{Ys, eb * rows * N, "Ys"}, {dY, eb * M * N, "dY"}, {positions, 4 * M * k, "positions"},
+                      {topk_w, 4 * M * k, "topk_w"}};
+    const Span out[] = {{dYs, eb * rows * N, "dYs"}, {dw, 4 * M * k, "dw"}};
+    if ((rc = check_arrays(in, 4, M == 0 ? 15u : 1u | 8u))) return rc;
+    if ((rc = check_arrays(out, 2, 2u | (empty ? 1u : 0u)))) return rc;
+    const uint32_t same[] = {1u, 0u};
+    if ((rc = check_apart(out, same, 2, in, 4))) return rc;
+    if (M == 0) return ok();
+    if ((rc = launched(ffn::launch_moe_combine_backward(dY, Ys, rows, positions, topk_w, dYs, dw, M, N, k,
+                                                        dtype == FFN_F32, reinterpret_cast<hipStream_t>(stream)),
+                       "combine backward kernel")))
+        return rc;
+    return ok();
+}
+
+int moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* dw, float* dlogits,
+                       int64_t M, int64_t E, int k, void* stream) {
+    int rc = check_rows(M, 8, E, k, 0, FFN_F32, false);
+    if (rc) return rc;
+    const Span in[] = {{topk_ids, 4 * M * k, "topk_ids"}, {topk_w, 4 * M * k, "topk_w"}, {dw, 4 * M * k, "dw"}};
+    const Span out[] = {{dlogits, 4 * M * E, "dlogits"}};
+    const uint32_t none = M == 0 ? 7u : 0u;
+    if ((rc = check_arrays(in, 3, none))) return rc;
+    if ((rc = check_arrays(out, 1, none))) return rc;
+    const uint32_t same[] = {0u};
+    if ((rc = check_apart(out, same, 1, in, 3))) return rc;
+    if (M == 0) return ok();
+    if ((rc = launched(ffn::launch_moe_route_backward(topk_ids, topk_w, dw, dlogits, M, (int)E, k,
+                                                      reinterpret_cast<hipStream_t>(stream)),
+                       "routing backward kernel")))
+        return rc;
+    return ok();
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+
+static int check_q4(int64_t K, int64_t C, int code, int group) {
+    if (code != FFN_Q4_INT && code != FFN_Q4_E2M1) return fail(FFN_EINVAL, "unknown 4-bit code %d", code);
+    if (group != 32 && group != 64 && group != 128)
+        return fail(FFN_EUNSUPPORTED, "group must be 32, 64 or 128 (got %d)", group);
+    if (K < 1 || C < 1) return fail(FFN_EINVAL, "K and C must be >= 1 (got %lld, %lld)", (long long)K, (long long)C);
+    const int64_t lim = (int64_t)1 << 22;
+    if (K % 8 || C % 8 || K >= lim || C >= lim || K * C >= ((int64_t)1 << 31))
+        return fail(FFN_EUNSUPPORTED, "K and C must be multiples of 8 below 2^22, K * C below 2^31 (got %lld, %lld)",
+                    (long long)K, (long long)C);
+    return FFN_OK;
+}
+
+static int64_t q4_tiles(int64_t K, int64_t C) {
+    return (C + ffn::kQ4TileCols - 1) / ffn::kQ4TileCols * ((K + ffn::kQ4TileK - 1) / ffn::kQ4TileK);
+}
+
+size_t ffn_q4_bytes(int64_t K, int64_t C) {
+    if (check_q4(K, C, FFN_Q4_INT, 128) != FFN_OK) return 0;
+    return (size_t)q4_tiles(K, C) * 1024;
+}
+
+// One or E matrices, plain (W[1] null) or gated.
+static int q4_product(const void* X, const int32_t* offsets, const void* const (&W)[2],
+                      const void* const (&scale)[2], const void* const (&zero)[2], const void* bias, void* Y,
+                      int64_t rows, int64_t E, int64_t K, int64_t C, int code, int group, int act, bool gated,
+                      bool experts, void* stream) {
+    int rc = check_q4(K, C, code, group);
+    if (rc) return rc;
+    if (!valid_act(act)) return fail(FFN_EINVAL, "unknown activation %d", act);
+    if (rows < 0) return fail(FFN_EINVAL, "the number of rows must be >= 0 (got %lld)", (long long)rows);
+    if (E < 1 || E > 256) return fail(FFN_EUNSUPPORTED, "E must be in [1, 256] (got %lld)", (long long)E);
+    const int64_t most = experts ? 4096 : ffn::kQ4Rows;
+    if (rows > most) return fail(FFN_EUNSUPPORTED, "at most %lld rows (got %lld)", (long long)most, (long long)rows);
+    if (code == FFN_Q4_E2M1 && (zero[0] || zero[1])) return fail(FFN_EINVAL, "zero points are for FFN_Q4_INT");
+    if (gated && !zero[0] != !zero[1]) return fail(FFN_EINVAL, "give both zero points or neither");
+    const int64_t wb = E * q4_tiles(K, C) * 1024, sb = E * q4_tiles(K, C) * 32 * (128 / group);
+    const Span in[] = {{X, 2 * rows * K, "X"}, {W[0], wb, gated ? "Wg" : "Wq"}, {scale[0], sb, gated ? "scale_g" : "scale"},
+                      {zero[0], sb, gated ? "zero_g" : "zero"}, {W[1], wb, "Wu"}, {scale[1], sb, "scale_u"},
+                      {zero[1], sb, "zero_u"}, {bias, 2 * E * C, "bias"}, {offsets, 4 * (E + 1), "expert_offsets"}};
+    const Span out[] = {{Y, 2 * rows * C, gated ? "H" : "Y"}};
+    const uint32_t none = rows == 0 ? 1u : 0u;
+    if ((rc = check_arrays(in, 9, none | 8u | 64u | 128u | (gated ? 0u : 48u) | (experts ? 0u : 256u)))) return rc;
+    if ((rc = check_arrays(out, 1, none))) return rc;
+    const uint32_t same[] = {0u};
+    if ((rc = check_apart(out, same, 1, in, 9))) return rc;
+    if (rows == 0) return ok();
+    ffn::Q4IO io;
+    io.X = static_cast<const uint16_t*>(X);
+    for (int m = 0; m < 2; ++m) {
+        io.W[m] = static_cast<const uint8_t*>(W[m]);
+        io.scale[m] = static_cast<const uint16_t*>(scale[m]);
+        io.zero[m] = static_cast<const uint16_t*>(zero[m]);
+    }
+    io.bias = static_cast<const uint16_t*>(bias);
+    io.Y = static_cast<uint16_t*>(Y);
+    io.offsets = offsets;
+    io.rows = rows;
+    io.K = K;
+    io.C = C;
+    io.E = (int)E;
+    io.code = code;
+    io.group = group;
+    io.act = act;
+    io.gated = gated;
+    if ((rc = launched(ffn::launch_q4(io, reinterpret_cast<hipStream_t>(stream)), "4-bit product kernel"))) return rc;
+    return ok();
+}
+
+int ffn_q4_matvec(const void* X, const void* Wq, const void* scale, const void* zero,
+                  const void* bias, void* Y, int64_t M, int64_t K, int64_t C, int code, int group,
+                  int act, void* stream) {
+    return q4_product(X, nullptr, {Wq, nullptr}, {scale, nullptr}, {zero, nullptr}, bias, Y, M, 1, K, C, code,
+                      group, act, false, false, stream);
+}
+
+int ffn_q4_swiglu(const void* X, const void* Wg, const void* scale_g, const void* zero_g,
+                  const void* Wu, const void* scale_u, const void* zero_u, void* H, int64_t M,
+                  int64_t K, int64_t C, int code, int group, void* stream) {
+    return q4_product(X, nullptr, {Wg, Wu}, {scale_g, scale_u}, {zero_g, zero_u}, nullptr, H, M, 1, K, C, code,
+                      group, FFN_ACT_NONE, true, false, stream);
+}
+
+int moe_q4_matvec(const void* X, const int32_t* expert_offsets, const void* Wq, const void* scale,
+                  const void* zero, const void* bias, void* Y, int64_t rows, int64_t E, int64_t K,
+                  int64_t C, int code, int group, int act, void* stream) {
+    return q4_product(X, expert_offsets, {Wq, nullptr}, {scale, nullptr}, {zero, nullptr}, bias, Y, rows, E, K, C,
+                      code, group, act, false, true, stream);
+}
+
+int moe_q4_swiglu(const void* X, const int32_t* expert_offsets, const void* Wg, const void* scale_g,
+                  const void* zero_g, const void* Wu, const void* scale_u, const void* zero_u,
+                  void* H, int64_t rows, int64_t E, int64_t K, int64_t C, int code, int group,
+                  void* stream) {
+    return q4_product(X, expert_offsets, {Wg, Wu}, {scale_g, scale_u}, {zero_g, zero_u}, nullptr, H, rows, E, K, C,
+                      code, group, FFN_ACT_NONE, true, true, stream);
+}
+
+// The matrix in (W or codes), its scales and zeros, and the packed three.
+static int check_q4_arrays(const Span (&in)[3], const void* Wq, const void* scale, const void* zero, int64_t K,
+                           int64_t C, int group, uint32_t optional) {
+    const int64_t wb = q4_tiles(K, C) * 1024, sb = q4_tiles(K, C) * 32 * (128 / group);
+    const Span out[] = {{Wq, wb, "Wq"}, {scale, sb, "scale"}, {zero, sb, "zero"}};
+    int rc = check_arrays(in, 3, optional);
+    if (!rc) rc = check_arrays(out, 3, 4u);
+    const uint32_t same[] = {0u, 0u, 0u};
+    if (!rc) rc = check_apart(out, same, 3, in, 3);
+    return rc;
+}
+
+int ffn_q4_quantize(const void* W, void* Wq, void* scale, void* zero, int64_t K, int64_t C,
+                    int dtype, int code, int group, void* stream) {
+    int rc = check_q4(K, C, code, group);
+    if (rc) return rc;
+    if (dtype != FFN_F32 && dtype != FFN_BF16) return fail(FFN_EINVAL, "unknown dtype %d", dtype);
+    if (code == FFN_Q4_E2M1 && zero) return fail(FFN_EINVAL, "zero points are for FFN_Q4_INT");
+    const Span in[] = {{W, (dtype == FFN_F32 ? 4 : 2) * K * C, "W"}, {nullptr, 0, ""}, {nullptr, 0, ""}};
+    if ((rc = check_q4_arrays(in, Wq, scale, zero, K, C, group, 6u))) return rc;
+    if ((rc = launched(ffn::launch_q4_quantize(W, dtype == FFN_F32, static_cast<uint8_t*>(Wq),
+                                               static_cast<uint16_t*>(scale), static_cast<uint16_t*>(zero), K, C,
+                                               code, group, reinterpret_cast<hipStream_t>(stream)),
+                       "4-bit quantisation kernel")))
+        return rc;
+    return ok();
+}
+
+int ffn_q4_pack(const void* codes, const void* scale_in, const void* zero_in, void* Wq, void* scale,
+                void* zero, int64_t K, int64_t C, int code, int group, void* stream) {
+    int rc = check_q4(K, C, code, group);
+    if (rc) return rc;
+    if (!zero_in != !zero) return fail(FFN_EINVAL, "give zero_in and zero together or neither");
+    if (code == FFN_Q4_E2M1 && zero) return fail(FFN_EINVAL, "zero points are for FFN_Q4_INT");
+    const int64_t gb = 2 * ((K + group - 1) / group) * C;
+    const Span in[] = {{codes, K * C, "codes"}, {scale_in, gb, "scale_in"}, {zero_in, gb, "zero_in"}};
+    if ((rc = check_q4_arrays(in, Wq, scale, zero, K, C, group, 4u))) return rc;
+    if ((rc = launched(ffn::launch_q4_pack(static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scale_in),
+                                           static_cast<const uint16_t*>(zero_in), static_cast<uint8_t*>(Wq),
+                                           static_cast<uint16_t*>(scale), static_cast<uint16_t*>(zero), K, C, code,
+                                           group, reinterpret_cast<hipStream_t>(stream)),
+                       "4-bit packing kernel")))
+        return rc;
+    return ok();
+}
 
 size_t ffn_ceiling_sink_bytes(void) { return (size_t)ffn::ceiling_sink_floats() * 4; }
 

@@ -1,0 +1,370 @@
+// ffn_q4.hip -- products of few rows with 4-bit weights and group scales: one
+// matrix, the gated pair of SwiGLU, and both over the experts' row lists.
+//
+//   W[k][c] = (q - z) s  (4-bit integers; z = 8 without zero points)  or  e2m1(q) s,
+//   one s (and z) per column and group of 32, 64 or 128 k
+//   Y = act(X W + b)   or   H = silu(X Wg) * (X Wu);   X, Y bf16, sums fp32
+//
+// Bound: the HBM time of the codes -- every weight is used for up to 16 rows only.
+//  * The packed layout is the matrix instruction's operand: a tile of 16 columns x 128 k
+//    is 64 lanes x 16 bytes in lane order, so a wave loads 1 KiB at once and no value
+//    changes lanes.  Lane l's word j holds the 8 codes of column l % 16, k = 32 j +
+//    8 (l / 16) + 0..7.
+//  * A code becomes bf16 by one shift and one and-or for two integers (the code in the
+//    upper mantissa bits of 16: 16 + q) or one conversion for two e2m1 floats; both are
+//    exact.  The group's sum x (16 + q) is corrected by (16 + z) sum x, which one more
+//    matrix instruction against ones gives in the same registers, and scaled in fp32.
+//  * The waves of a workgroup share its columns and split K; their sums are joined in
+//    LDS in ascending order, so results do not depend on timing, and one launch is all.
+#include <type_traits>
+
+#include "ffn_device.h"
+#include "sublayer.h"
+
+namespace ffn {
+
+namespace {
+
+constexpr int kMaxWaves = 16;
+enum { kQ4Int = 0, kQ4E2m1 = 1 };
+
+struct Q4Args {
+    const uint16_t* X;
+    const char* W[2];
+    const char* S[2];
+    const char* Z[2];      // null: 8 (integers) or none (e2m1)
+    const uint16_t* bias;
+    uint16_t* Y;
+    const int32_t* offsets;
+    int64_t rows, K, C;
+    int64_t w_stride, s_stride, b_stride;   // per expert: bytes, bytes, elements
+    int kt;                                 // tiles along K
+    int act;
+};
+
+__device__ __forceinline__ uint4 decode8(uint32_t w, std::integral_constant<int, kQ4Int>) {
+    // nibbles i and i + 4 are neighbours: bits 3..6 and 19..22 of the shifted word
+    constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;   // bf16 16.0 twice
+    return make_uint4(((w << 3) & kMask) | kBase, ((w >> 1) & kMask) | kBase, ((w >> 5) & kMask) | kBase,
+                      ((w >> 9) & kMask) | kBase);
+}
+__device__ __forceinline__ uint4 decode8(uint32_t w, std::integral_constant<int, kQ4E2m1>) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    auto two = [&](auto b) {
+        return __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, b.value));
+    };
+    return make_uint4(two(std::integral_constant<int, 0>()), two(std::integral_constant<int, 1>()),
+                      two(std::integral_constant<int, 2>()), two(std::integral_constant<int, 3>()));
+}
+
+// kPer groups per tile; kTiles column tiles per wave (of each matrix), gated: of both.
+template <int kCode, int kPer, bool kGated, int kTiles>
+__global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
+    constexpr int kMats = kGated ? 2 : 1, kNT = kTiles * kMats;
+    constexpr int kSteps = 4 / kPer;              // matrix instructions per group
+    extern __shared__ float s_red[];              // [wave][tile][16 rows][16 columns]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    const int c = lane & 15, g = lane >> 4;
+    const int64_t ct0 = (int64_t)blockIdx.x * kTiles;
+    const int64_t tiles = (a.C + kQ4TileCols - 1) / kQ4TileCols;
+    const int e = blockIdx.y;
+    int64_t lo = 0, hi = a.rows;
+    if (a.offsets) {      // kept inside the rows whatever the offsets hold
+        const int64_t p = a.offsets[e], q = a.offsets[e + 1];
+        lo = p < 0 ? 0 : p > a.rows ? a.rows : p;
+        hi = q < lo ? lo : q > a.rows ? a.rows : q;
+    }
+    if (lo >= hi) return;
+    const char *wp[kNT], *sp[kNT], *zp[kNT];
+    const bool zeros = a.Z[0] != nullptr;
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            // (a tile past the last column repeats it and is not stored)
+            const int64_t ct = ct0 + t < tiles ? ct0 + t : tiles - 1;
+            const int i = m * kTiles + t;
+            wp[i] = a.W[m] + e * a.w_stride + ct * a.kt * 1024 + lane * 16;
+            sp[i] = a.S[m] + e * a.s_stride + (ct * a.kt * 16 + c) * (2 * kPer);
+            zp[i] = zeros ? a.Z[m] + e * a.s_stride + (ct * a.kt * 16 + c) * (2 * kPer) : sp[i];
+        }
+    struct Stage {
+        uint4 w[kNT], x[4];
+        uint32_t s[kNT][(kPer + 1) / 2], z[kNT][(kPer + 1) / 2];
+    };
+    auto groups = [&](const char* p, uint32_t (&v)[(kPer + 1) / 2]) {
+        if constexpr (kPer == 1) v[0] = *reinterpret_cast<const uint16_t*>(p);
+        else if constexpr (kPer == 2) v[0] = *reinterpret_cast<const uint32_t*>(p);
+        else {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            v[0] = u.x;
+            v[1] = u.y;
+        }
+    };
+    auto value = [&](const uint32_t (&v)[(kPer + 1) / 2], int p) {
+        return (p & 1) ? bf16_hi(v[p / 2]) : bf16_lo(v[p / 2]);
+    };
+    const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+
+    for (int64_t r0 = lo; r0 < hi; r0 += kQ4Rows) {
+        const int64_t have = hi - r0 < kQ4Rows ? hi - r0 : kQ4Rows;
+        // rows past the last one repeat it (their results are not stored)
+        const uint16_t* xrow = a.X + (r0 + (c < have ? c : have - 1)) * a.K;
+        auto load = [&](Stage& st, int kt) {
+#pragma unroll
+            for (int i = 0; i < kNT; ++i) {
+                st.w[i] = ld16(wp[i] + (int64_t)kt * 1024);
+                groups(sp[i] + (int64_t)kt * (32 * kPer), st.s[i]);
+                if (zeros) groups(zp[i] + (int64_t)kt * (32 * kPer), st.z[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t k0 = (int64_t)kt * kQ4TileK + 32 * j + 8 * g;
+                st.x[j] = k0 < a.K ? ld16(xrow + k0) : zero16();
+            }
+        };
+        floatx4_t acc[kNT];
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) acc[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        auto multiply = [&](const Stage& st, int kt) {
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) {
+                // a group past K: its scale may be anything
+                const bool real = (int64_t)kt * kQ4TileK + p * (kQ4TileK / kPer) < a.K;
+                floatx4_t xs = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (kCode == kQ4Int)
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) xs = mfma16x16x32(st.x[p * kSteps + j], ones, xs);
+#pragma unroll
+                for (int i = 0; i < kNT; ++i) {
+                    const uint32_t words[4] = {st.w[i].x, st.w[i].y, st.w[i].z, st.w[i].w};
+                    floatx4_t sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j)
+                        sum = mfma16x16x32(st.x[p * kSteps + j],
+                                           decode8(words[p * kSteps + j], std::integral_constant<int, kCode>()), sum);
+                    const float s = real ? value(st.s[i], p) : 0.f;
+                    if constexpr (kCode == kQ4Int) {
+                        const float z = 16.f + (zeros ? (real ? value(st.z[i], p) : 0.f) : 8.f);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(s, fmaf(-z, xs[r], sum[r]), acc[i][r]);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(s, sum[r], acc[i][r]);
+                    }
+                }
+            }
+        };
+        Stage st[2];
+        int kt = wave;
+        if (kt < a.kt) load(st[0], kt);
+        for (; kt < a.kt; kt += 2 * waves) {
+            if (kt + waves < a.kt) load(st[1], kt + waves);
+            multiply(st[0], kt);
+            if (kt + 2 * waves < a.kt) load(st[0], kt + 2 * waves);
+            if (kt + waves < a.kt) multiply(st[1], kt + waves);
+        }
+        // result: lane holds row 4 g + r, column c
+#pragma unroll
+        for (int i = 0; i < kNT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s_red[((wave * kNT + i) * 16 + 4 * g + r) * 16 + c] = acc[i][r];
+        __syncthreads();
+        for (int o = threadIdx.x; o < kTiles * 256; o += blockDim.x) {
+            const int t = o >> 8, m = (o >> 4) & 15;
+            const int64_t col = (ct0 + t) * kQ4TileCols + (o & 15);
+            float v[kMats];
+#pragma unroll
+            for (int q = 0; q < kMats; ++q) {
+                v[q] = 0.f;
+                for (int w = 0; w < waves; ++w) v[q] += s_red[(w * kNT + q * kTiles) * 256 + o];
+            }
+            if (m >= have || col >= a.C) continue;
+            float y;
+            if constexpr (kGated) {
+                y = silu(v[0]) * v[1];
+            } else {
+                if (a.bias) v[0] += bf16_to_f32(a.bias[e * a.b_stride + col]);
+                y = apply_act(a.act, v[0]);
+            }
+            a.Y[(r0 + m) * a.C + col] = __builtin_bit_cast(uint16_t, (__bf16)y);
+        }
+        if (r0 + kQ4Rows < hi) __syncthreads();   // read before the next rows' sums
+    }
+}
+
+// ---------------------------------------------------------------- packing
+
+// Nibble of a word that holds its code e (k = .. + e).
+__device__ __forceinline__ int nibble_of(int code, int e) {
+    return code == kQ4E2m1 ? e : (e >> 1) + 4 * (e & 1);
+}
+
+// The e2m1 code nearest to v (|v| beyond 6: 6), ties to the even code.
+__device__ __forceinline__ uint32_t to_e2m1(float v) {
+    const float m = fabsf(v);
+    // halfway points between 0, .5, 1, 1.5, 2, 3, 4, 6; a tie goes to the even code
+    const uint32_t q = (m > 0.25f) + (m >= 0.75f) + (m > 1.25f) + (m >= 1.75f) + (m > 2.5f) + (m >= 3.5f) + (m > 5.0f);
+    return q | (v < 0.f && q ? 8u : 0u);
+}
+
+// 128 k x 64 columns per workgroup: through LDS, so that W is read in whole lines.
+template <bool kF32>
+__global__ __launch_bounds__(256) void q4_quantize_kernel(const void* W, uint8_t* Wq, uint16_t* scale,
+                                                          uint16_t* zero, int64_t K, int64_t C, int kt_all,
+                                                          int code, int per) {
+    __shared__ float s_w[kQ4TileK][64 + 1];
+    __shared__ float s_s[4][64], s_z[4][64];
+    const int tid = threadIdx.x;
+    const int64_t kt = blockIdx.y, c0 = (int64_t)blockIdx.x * 64;
+    const int64_t tiles = (C + kQ4TileCols - 1) / kQ4TileCols;
+    for (int i = tid; i < kQ4TileK * 64; i += 256) {
+        const int64_t k = kt * kQ4TileK + (i >> 6), col = c0 + (i & 63);
+        float v = 0.f;
+        if (k < K && col < C)
+            v = kF32 ? static_cast<const float*>(W)[k * C + col] : bf16_to_f32(static_cast<const uint16_t*>(W)[k * C + col]);
+        s_w[i >> 6][i & 63] = v;
+    }
+    __syncthreads();
+    const int len = kQ4TileK / per;
+    if (tid < per * 64) {
+        const int p = tid >> 6, col = tid & 63;
+        float lo = 0.f, hi = 0.f;
+        for (int k = 0; k < len; ++k) {
+            lo = fminf(lo, s_w[p * len + k][col]);
+            hi = fmaxf(hi, s_w[p * len + k][col]);
+        }
+        const float top = fmaxf(-lo, hi);
+        float s = code == kQ4E2m1 ? top / 6.f : zero ? (hi - lo) / 15.f : top / 7.f;
+        if (top < 0x1p-100f) s = 0.f;         // nothing to keep
+        s = (float)(__bf16)s;                 // codes are taken under the scale as it is kept
+        float z = 8.f;
+        if (zero) z = s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 8.f;
+        s_s[p][col] = s;
+        s_z[p][col] = z;
+        const int64_t ct = (c0 + col) / kQ4TileCols;
+        if (ct < tiles) {
+            const int64_t at = ((ct * kt_all + kt) * 16 + col % 16) * per + p;
+            scale[at] = __builtin_bit_cast(uint16_t, (__bf16)s);
+            if (zero) zero[at] = __builtin_bit_cast(uint16_t, (__bf16)z);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < 1024; i += 256) {   // one word each: tile, lane, step
+        const int t = i >> 8, l = (i >> 2) & 63, j = i & 3;
+        const int64_t ct = c0 / kQ4TileCols + t;
+        if (ct >= tiles) continue;
+        const int col = 16 * t + l % 16, k0 = 32 * j + 8 * (l / 16);
+        const float s = s_s[k0 / len][col], z = s_z[k0 / len][col];
+        uint32_t word = 0;
+        for (int e = 0; e < 8; ++e) {
+            const float v = s_w[k0 + e][col];
+            uint32_t q;
+            if (code == kQ4E2m1) q = s > 0.f ? to_e2m1(v / s) : 0u;
+            else q = s > 0.f ? (uint32_t)fminf(fmaxf(rintf(v / s) + z, 0.f), 15.f) : (uint32_t)z;
+            word |= q << (4 * nibble_of(code, e));
+        }
+        reinterpret_cast<uint32_t*>(Wq)[((ct * kt_all + kt) * 64 + l) * 4 + j] = word;
+    }
+}
+
+// One word per thread; the first threads of a tile also place its scales and zeros.
+__global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* codes, const uint16_t* scale_in,
+                                                      const uint16_t* zero_in, uint8_t* Wq, uint16_t* scale,
+                                                      uint16_t* zero, int64_t K, int64_t C, int kt_all, int code,
+                                                      int per) {
+    const int64_t tile = blockIdx.x;          // ct * kt_all + kt
+    const int64_t ct = tile / kt_all, kt = tile - ct * kt_all;
+    const int tid = threadIdx.x, l = tid >> 2, j = tid & 3;
+    const int64_t col = ct * kQ4TileCols + l % 16, k0 = kt * kQ4TileK + 32 * j + 8 * (l / 16);
+    uint32_t word = 0;
+    for (int e = 0; e < 8; ++e) {
+        // past the matrix: the code of zero
+        uint32_t q = code == kQ4E2m1 ? 0u : 8u;
+        if (col < C && k0 + e < K) q = codes[(k0 + e) * C + col] & 15u;
+        word |= q << (4 * nibble_of(code, e));
+    }
+    reinterpret_cast<uint32_t*>(Wq)[tile * 256 + tid] = word;
+    if (tid < 16 * per) {
+        const int p = tid % per;
+        const int64_t cc = ct * kQ4TileCols + tid / per, grp = kt * per + p;
+        const bool real = cc < C && grp * (kQ4TileK / per) < K;
+        scale[tile * 16 * per + tid] = real ? scale_in[grp * C + cc] : (uint16_t)0;
+        if (zero) zero[tile * 16 * per + tid] = real ? zero_in[grp * C + cc] : (uint16_t)0;
+    }
+}
+
+template <int kCode, int kPer, bool kGated>
+void start(const Q4Args& a, int tiles_per, int waves, int E, hipStream_t stream) {
+    const int64_t tiles = (a.C + kQ4TileCols - 1) / kQ4TileCols;
+    const dim3 grid((unsigned)((tiles + tiles_per - 1) / tiles_per), (unsigned)E), block(64 * waves);
+    const size_t lds = (size_t)waves * tiles_per * (kGated ? 2 : 1) * 1024;   // at most 64 KiB
+    if (tiles_per == 1) hipLaunchKernelGGL((q4_kernel<kCode, kPer, kGated, 1>), grid, block, lds, stream, a);
+    else hipLaunchKernelGGL((q4_kernel<kCode, kPer, kGated, 2>), grid, block, lds, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_q4(const Q4IO& io, hipStream_t stream) {
+    Q4Args a;
+    const int per = kQ4TileK / io.group;
+    const int64_t tiles = (io.C + kQ4TileCols - 1) / kQ4TileCols;
+    a.kt = (int)((io.K + kQ4TileK - 1) / kQ4TileK);
+    for (int m = 0; m < 2; ++m) {
+        a.W[m] = reinterpret_cast<const char*>(io.W[m]);
+        a.S[m] = reinterpret_cast<const char*>(io.scale[m]);
+        a.Z[m] = reinterpret_cast<const char*>(io.zero[m]);
+    }
+    a.X = io.X;
+    a.bias = io.bias;
+    a.Y = io.Y;
+    a.offsets = io.offsets;
+    a.rows = io.rows;
+    a.K = io.K;
+    a.C = io.C;
+    a.w_stride = tiles * a.kt * 1024;
+    a.s_stride = tiles * a.kt * 32 * per;
+    a.b_stride = io.C;
+    a.act = io.act;
+    int waves = kMaxWaves;
+    while (waves > 1 && waves / 2 >= a.kt) waves /= 2;
+    const int tiles_per = 1;
+    auto go = [&](auto code, auto p) {
+        if (io.gated) start<code.value, p.value, true>(a, tiles_per, waves, io.E, stream);
+        else start<code.value, p.value, false>(a, tiles_per, waves, io.E, stream);
+    };
+    auto with = [&](auto code) {
+        if (per == 1) go(code, std::integral_constant<int, 1>());
+        else if (per == 2) go(code, std::integral_constant<int, 2>());
+        else go(code, std::integral_constant<int, 4>());
+    };
+    if (io.code == kQ4Int) with(std::integral_constant<int, kQ4Int>());
+    else with(std::integral_constant<int, kQ4E2m1>());
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_quantize(const void* W, bool f32, uint8_t* Wq, uint16_t* scale, uint16_t* zero,
+                              int64_t K, int64_t C, int code, int group, hipStream_t stream) {
+    const int kt = (int)((K + kQ4TileK - 1) / kQ4TileK);
+    const dim3 grid((unsigned)((C + 63) / 64), (unsigned)kt);
+    if (f32)
+        hipLaunchKernelGGL(q4_quantize_kernel<true>, grid, dim3(256), 0, stream, W, Wq, scale, zero, K, C, kt,
+                           code, kQ4TileK / group);
+    else
+        hipLaunchKernelGGL(q4_quantize_kernel<false>, grid, dim3(256), 0, stream, W, Wq, scale, zero, K, C, kt,
+                           code, kQ4TileK / group);
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_pack(const uint8_t* codes, const uint16_t* scale_in, const uint16_t* zero_in,
+                          uint8_t* Wq, uint16_t* scale, uint16_t* zero, int64_t K, int64_t C, int code,
+                          int group, hipStream_t stream) {
+    const int kt = (int)((K + kQ4TileK - 1) / kQ4TileK);
+    const int64_t tiles = (C + kQ4TileCols - 1) / kQ4TileCols * kt;
+    hipLaunchKernelGGL(q4_pack_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, codes, scale_in, zero_in, Wq,
+                       scale, zero, K, C, kt, code, kQ4TileK / group);
+    return hipGetLastError();
+}
+
+}  // namespace ffn

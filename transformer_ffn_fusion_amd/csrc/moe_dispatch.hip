@@ -1,0 +1,522 @@
+// moe_dispatch.hip -- a Mixture-of-Experts layer's tokens sorted by expert and
+// back, with the gate weights applied, and the gradients of both.
+//
+//   dispatch:  entry i = t k + s belongs to expert ids[t][s] (in [0, E), else it is
+//              dropped); its position is the number of kept entries of smaller experts
+//              plus the earlier entries of its own;  Xs[pos] = X[t]
+//   combine:   Y[t] = res[t] + sum_s w[t][s] Ys[pos[t][s]]   (ascending s, dropped
+//              entries add nothing); dispatch's gradient is this sum without w
+//   backward:  dYs[pos] = w[t][s] dY[t],  dw[t][s] = <Ys[pos], dY[t]>
+//   routing:   w = softmax over the k chosen logits, so
+//              dlogits[t][ids[t][s]] = w_s (dw_s - sum_j w_j dw_j)
+//
+// Bound: HBM bytes for many tokens (each row is read once and written where it goes,
+// whole 16-byte pieces), launches for few.  Positions come from counts, not from
+// atomics on lists, so they never depend on the order of arrival.
+#include <type_traits>
+
+#include "ffn_device.h"
+#include "rows.h"
+#include "sublayer.h"
+
+namespace ffn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxK = 8, kMaxExperts = 256;
+constexpr int kSmallEntries = 1024;     // most entries that every workgroup counts by itself
+constexpr int kSortThreads = 1024;      // entries of one turn of a sort workgroup
+constexpr int kSortBlocks = 256;        // most sort workgroups
+
+struct DispatchArgs {
+    const char* X;
+    const int32_t* ids;
+    const float* scale;
+    char* Xs;
+    float* scale_sorted;
+    int32_t *offsets, *entries, *positions;
+    int32_t* counts;       // [sort block][E]
+    int64_t M, n, row_bytes, scale_cols;
+    int64_t per;           // entries per sort block
+    int E, k, blocks;
+    int chunks;            // pieces of a row
+};
+
+// Few entries: one launch.  A workgroup takes 256 pieces of one token's row and counts
+// the entries before each of the token's k by itself, over all ids (at most 1024, from
+// the L2): no launch for a sort, and the row's load is under way meanwhile.
+template <typename Vec>
+__global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a) {
+    constexpr int kEach = kSmallEntries / kThreads;
+    __shared__ int s_cnt[kThreads / 64][kMaxK];
+    __shared__ int s_hist[kMaxExperts];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int k = a.k, E = a.E, n = (int)a.n;
+    const int64_t t = blockIdx.x;
+    const int chunk = blockIdx.y * kThreads + tid;
+    Vec row{};
+    if (chunk < a.chunks)
+        row = *reinterpret_cast<const Vec*>(a.X + t * a.row_bytes + (int64_t)chunk * sizeof(Vec));
+    int id[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int i = u * kThreads + tid;
+        id[u] = i < n ? a.ids[i] : E;
+        if ((unsigned)id[u] >= (unsigned)E) id[u] = E;   // dropped: after all experts
+    }
+    int mine[kMaxK];
+#pragma unroll
+    for (int s = 0; s < kMaxK; ++s) {
+        mine[s] = s < k ? a.ids[t * k + s] : -1;
+        int before = 0;
+        if (s < k) {
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int i = u * kThreads + tid;
+                const bool ahead = id[u] < mine[s] || (id[u] == mine[s] && i < (int)t * k + s);
+                before += __popcll(__ballot(ahead));
+            }
+        }
+        if (lane == 0) s_cnt[wave][s] = before;
+    }
+    const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+    if (first && tid < E) s_hist[tid] = 0;
+    __syncthreads();
+    if (first) {     // the same for the whole workgroup
+#pragma unroll
+        for (int u = 0; u < kEach; ++u)
+            if (id[u] < E) atomicAdd(&s_hist[id[u]], 1);   // a count: the order does not matter
+        __syncthreads();
+        int off = 0, all = 0;
+        for (int e = 0; e < E; ++e) {
+            if (e < tid) off += s_hist[e];
+            all += s_hist[e];
+        }
+        if (tid < E) a.offsets[tid] = off;
+        if (tid == 0) a.offsets[E] = all;
+    }
+#pragma unroll
+    for (int s = 0; s < kMaxK; ++s) {
+        if (s >= k) break;
+        int pos = 0;
+#pragma unroll
+        for (int q = 0; q < kThreads / 64; ++q) pos += s_cnt[q][s];
+        const bool kept = (unsigned)mine[s] < (unsigned)E;
+        if (blockIdx.y == 0 && tid == 0) {
+            a.positions[t * k + s] = kept ? pos : -1;
+            if (kept) a.entries[pos] = (int32_t)(t * k + s);
+        }
+        if (!kept) continue;
+        if (chunk < a.chunks)
+            *reinterpret_cast<Vec*>(a.Xs + (int64_t)pos * a.row_bytes + (int64_t)chunk * sizeof(Vec)) = row;
+        if (a.scale && blockIdx.y == 0)
+            for (int64_t c = tid; c < a.scale_cols; c += kThreads)
+                a.scale_sorted[pos * a.scale_cols + c] = a.scale[t * a.scale_cols + c];
+    }
+}
+
+// Many entries, step 1: each block's entries per expert.
+__global__ __launch_bounds__(kSortThreads) void dispatch_count_kernel(DispatchArgs a) {
+    __shared__ int s_hist[kMaxExperts];
+    const int tid = threadIdx.x, E = a.E;
+    if (tid < E) s_hist[tid] = 0;
+    __syncthreads();
+    const int64_t lo = blockIdx.x * a.per, hi = lo + a.per < a.n ? lo + a.per : a.n;
+    for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
+        const int e = a.ids[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&s_hist[e], 1);   // a count: the order does not matter
+    }
+    __syncthreads();
+    if (tid < E) a.counts[(int64_t)blockIdx.x * E + tid] = s_hist[tid];
+}
+
+// Step 2: a block adds the counts of the blocks before it and all blocks' totals, then
+// ranks its entries in order, 1024 at a time: within a wave by ballots over the bits of
+// the expert (lanes that agree in every bit are peers), between waves by their counts.
+__global__ __launch_bounds__(kSortThreads) void dispatch_rank_kernel(DispatchArgs a) {
+    constexpr int kWaves = kSortThreads / 64;
+    __shared__ int s_one[kSortThreads], s_two[kSortThreads];
+    __shared__ int s_base[kMaxExperts], s_scan[kMaxExperts];
+    __shared__ int s_w[kWaves][kMaxExperts];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.E;
+    int epow = 1, bits = 0;
+    while (epow < E) {
+        epow <<= 1;
+        ++bits;
+    }
+    {
+        const int parts = kSortThreads / epow, e = tid & (epow - 1), p = tid / epow;
+        int before = 0, total = 0;
+        if (e < E)
+#pragma unroll 4
+            for (int b = p; b < a.blocks; b += parts) {
+                const int c = a.counts[(int64_t)b * E + e];
+                total += c;
+                if (b < (int)blockIdx.x) before += c;
+            }
+        s_one[tid] = before;
+        s_two[tid] = total;
+        __syncthreads();
+        before = total = 0;
+        if (tid < epow)
+            for (int q = 0; q < parts; ++q) {
+                before += s_one[q * epow + tid];
+                total += s_two[q * epow + tid];
+            }
+        // exclusive prefix of the totals over the experts
+        if (tid < kMaxExperts) s_scan[tid] = tid < epow ? total : 0;
+        __syncthreads();
+        for (int d = 1; d < epow; d <<= 1) {
+            const int v = tid < epow && tid >= d ? s_scan[tid - d] : 0;
+            __syncthreads();
+            if (tid < epow) s_scan[tid] += v;
+            __syncthreads();
+        }
+        if (tid < E) {
+            const int off = s_scan[tid] - total;
+            s_base[tid] = off + before;
+            if (blockIdx.x == 0) {
+                a.offsets[tid] = off;
+                if (tid == E - 1) a.offsets[E] = off + total;
+            }
+        }
+    }
+    const uint64_t lt = lane == 0 ? 0ull : ~0ull >> (64 - lane);
+    const int64_t lo = blockIdx.x * a.per, hi = lo + a.per < a.n ? lo + a.per : a.n;
+    for (int64_t i0 = lo; i0 < hi; i0 += kSortThreads) {
+        const int64_t i = i0 + tid;
+        const int e = i < hi ? a.ids[i] : -1;
+        const bool kept = (unsigned)e < (unsigned)E;
+        for (int q = tid; q < kWaves * kMaxExperts; q += kSortThreads) (&s_w[0][0])[q] = 0;
+        uint64_t peers = __ballot(kept);
+        for (int b = 0; b < bits; ++b) {
+            const bool one = (e >> b) & 1;
+            const uint64_t m = __ballot(one);
+            peers &= one ? m : ~m;
+        }
+        const int rank = __popcll(peers & lt);
+        __syncthreads();   // s_w cleared; s_base written
+        if (kept && rank == 0) s_w[wave][e] = __popcll(peers);
+        __syncthreads();
+        if (tid < E) {
+            int run = s_base[tid];
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q) {
+                const int c = s_w[q][tid];
+                s_w[q][tid] = run;
+                run += c;
+            }
+            s_base[tid] = run;
+        }
+        __syncthreads();
+        int pos = -1;
+        if (kept) pos = s_w[wave][e] + rank;
+        if (pos >= a.n) pos = -1;   // (only if the ids were changed meanwhile)
+        if (i < hi) {
+            a.positions[i] = pos;
+            if (pos >= 0) a.entries[pos] = (int32_t)i;
+        }
+        __syncthreads();   // s_w read before it is cleared again
+    }
+}
+
+// Step 3: the rows.  A workgroup holds 256 / tpr tokens, tpr threads each; a thread
+// reads its piece once and writes it to the token's kept positions.
+template <typename Vec>
+__global__ __launch_bounds__(kThreads) void dispatch_rows_kernel(DispatchArgs a, int tpr_log) {
+    const int tpr = 1 << tpr_log;
+    const int c0 = threadIdx.x & (tpr - 1);
+    const int64_t t = (int64_t)blockIdx.x * (kThreads >> tpr_log) + (threadIdx.x >> tpr_log);
+    if (t >= a.M) return;
+    const int k = a.k;
+    int pos[kMaxK];
+#pragma unroll
+    for (int s = 0; s < kMaxK; ++s) pos[s] = s < k ? a.positions[t * k + s] : -1;
+    const char* src = a.X + t * a.row_bytes;
+    for (int c = c0; c < a.chunks; c += tpr) {
+        const Vec v = *reinterpret_cast<const Vec*>(src + (int64_t)c * sizeof(Vec));
+#pragma unroll
+        for (int s = 0; s < kMaxK; ++s)
+            if (pos[s] >= 0)
+                *reinterpret_cast<Vec*>(a.Xs + pos[s] * a.row_bytes + (int64_t)c * sizeof(Vec)) = v;
+    }
+    if (!a.scale) return;
+    for (int64_t c = c0; c < a.scale_cols; c += tpr) {
+        const float v = a.scale[t * a.scale_cols + c];
+#pragma unroll
+        for (int s = 0; s < kMaxK; ++s)
+            if (pos[s] >= 0) a.scale_sorted[pos[s] * a.scale_cols + c] = v;
+    }
+}
+
+int64_t sort_per_block(int64_t n) {
+    const int64_t turns = (n + (int64_t)kSortBlocks * kSortThreads - 1) / ((int64_t)kSortBlocks * kSortThreads);
+    return turns * kSortThreads;
+}
+int64_t sort_blocks(int64_t n) { return n <= kSmallEntries ? 0 : (n + sort_per_block(n) - 1) / sort_per_block(n); }
+
+// Threads per row (a power of two up to 256) for `pieces` of a row: log2.
+int threads_per_row_log(int64_t pieces) {
+    int l = 0;
+    while (l < 8 && ((int64_t)1 << l) < pieces) ++l;
+    return l;
+}
+
+// ---------------------------------------------------------------- combine
+
+struct CombineArgs {
+    const void* rows;
+    const int32_t* pos;
+    const float* w;
+    const void* res;
+    void* Y;
+    int64_t M, R;
+    int N;
+};
+
+// All of a piece's k loads are issued before the first is used; the sum is fp32, in
+// ascending s, rounded once.
+template <bool kF32, int K>
+__global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineArgs a, int tpr_log) {
+    const int tpr = 1 << tpr_log;
+    const int c0 = (threadIdx.x & (tpr - 1)) * 8;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads >> tpr_log) + (threadIdx.x >> tpr_log);
+    if (t >= a.M) return;
+    int64_t at[K];
+    float w[K];
+#pragma unroll
+    for (int s = 0; s < K; ++s) {
+        const int p = a.pos[t * K + s];
+        at[s] = (unsigned)p < (uint64_t)a.R && p >= 0 ? (int64_t)p * a.N : -1;
+        w[s] = a.w ? a.w[t * K + s] : 1.f;
+    }
+    for (int c = c0; c < a.N; c += 8 * tpr) {
+        Ln8<kF32> in[K], r;
+        r.zero();
+        if (a.res) r.load(a.res, t * a.N + c);
+#pragma unroll
+        for (int s = 0; s < K; ++s) {
+            in[s].zero();
+            if (at[s] >= 0) in[s].load(a.rows, at[s] + c);
+        }
+        float y[8];
+        r.get(y);
+#pragma unroll
+        for (int s = 0; s < K; ++s) {
+            if (at[s] < 0) continue;   // (a dropped entry's weight may be anything)
+            float v[8];
+            in[s].get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(w[s], v[e], y[e]);
+        }
+        ln_store<kF32>(a.Y, t * a.N + c, y);
+    }
+}
+
+struct CombineBackwardArgs {
+    const void *dY, *rows;
+    const int32_t* pos;
+    const float* w;
+    void* drows;
+    float* dw;
+    int64_t M, R;
+    int N, W, G;     // W waves per token, G tokens per workgroup
+};
+
+// dY is read once: every piece is multiplied into the k dot products and written,
+// weighted, to the k rows.  The dots are fp32 lane sums over a lane's pieces, then over
+// the wave, then over the W waves, in a fixed order.
+template <bool kF32, int K>
+__global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackwardArgs a) {
+    __shared__ float s_part[kThreads / 64][K];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = wave / a.W, w = wave % a.W;
+    const int64_t t = (int64_t)blockIdx.x * a.G + g;
+    const bool on = t < a.M;
+    int64_t at[K];
+    float wt[K], dot[K];
+#pragma unroll
+    for (int s = 0; s < K; ++s) {
+        const int p = on ? a.pos[t * K + s] : -1;
+        at[s] = (unsigned)p < (uint64_t)a.R && p >= 0 ? (int64_t)p * a.N : -1;
+        wt[s] = on && a.w ? a.w[t * K + s] : 1.f;
+        dot[s] = 0.f;
+    }
+    if (on)
+        for (int c = (w * 64 + lane) * 8; c < a.N; c += a.W * kLnCols) {
+            Ln8<kF32> d, in[K];
+            d.load(a.dY, t * a.N + c);
+            if (a.dw) {
+#pragma unroll
+                for (int s = 0; s < K; ++s) {
+                    in[s].zero();
+                    if (at[s] >= 0) in[s].load(a.rows, at[s] + c);
+                }
+            }
+            float y[8];
+            d.get(y);
+#pragma unroll
+            for (int s = 0; s < K; ++s) {
+                if (at[s] < 0) continue;
+                float v[8];
+                if (a.dw) {
+                    in[s].get(v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot[s] = fmaf(y[e], v[e], dot[s]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = wt[s] * y[e];
+                ln_store<kF32>(a.drows, at[s] + c, v);
+            }
+        }
+    if (!a.dw) return;
+#pragma unroll
+    for (int s = 0; s < K; ++s) {
+        const float v = wave_sum(dot[s]);
+        if (lane == 0) s_part[wave][s] = v;
+    }
+    __syncthreads();
+    if (on && w == 0 && lane < K) {
+        float v = 0.f;
+        for (int q = 0; q < a.W; ++q) v += s_part[g * a.W + q][lane];
+        a.dw[t * K + lane] = v;
+    }
+}
+
+// One thread per logit: the k choices of its token, compared with its expert.
+__global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
+                                                                  const float* __restrict__ w,
+                                                                  const float* __restrict__ dw,
+                                                                  float* __restrict__ dlogits, int64_t total,
+                                                                  int E, int k) {
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t t = i / E;
+        const int e = (int)(i - t * E);
+        float mean = 0.f;
+        for (int s = 0; s < k; ++s) mean = fmaf(w[t * k + s], dw[t * k + s], mean);
+        float d = 0.f;
+        for (int s = 0; s < k; ++s)
+            if (ids[t * k + s] == e) d += w[t * k + s] * (dw[t * k + s] - mean);
+        dlogits[i] = d;
+    }
+}
+
+template <typename F>
+hipError_t with_k(int k, F&& f) {
+    switch (k) {
+        case 1: f(std::integral_constant<int, 1>()); break;
+        case 2: f(std::integral_constant<int, 2>()); break;
+        case 3: f(std::integral_constant<int, 3>()); break;
+        case 4: f(std::integral_constant<int, 4>()); break;
+        case 5: f(std::integral_constant<int, 5>()); break;
+        case 6: f(std::integral_constant<int, 6>()); break;
+        case 7: f(std::integral_constant<int, 7>()); break;
+        case 8: f(std::integral_constant<int, 8>()); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t dispatch_count_ints(int64_t M, int64_t E, int k) { return (size_t)(sort_blocks(M * k) * E); }
+
+hipError_t launch_moe_dispatch(const DispatchIO& io, hipStream_t stream) {
+    DispatchArgs a;
+    a.X = static_cast<const char*>(io.X);
+    a.ids = io.ids;
+    a.scale = io.scale;
+    a.Xs = static_cast<char*>(io.Xs);
+    a.scale_sorted = io.scale_sorted;
+    a.offsets = io.offsets;
+    a.entries = io.entries;
+    a.positions = io.positions;
+    a.counts = io.counts;
+    a.M = io.M;
+    a.n = io.M * io.k;
+    a.row_bytes = io.row_bytes;
+    a.scale_cols = io.scale_cols;
+    a.E = io.E;
+    a.k = io.k;
+    a.per = sort_per_block(a.n);
+    a.blocks = (int)sort_blocks(a.n);
+    const bool wide = io.row_bytes % 16 == 0;   // e4m3 rows of odd multiples of 8: 8-byte pieces
+    a.chunks = (int)(io.row_bytes / (wide ? 16 : 8));
+    if (a.n <= kSmallEntries) {
+        const dim3 grid((unsigned)io.M, (unsigned)((a.chunks + kThreads - 1) / kThreads));
+        if (wide) hipLaunchKernelGGL(dispatch_small_kernel<uint4>, grid, dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL(dispatch_small_kernel<uint2>, grid, dim3(kThreads), 0, stream, a);
+        return hipGetLastError();
+    }
+    const dim3 blocks((unsigned)a.blocks);
+    hipLaunchKernelGGL(dispatch_count_kernel, blocks, dim3(kSortThreads), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(dispatch_rank_kernel, blocks, dim3(kSortThreads), 0, stream, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int l = threads_per_row_log(a.chunks);
+    const dim3 grid((unsigned)((io.M + (kThreads >> l) - 1) / (kThreads >> l)));
+    if (wide) hipLaunchKernelGGL(dispatch_rows_kernel<uint4>, grid, dim3(kThreads), 0, stream, a, l);
+    else hipLaunchKernelGGL(dispatch_rows_kernel<uint2>, grid, dim3(kThreads), 0, stream, a, l);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_rows(const void* rows, int64_t R, const int32_t* pos, const float* w,
+                                   const void* res, void* Y, int64_t M, int64_t N, int k, bool f32,
+                                   hipStream_t stream) {
+    CombineArgs a;
+    a.rows = rows;
+    a.pos = pos;
+    a.w = w;
+    a.res = res;
+    a.Y = Y;
+    a.M = M;
+    a.R = R;
+    a.N = (int)N;
+    const int l = threads_per_row_log(N / 8);
+    const dim3 grid((unsigned)((M + (kThreads >> l) - 1) / (kThreads >> l)));
+    return with_k(k, [&](auto K) {
+        if (f32)
+            hipLaunchKernelGGL((combine_rows_kernel<true, K.value>), grid, dim3(kThreads), 0, stream, a, l);
+        else
+            hipLaunchKernelGGL((combine_rows_kernel<false, K.value>), grid, dim3(kThreads), 0, stream, a, l);
+    });
+}
+
+hipError_t launch_moe_combine_backward(const void* dY, const void* rows, int64_t R, const int32_t* pos,
+                                       const float* w, void* drows, float* dw, int64_t M, int64_t N,
+                                       int k, bool f32, hipStream_t stream) {
+    CombineBackwardArgs a;
+    a.dY = dY;
+    a.rows = rows;
+    a.pos = pos;
+    a.w = w;
+    a.drows = drows;
+    a.dw = dw;
+    a.M = M;
+    a.R = R;
+    a.N = (int)N;
+    a.W = N > 2 * kLnCols ? 4 : N > kLnCols ? 2 : 1;
+    a.G = kThreads / 64 / a.W;
+    const dim3 grid((unsigned)((M + a.G - 1) / a.G));
+    return with_k(k, [&](auto K) {
+        if (f32)
+            hipLaunchKernelGGL((combine_backward_kernel<true, K.value>), grid, dim3(kThreads), 0, stream, a);
+        else
+            hipLaunchKernelGGL((combine_backward_kernel<false, K.value>), grid, dim3(kThreads), 0, stream, a);
+    });
+}
+
+hipError_t launch_moe_route_backward(const int32_t* ids, const float* w, const float* dw, float* dlogits,
+                                     int64_t M, int E, int k, hipStream_t stream) {
+    const int64_t total = M * E;
+    int64_t blocks = (total + kThreads - 1) / kThreads;
+    if (blocks > 16384) blocks = 16384;
+    hipLaunchKernelGGL(route_backward_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, ids, w, dw,
+                       dlogits, total, E, k);
+    return hipGetLastError();
+}
+
+}  // namespace ffn
