@@ -78,8 +78,23 @@ def test_swiglu(shape, kind):
         ref.check({"H": H}, ref.q4_swiglu(X, *cpu(wg), *cpu(wu), C, kind[0]), f"{shape} {kind} {M} rows")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", [(136, 8184), (136, 8200), (264, 20488), (1032, 10248)])
+def test_wide(shape, kind):
+    """Around the widths at which a wave takes two column tiles and a workgroup four waves."""
+    K, C = shape
+    print(f"case 4-bit, wide {shape} {kind}", flush=True)
+    wg, wu = weight(K, C, kind, 1), weight(K, C, kind, 2)
+    for M in (3, 6, 12):      # one, two and four loads of X per tile
+        X, Y, H = inputs(M, K, M), empty(M, C), empty(M, C)
+        ffn.ffn_q4_matvec(X, wg[0], wg[1], Y, zero=wg[2], code=kind[0])
+        ref.check({"Y": Y}, ref.q4_matvec(X, *cpu(wg), None, "none", C, kind[0]), f"{shape} {kind} {M} rows")
+        ffn.ffn_q4_swiglu(X, wg[0], wg[1], wu[0], wu[1], H, zero_g=wg[2], zero_u=wu[2], code=kind[0])
+        ref.check({"H": H}, ref.q4_swiglu(X, *cpu(wg), *cpu(wu), C, kind[0]), f"{shape} {kind} {M} rows")
+
+
 # rows per expert: none, one, a full tile, more than one tile, more than two
-LISTS = [[1], [0, 0, 3, 0], [1, 0, 16, 17, 2], [5, 40, 0, 33, 1, 0, 16], [0, 0, 0]]
+LISTS = [[1], [0, 0, 3, 0], [1, 0, 16, 17, 2], [5, 40, 0, 33, 1, 0, 16], [0, 0, 0], [i % 7 for i in range(200)]]
 
 
 @pytest.mark.parametrize("kind", [KINDS[0], KINDS[1], KINDS[4]])

@@ -25,7 +25,8 @@ namespace ffn {
 
 namespace {
 
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = 8;
+constexpr int kWaveLds = kQ4Rows * kQ4TileK * 2;   // a wave's rows of one tile, then its sums
 enum { kQ4Int = 0, kQ4E2m1 = 1 };
 
 struct Q4Args {
@@ -36,19 +37,27 @@ struct Q4Args {
     const uint16_t* bias;
     uint16_t* Y;
     const int32_t* offsets;
-    int64_t rows, K, C;
+    int64_t K, C;
     int64_t w_stride, s_stride, b_stride;   // per expert: bytes, bytes, elements
+    int rows;
     int kt;                                 // tiles along K
     int act;
 };
 
-__device__ __forceinline__ uint4 decode8(uint32_t w, std::integral_constant<int, kQ4Int>) {
-    // nibbles i and i + 4 are neighbours: bits 3..6 and 19..22 of the shifted word
-    constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;   // bf16 16.0 twice
-    return make_uint4(((w << 3) & kMask) | kBase, ((w >> 1) & kMask) | kBase, ((w >> 5) & kMask) | kBase,
-                      ((w >> 9) & kMask) | kBase);
+// The mask of decode8, in a vector register: beside the base in a scalar one it lets the
+// and and the or be one instruction.
+__device__ __forceinline__ uint32_t code_mask() {
+    uint32_t m = 0x00780078u;
+    asm("" : "+v"(m));
+    return m;
 }
-__device__ __forceinline__ uint4 decode8(uint32_t w, std::integral_constant<int, kQ4E2m1>) {
+__device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t mask, std::integral_constant<int, kQ4Int>) {
+    // nibbles i and i + 4 are neighbours: bits 3..6 and 19..22 of the shifted word
+    constexpr uint32_t kBase = 0x41804180u;   // bf16 16.0 twice
+    return make_uint4(((w << 3) & mask) | kBase, ((w >> 1) & mask) | kBase, ((w >> 5) & mask) | kBase,
+                      ((w >> 9) & mask) | kBase);
+}
+__device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t, std::integral_constant<int, kQ4E2m1>) {
     typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
     auto two = [&](auto b) {
         return __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, b.value));
@@ -57,27 +66,40 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, std::integral_constant<int,
                       two(std::integral_constant<int, 2>()), two(std::integral_constant<int, 3>()));
 }
 
-// kPer groups per tile; kTiles column tiles per wave (of each matrix), gated: of both.
-template <int kCode, int kPer, bool kGated, int kTiles>
-__global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
+// Orders LDS accesses of one wave's lanes among each other (nothing is executed).
+__device__ __forceinline__ void lanes_meet() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// kZero: integers with zero points; kPer groups per tile; kTiles column tiles per wave
+// (of each matrix; a pair's two take 128 registers a lane, two plain ones more).
+template <int kCode, bool kZero, int kPer, bool kGated, int kTiles>
+__global__ __launch_bounds__(64 * kMaxWaves, kTiles == 1 ? 4 : 2) void q4_kernel(Q4Args a) {
     constexpr int kMats = kGated ? 2 : 1, kNT = kTiles * kMats;
     constexpr int kSteps = 4 / kPer;              // matrix instructions per group
-    extern __shared__ float s_red[];              // [wave][tile][16 rows][16 columns]
+    static_assert(1024 * kNT <= kWaveLds, "a wave's sums take the place of its rows");
+    extern __shared__ __attribute__((aligned(16))) char s_all[];   // kWaveLds per wave
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
     const int c = lane & 15, g = lane >> 4;
+    char* s_wave = s_all + wave * kWaveLds;
     const int64_t ct0 = (int64_t)blockIdx.x * kTiles;
     const int64_t tiles = (a.C + kQ4TileCols - 1) / kQ4TileCols;
     const int e = blockIdx.y;
-    int64_t lo = 0, hi = a.rows;
+    int lo = 0, hi = a.rows;
     if (a.offsets) {      // kept inside the rows whatever the offsets hold
-        const int64_t p = a.offsets[e], q = a.offsets[e + 1];
+        const int p = __builtin_amdgcn_readfirstlane(a.offsets[e]);
+        const int q = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]);
         lo = p < 0 ? 0 : p > a.rows ? a.rows : p;
         hi = q < lo ? lo : q > a.rows ? a.rows : q;
     }
     if (lo >= hi) return;
-    const char *wp[kNT], *sp[kNT], *zp[kNT];
-    const bool zeros = a.Z[0] != nullptr;
+    // Loads go through buffer resources made for their tile by scalar instructions, with
+    // per-lane offsets that never change.  One of a tile past the last is empty: its loads
+    // read zeros and move nothing, so the loop's loads need no branch (behind one, the wait
+    // for a stage would be a wait for every load).
+    const char *wp[kNT], *sp[kNT], *zp[kNT];   // codes, scales, zero points of the column tiles
 #pragma unroll
     for (int m = 0; m < kMats; ++m)
 #pragma unroll
@@ -85,19 +107,21 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
             // (a tile past the last column repeats it and is not stored)
             const int64_t ct = ct0 + t < tiles ? ct0 + t : tiles - 1;
             const int i = m * kTiles + t;
-            wp[i] = a.W[m] + e * a.w_stride + ct * a.kt * 1024 + lane * 16;
-            sp[i] = a.S[m] + e * a.s_stride + (ct * a.kt * 16 + c) * (2 * kPer);
-            zp[i] = zeros ? a.Z[m] + e * a.s_stride + (ct * a.kt * 16 + c) * (2 * kPer) : sp[i];
+            wp[i] = a.W[m] + e * a.w_stride + ct * a.kt * 1024;
+            sp[i] = a.S[m] + e * a.s_stride + ct * a.kt * (32 * kPer);
+            if constexpr (kZero) zp[i] = a.Z[m] + e * a.s_stride + ct * a.kt * (32 * kPer);
         }
-    struct Stage {
-        uint4 w[kNT], x[4];
-        uint32_t s[kNT][(kPer + 1) / 2], z[kNT][(kPer + 1) / 2];
+    auto part = [&](const char* p, int kt, int bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p) + (int64_t)kt * bytes, (short)0,
+                                                 kt < a.kt ? bytes : 0, kRsrcWord3);
     };
-    auto groups = [&](const char* p, uint32_t (&v)[(kPer + 1) / 2]) {
-        if constexpr (kPer == 1) v[0] = *reinterpret_cast<const uint16_t*>(p);
-        else if constexpr (kPer == 2) v[0] = *reinterpret_cast<const uint32_t*>(p);
+    auto groups = [&](const char* p, int kt, uint32_t (&v)[(kPer + 1) / 2]) {
+        const __amdgpu_buffer_rsrc_t r = part(p, kt, 32 * kPer);
+        const uint32_t off = (uint32_t)(c * 2 * kPer);
+        if constexpr (kPer == 1) v[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+        else if constexpr (kPer == 2) v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
         else {
-            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            const uint2 u = bload8(r, off);
             v[0] = u.x;
             v[1] = u.y;
         }
@@ -105,29 +129,64 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
     auto value = [&](const uint32_t (&v)[(kPer + 1) / 2], int p) {
         return (p & 1) ? bf16_hi(v[p / 2]) : bf16_lo(v[p / 2]);
     };
+    const uint32_t mask = code_mask();
     const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    const int waves = blockDim.x >> 6;
 
-    for (int64_t r0 = lo; r0 < hi; r0 += kQ4Rows) {
-        const int64_t have = hi - r0 < kQ4Rows ? hi - r0 : kQ4Rows;
-        // rows past the last one repeat it (their results are not stored)
-        const uint16_t* xrow = a.X + (r0 + (c < have ? c : have - 1)) * a.K;
+    // Rows r0 .. r0 + have, loaded with kXLoads loads per tile: of 4, 8 or 16 rows.
+    auto rows = [&](int r0, int have, auto loads) {
+        constexpr int kXLoads = loads.value;
+        struct Stage {
+            uint4 w[kNT], x[kXLoads];
+            uint32_t s[kNT][(kPer + 1) / 2], z[kNT][(kPer + 1) / 2];
+        };
+        // A load takes 256 B of each of four rows, 16 lanes in order: the operand's own order (64 B
+        // of 16 rows, neighbours in lanes 16 apart) is 64 accesses instead of eight lines.  Rows
+        // past the last one and, in the last tile, k past K read zeros.
+        uint32_t xin[kXLoads], xlast[kXLoads];
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j) {
+            xin[j] = (uint32_t)((4 * j + (lane >> 4)) * a.K * 2 + 16 * c);
+            xlast[j] = (a.kt - 1) * kQ4TileK + 8 * c < a.K ? xin[j] : kOOB;
+        }
+        const int xbytes = (int)(have * a.K * 2);
         auto load = [&](Stage& st, int kt) {
 #pragma unroll
-            for (int i = 0; i < kNT; ++i) {
-                st.w[i] = ld16(wp[i] + (int64_t)kt * 1024);
-                groups(sp[i] + (int64_t)kt * (32 * kPer), st.s[i]);
-                if (zeros) groups(zp[i] + (int64_t)kt * (32 * kPer), st.z[i]);
-            }
+            for (int i = 0; i < kNT; ++i) st.w[i] = bload16(part(wp[i], kt, 1024), (uint32_t)(lane * 16));
+            const int past = kt * kQ4TileK * 2;
+            const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint16_t*>(a.X) + (int64_t)r0 * a.K + (int64_t)kt * kQ4TileK, (short)0,
+                kt < a.kt ? xbytes - past : 0, kRsrcWord3);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t k0 = (int64_t)kt * kQ4TileK + 32 * j + 8 * g;
-                st.x[j] = k0 < a.K ? ld16(xrow + k0) : zero16();
+            for (int j = 0; j < kXLoads; ++j) st.x[j] = bload16(rx, kt < a.kt - 1 ? xin[j] : xlast[j]);
+#pragma unroll
+            for (int i = 0; i < kNT; ++i) {
+                groups(sp[i], kt, st.s[i]);
+                if constexpr (kZero) groups(zp[i], kt, st.z[i]);
             }
+        };
+        // The operands of a tile's four steps, through the wave's own LDS (a wave's LDS accesses
+        // keep their order): row r's 16-byte piece p lies at 256 r + 16 (p ^ r), so that neither
+        // the writes (16 pieces of a row) nor the reads (one piece of 16 rows) meet in a bank.
+        // Rows that no load brings hold what was there; their results are not stored.
+        auto operands = [&](const Stage& st, uint4 (&x)[4]) {
+            lanes_meet();   // (the last tile's reads)
+#pragma unroll
+            for (int j = 0; j < kXLoads; ++j) {
+                const int r = 4 * j + (lane >> 4);
+                *reinterpret_cast<uint4*>(s_wave + 256 * r + 16 * (c ^ r)) = st.x[j];
+            }
+            lanes_meet();
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x[s] = *reinterpret_cast<const uint4*>(s_wave + 256 * c + 16 * ((4 * s + g) ^ c));
         };
         floatx4_t acc[kNT];
 #pragma unroll
         for (int i = 0; i < kNT; ++i) acc[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
         auto multiply = [&](const Stage& st, int kt) {
+            uint4 x[4];
+            operands(st, x);
 #pragma unroll
             for (int p = 0; p < kPer; ++p) {
                 // a group past K: its scale may be anything
@@ -135,18 +194,19 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
                 floatx4_t xs = {0.f, 0.f, 0.f, 0.f};
                 if constexpr (kCode == kQ4Int)
 #pragma unroll
-                    for (int j = 0; j < kSteps; ++j) xs = mfma16x16x32(st.x[p * kSteps + j], ones, xs);
+                    for (int j = 0; j < kSteps; ++j) xs = mfma16x16x32(x[p * kSteps + j], ones, xs);
 #pragma unroll
                 for (int i = 0; i < kNT; ++i) {
                     const uint32_t words[4] = {st.w[i].x, st.w[i].y, st.w[i].z, st.w[i].w};
                     floatx4_t sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int j = 0; j < kSteps; ++j)
-                        sum = mfma16x16x32(st.x[p * kSteps + j],
-                                           decode8(words[p * kSteps + j], std::integral_constant<int, kCode>()), sum);
+                        sum = mfma16x16x32(x[p * kSteps + j],
+                                           decode8(words[p * kSteps + j], mask, std::integral_constant<int, kCode>()), sum);
                     const float s = real ? value(st.s[i], p) : 0.f;
                     if constexpr (kCode == kQ4Int) {
-                        const float z = 16.f + (zeros ? (real ? value(st.z[i], p) : 0.f) : 8.f);
+                        float z = 24.f;
+                        if constexpr (kZero) z = 16.f + (real ? value(st.z[i], p) : 0.f);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(s, fmaf(-z, xs[r], sum[r]), acc[i][r]);
                     } else {
@@ -156,30 +216,47 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
                 }
             }
         };
-        Stage st[2];
-        int kt = wave;
-        if (kt < a.kt) load(st[0], kt);
-        for (; kt < a.kt; kt += 2 * waves) {
-            if (kt + waves < a.kt) load(st[1], kt + waves);
-            multiply(st[0], kt);
-            if (kt + 2 * waves < a.kt) load(st[0], kt + 2 * waves);
-            if (kt + waves < a.kt) multiply(st[1], kt + waves);
+        constexpr int kDepth = 2;
+        Stage st[kDepth];
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            load(st[d], wave + d * waves);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // result: lane holds row 4 g + r, column c
+        for (int kt = wave; kt < a.kt; kt += kDepth * waves) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                // (left alone, the scheduler joins the stages and waits for all loads at once)
+                multiply(st[d], kt + d * waves);
+                __builtin_amdgcn_sched_barrier(0);
+                load(st[d], kt + (d + kDepth) * waves);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kNT; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s_red[((wave * kNT + i) * 16 + 4 * g + r) * 16 + c] = acc[i][r];
+            *reinterpret_cast<floatx4_t*>(s_wave + 1024 * i + 16 * lane) = acc[i];
+    };
+
+    for (int r0 = lo; r0 < hi; r0 += kQ4Rows) {
+        const int have = hi - r0 < kQ4Rows ? hi - r0 : kQ4Rows;
+        if (have <= 4) rows(r0, have, std::integral_constant<int, 1>());
+        else if (have <= 8) rows(r0, have, std::integral_constant<int, 2>());
+        else rows(r0, have, std::integral_constant<int, 4>());
         __syncthreads();
         for (int o = threadIdx.x; o < kTiles * 256; o += blockDim.x) {
-            const int t = o >> 8, m = (o >> 4) & 15;
-            const int64_t col = (ct0 + t) * kQ4TileCols + (o & 15);
+            // a lane's four sums are rows 4 (lane / 16) .. + 3 of column lane % 16
+            const int t = o >> 8, m = 4 * ((o >> 6) & 3) + (o & 3);
+            const int64_t col = (ct0 + t) * kQ4TileCols + ((o >> 2) & 15);
             float v[kMats];
 #pragma unroll
-            for (int q = 0; q < kMats; ++q) {
-                v[q] = 0.f;
-                for (int w = 0; w < waves; ++w) v[q] += s_red[(w * kNT + q * kTiles) * 256 + o];
-            }
+            for (int q = 0; q < kMats; ++q) v[q] = 0.f;
+            for (int w = 0; w < waves; w += 4)      // (waves is a multiple of four)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int q = 0; q < kMats; ++q)
+                        v[q] += *reinterpret_cast<const float*>(s_all + (w + u) * kWaveLds + 1024 * (q * kTiles) + 4 * o);
             if (m >= have || col >= a.C) continue;
             float y;
             if constexpr (kGated) {
@@ -188,7 +265,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
                 if (a.bias) v[0] += bf16_to_f32(a.bias[e * a.b_stride + col]);
                 y = apply_act(a.act, v[0]);
             }
-            a.Y[(r0 + m) * a.C + col] = __builtin_bit_cast(uint16_t, (__bf16)y);
+            a.Y[(int64_t)(r0 + m) * a.C + col] = __builtin_bit_cast(uint16_t, (__bf16)y);
         }
         if (r0 + kQ4Rows < hi) __syncthreads();   // read before the next rows' sums
     }
@@ -295,13 +372,34 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* codes, cons
     }
 }
 
-template <int kCode, int kPer, bool kGated>
-void start(const Q4Args& a, int tiles_per, int waves, int E, hipStream_t stream) {
-    const int64_t tiles = (a.C + kQ4TileCols - 1) / kQ4TileCols;
-    const dim3 grid((unsigned)((tiles + tiles_per - 1) / tiles_per), (unsigned)E), block(64 * waves);
-    const size_t lds = (size_t)waves * tiles_per * (kGated ? 2 : 1) * 1024;   // at most 64 KiB
-    if (tiles_per == 1) hipLaunchKernelGGL((q4_kernel<kCode, kPer, kGated, 1>), grid, block, lds, stream, a);
-    else hipLaunchKernelGGL((q4_kernel<kCode, kPer, kGated, 2>), grid, block, lds, stream, a);
+// Column tiles per wave and waves per workgroup.  Two tiles share a wave's rows of X, which
+// for 16 rows are more bytes than a tile's codes, and halve the workgroups: taken where at
+// least one workgroup per CU is left (16 x 8192 x 8192: 12.6 -> 10.8 us; 16 x 4096 x 4096, 128
+// workgroups: 5.3 -> 6.4 us; the gated pair shares them already).  Few workgroups take eight
+// waves each (16 rows, pair of 8192 x 3584, 224 workgroups: 10.3 us, with four 11.6), many take
+// four, of which more fit a CU while others join their sums (pair of 4096 x 14336, 896: 17.7 ->
+// 15.8 us).
+struct Q4Shape {
+    int tiles, waves;
+};
+Q4Shape q4_shape(const Q4IO& io, int64_t tiles, int kt) {
+    Q4Shape s;
+    s.tiles = !io.gated && tiles * io.E >= 512 ? 2 : 1;
+    const int64_t groups = (tiles + s.tiles - 1) / s.tiles * io.E;
+    s.waves = groups >= 640 || kt <= 4 ? 4 : kMaxWaves;
+    return s;
+}
+
+template <int kCode, bool kZero, int kPer>
+void start(const Q4Args& a, const Q4Shape& s, const Q4IO& io, int64_t tiles, hipStream_t stream) {
+    const dim3 grid((unsigned)((tiles + s.tiles - 1) / s.tiles), (unsigned)io.E), block(64 * s.waves);
+    const size_t lds = (size_t)s.waves * kWaveLds;
+    if (io.gated)
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, true, 1>), grid, block, lds, stream, a);
+    else if (s.tiles == 1)
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 1>), grid, block, lds, stream, a);
+    else
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 2>), grid, block, lds, stream, a);
 }
 
 }  // namespace
@@ -320,27 +418,24 @@ hipError_t launch_q4(const Q4IO& io, hipStream_t stream) {
     a.bias = io.bias;
     a.Y = io.Y;
     a.offsets = io.offsets;
-    a.rows = io.rows;
+    a.rows = (int)io.rows;
     a.K = io.K;
     a.C = io.C;
     a.w_stride = tiles * a.kt * 1024;
     a.s_stride = tiles * a.kt * 32 * per;
     a.b_stride = io.C;
     a.act = io.act;
-    int waves = kMaxWaves;
-    while (waves > 1 && waves / 2 >= a.kt) waves /= 2;
-    const int tiles_per = 1;
-    auto go = [&](auto code, auto p) {
-        if (io.gated) start<code.value, p.value, true>(a, tiles_per, waves, io.E, stream);
-        else start<code.value, p.value, false>(a, tiles_per, waves, io.E, stream);
+    const Q4Shape s = q4_shape(io, tiles, a.kt);
+    auto go = [&](auto code, auto z, auto p) { start<code.value, z.value, p.value>(a, s, io, tiles, stream); };
+    auto with = [&](auto code, auto z) {
+        if (per == 1) go(code, z, std::integral_constant<int, 1>());
+        else if (per == 2) go(code, z, std::integral_constant<int, 2>());
+        else go(code, z, std::integral_constant<int, 4>());
     };
-    auto with = [&](auto code) {
-        if (per == 1) go(code, std::integral_constant<int, 1>());
-        else if (per == 2) go(code, std::integral_constant<int, 2>());
-        else go(code, std::integral_constant<int, 4>());
-    };
-    if (io.code == kQ4Int) with(std::integral_constant<int, kQ4Int>());
-    else with(std::integral_constant<int, kQ4E2m1>());
+    using Int = std::integral_constant<int, kQ4Int>;
+    if (io.code == kQ4E2m1) with(std::integral_constant<int, kQ4E2m1>(), std::false_type());
+    else if (io.zero[0]) with(Int(), std::true_type());
+    else with(Int(), std::false_type());
     return hipGetLastError();
 }
 
