@@ -266,6 +266,35 @@ def _torch_dtype(code):
     return torch.bfloat16 if code == BF16 else torch.float32
 
 
+def _tensors(need, may=()):
+    """Checks (tensor, name, shape, dtype) as ``_arg`` and ``_on_device`` do, in one pass for calls of a few
+    microseconds; ``may``: those that may be None.  Returns the device's index."""
+    import torch
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    elsewhere = dev < 0
+    for spec in (need, may) if may else (need,):
+        for t, name, shape, dtype in spec:
+            if t is None:
+                if spec is need:
+                    raise ValueError(f"{name} must not be None")
+                continue
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+                _arg(t, name, shape, dtype)
+            if t.get_device() != dev:
+                elsewhere = True
+    if elsewhere:
+        _on_device(*(s[0] for s in (*need, *may)))
+    return dev
+
+
+def _stream_of(stream, dev):
+    """The call's stream: the given one, or the current one of the device that its tensors are on."""
+    if stream is not None:
+        return stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def ffn_workspace_size(M, N, O, P, dtype=BF16, variant=VARIANT_AUTO) -> int:
     return lib().ffn_workspace_size_ex(M, N, O, P, dtype, variant)
 
@@ -486,28 +515,24 @@ def ffn_layernorm_backward(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws=None,
                                         ws.numel(), _stream(stream)))
 
 
-def _rmsnorm_args(X, gamma, R, S, rstd):
+def _rmsnorm_args(X, gamma, R, S, rstd, *more):
     import torch
     M, N = _dims(X, "X", 2)
     dt = _dtype_code(X)
-    _arg(X, "X", (M, N), X.dtype)
-    _arg(gamma, "gamma", (N,), X.dtype)
-    _arg(R, "R", (M, N), X.dtype, optional=True)
-    _arg(S, "S", (M, N), X.dtype, optional=True)
-    _arg(rstd, "rstd", (M,), torch.float32, optional=True)
     if (R is None) != (S is None):
         raise ValueError("S is written with R alone: give both or neither")
-    return M, N, dt
+    full, d = (M, N), X.dtype
+    dev = _tensors(((X, "X", full, d), (gamma, "gamma", (N,), d), *more),
+                   ((R, "R", full, d), (S, "S", full, d), (rstd, "rstd", (M,), torch.float32)))
+    return M, N, dt, dev
 
 
 def ffn_rmsnorm_forward(X, gamma, Y, R=None, S=None, rstd=None, eps=1e-5, stream=None):
     """``S = X + R`` (where a residual ``R`` is given) and ``Y = S rstd gamma`` over the last dimension
     (M x N, bf16 or fp32); ``S``, ``Y`` and, when given, ``rstd`` (M, fp32) are written in place."""
-    M, N, dt = _rmsnorm_args(X, gamma, R, S, rstd)
-    _arg(Y, "Y", (M, N), X.dtype)
-    _on_device(X, gamma, Y, R, S, rstd)
-    _check(lib().ffn_rmsnorm_forward(_ptr(X), _ptr(R), _ptr(gamma), _ptr(S), _ptr(Y), _ptr(rstd), M, N, dt,
-                                     float(eps), _stream(stream)))
+    M, N, dt, dev = _rmsnorm_args(X, gamma, R, S, rstd, (Y, "Y", X.shape, X.dtype))
+    _check(lib().ffn_rmsnorm_forward(X.data_ptr(), _ptr(R), gamma.data_ptr(), _ptr(S), Y.data_ptr(), _ptr(rstd), M, N,
+                                     dt, eps, _stream_of(stream, dev)))
     return Y
 
 
@@ -515,14 +540,13 @@ def ffn_rmsnorm_q8_forward(X, gamma, Q, scale, R=None, S=None, rstd=None, group=
     """As ``ffn_rmsnorm_forward`` with the output as e4m3 codes ``Q`` (M x N, float8_e4m3fn) and fp32
     ``scale``: M x ceil(N / 128) for groups of 128 columns, M x 1 for whole rows (``group=0``)."""
     import torch
-    M, N, dt = _rmsnorm_args(X, gamma, R, S, rstd)
     if group not in (0, 128):
         raise ValueError(f"group must be 128, or 0 for whole rows (got {group})")
-    _arg(Q, "Q", (M, N), torch.float8_e4m3fn)
-    _arg(scale, "scale", (M, -(-N // group) if group else 1), torch.float32)
-    _on_device(X, gamma, Q, scale, R, S, rstd)
-    _check(lib().ffn_rmsnorm_q8_forward(_ptr(X), _ptr(R), _ptr(gamma), _ptr(S), _ptr(Q), _ptr(scale), _ptr(rstd),
-                                        M, N, dt, group, float(eps), _stream(stream)))
+    M, N = _dims(X, "X", 2)
+    M, N, dt, dev = _rmsnorm_args(X, gamma, R, S, rstd, (Q, "Q", X.shape, torch.float8_e4m3fn),
+                                  (scale, "scale", (M, -(-N // group) if group else 1), torch.float32))
+    _check(lib().ffn_rmsnorm_q8_forward(X.data_ptr(), _ptr(R), gamma.data_ptr(), _ptr(S), Q.data_ptr(),
+                                        scale.data_ptr(), _ptr(rstd), M, N, dt, group, eps, _stream_of(stream, dev)))
     return Q
 
 
@@ -537,20 +561,16 @@ def ffn_rmsnorm_backward(S, dY, gamma, rstd, dX, dgamma, dS=None, ws=None, strea
     import torch
     M, N = _dims(S, "S", 2)
     dt = _dtype_code(S)
-    f32 = torch.float32
-    _arg(S, "S", (M, N), S.dtype)
-    _arg(dY, "dY", (M, N), S.dtype)
-    _arg(gamma, "gamma", (N,), S.dtype)
-    _arg(rstd, "rstd", (M,), f32)
-    _arg(dX, "dX", (M, N), S.dtype)
-    _arg(dgamma, "dgamma", (N,), f32)
-    _arg(dS, "dS", (M, N), S.dtype, optional=True)
+    f32, full, d = torch.float32, (M, N), S.dtype
     _ws_arg(ws)
-    _on_device(S, dY, gamma, rstd, dX, dgamma, dS, ws)
+    dev = _tensors(((S, "S", full, d), (dY, "dY", full, d), (gamma, "gamma", (N,), d), (rstd, "rstd", (M,), f32),
+                    (dX, "dX", full, d), (dgamma, "dgamma", (N,), f32)),
+                   ((dS, "dS", full, d), (ws, "ws", () if ws is None else ws.shape, torch.uint8)))
     if ws is None:
         ws = _own_workspace(ffn_rmsnorm_backward_workspace_size(M, N, dt), S.device, stream)
-    _check(lib().ffn_rmsnorm_backward(_ptr(S), _ptr(dY), _ptr(dS), _ptr(gamma), _ptr(rstd), _ptr(dX), _ptr(dgamma),
-                                      M, N, dt, _ptr(ws), ws.numel(), _stream(stream)))
+    _check(lib().ffn_rmsnorm_backward(S.data_ptr(), dY.data_ptr(), _ptr(dS), gamma.data_ptr(), rstd.data_ptr(),
+                                      dX.data_ptr(), dgamma.data_ptr(), M, N, dt, ws.data_ptr(), ws.numel(),
+                                      _stream_of(stream, dev)))
 
 
 def ffn_orthogonalize_workspace_size(B, R, C, dtype=BF16) -> int:
@@ -702,12 +722,6 @@ def moe_dispatch(X, topk_ids, Xs, expert_offsets, sorted_entries, positions, sca
     E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
     i32 = torch.int32
     dt = E4M3 if X.dtype == torch.float8_e4m3fn else _dtype_code(X)
-    _arg(X, "X", (M, N), X.dtype)
-    _arg(topk_ids, "topk_ids", (M, k), i32)
-    _arg(Xs, "Xs", (M * k, N), X.dtype)
-    _arg(expert_offsets, "expert_offsets", (E + 1,), i32)
-    _arg(sorted_entries, "sorted_entries", (M * k,), i32)
-    _arg(positions, "positions", (M, k), i32)
     if (scale is None) != (scale_sorted is None):
         raise ValueError("give scale and scale_sorted together or neither")
     G = 0
@@ -715,15 +729,17 @@ def moe_dispatch(X, topk_ids, Xs, expert_offsets, sorted_entries, positions, sca
         G = _dims(scale, "scale", 2)[1]
         if G < 1:
             raise ValueError("scale must have columns")
-        _arg(scale, "scale", (M, G), torch.float32)
-        _arg(scale_sorted, "scale_sorted", (M * k, G), torch.float32)
     _ws_arg(ws)
-    _on_device(X, topk_ids, Xs, expert_offsets, sorted_entries, positions, scale, scale_sorted, ws)
+    dev = _tensors(((X, "X", (M, N), X.dtype), (topk_ids, "topk_ids", (M, k), i32), (Xs, "Xs", (M * k, N), X.dtype),
+                    (expert_offsets, "expert_offsets", (E + 1,), i32),
+                    (sorted_entries, "sorted_entries", (M * k,), i32), (positions, "positions", (M, k), i32)),
+                   ((scale, "scale", (M, G), torch.float32), (scale_sorted, "scale_sorted", (M * k, G), torch.float32),
+                    (ws, "ws", () if ws is None else ws.shape, torch.uint8)))
     if ws is None:
         ws = _own_workspace(moe_dispatch_workspace_size(M, E, k), X.device, stream)
-    _check(lib().moe_dispatch(_ptr(X), _ptr(topk_ids), _ptr(scale), M, N, E, k, dt, G, _ptr(Xs), _ptr(scale_sorted),
-                              _ptr(expert_offsets), _ptr(sorted_entries), _ptr(positions), _ptr(ws), ws.numel(),
-                              _stream(stream)))
+    _check(lib().moe_dispatch(X.data_ptr(), topk_ids.data_ptr(), _ptr(scale), M, N, E, k, dt, G, Xs.data_ptr(),
+                              _ptr(scale_sorted), expert_offsets.data_ptr(), sorted_entries.data_ptr(),
+                              positions.data_ptr(), ws.data_ptr(), ws.numel(), _stream_of(stream, dev)))
     return Xs
 
 
@@ -734,11 +750,10 @@ def moe_dispatch_backward(dXs, positions, dX, stream=None):
     k = _dims(positions, "positions", 2)[1]
     dt = _dtype_code(dX)
     rows = _dims(dXs, "dXs", 2)[0]
-    _arg(dXs, "dXs", (rows, N), dX.dtype)
-    _arg(positions, "positions", (M, k), torch.int32)
-    _arg(dX, "dX", (M, N), dX.dtype)
-    _on_device(dXs, positions, dX)
-    _check(lib().moe_dispatch_backward(_ptr(dXs), _ptr(positions), _ptr(dX), M, N, k, rows, dt, _stream(stream)))
+    dev = _tensors(((dXs, "dXs", (rows, N), dX.dtype), (positions, "positions", (M, k), torch.int32),
+                    (dX, "dX", (M, N), dX.dtype)))
+    _check(lib().moe_dispatch_backward(dXs.data_ptr(), positions.data_ptr(), dX.data_ptr(), M, N, k, rows, dt,
+                                       _stream_of(stream, dev)))
     return dX
 
 
@@ -750,14 +765,11 @@ def moe_combine(Ys, positions, Y, topk_w=None, R=None, stream=None):
     k = _dims(positions, "positions", 2)[1]
     dt = _dtype_code(Y)
     rows = _dims(Ys, "Ys", 2)[0]
-    _arg(Ys, "Ys", (rows, N), Y.dtype)
-    _arg(positions, "positions", (M, k), torch.int32)
-    _arg(topk_w, "topk_w", (M, k), torch.float32, optional=True)
-    _arg(R, "R", (M, N), Y.dtype, optional=True)
-    _arg(Y, "Y", (M, N), Y.dtype)
-    _on_device(Ys, positions, topk_w, R, Y)
-    _check(lib().moe_combine(_ptr(Ys), _ptr(positions), _ptr(topk_w), _ptr(R), _ptr(Y), M, N, k, rows, dt,
-                             _stream(stream)))
+    dev = _tensors(((Ys, "Ys", (rows, N), Y.dtype), (positions, "positions", (M, k), torch.int32),
+                    (Y, "Y", (M, N), Y.dtype)),
+                   ((topk_w, "topk_w", (M, k), torch.float32), (R, "R", (M, N), Y.dtype)))
+    _check(lib().moe_combine(Ys.data_ptr(), positions.data_ptr(), _ptr(topk_w), _ptr(R), Y.data_ptr(), M, N, k, rows,
+                             dt, _stream_of(stream, dev)))
     return Y
 
 
@@ -771,15 +783,12 @@ def moe_combine_backward(dY, Ys, positions, topk_w, dYs, dw, stream=None):
     rows = _dims(dYs, "dYs", 2)[0]
     if (Ys is None) != (dw is None):
         raise ValueError("dw takes Ys: give both or neither")
-    _arg(dY, "dY", (M, N), dY.dtype)
-    _arg(Ys, "Ys", (rows, N), dY.dtype, optional=True)
-    _arg(positions, "positions", (M, k), torch.int32)
-    _arg(topk_w, "topk_w", (M, k), torch.float32, optional=True)
-    _arg(dYs, "dYs", (rows, N), dY.dtype)
-    _arg(dw, "dw", (M, k), torch.float32, optional=True)
-    _on_device(dY, Ys, positions, topk_w, dYs, dw)
-    _check(lib().moe_combine_backward(_ptr(dY), _ptr(Ys), _ptr(positions), _ptr(topk_w), _ptr(dYs), _ptr(dw), M, N,
-                                      k, rows, dt, _stream(stream)))
+    f32 = torch.float32
+    dev = _tensors(((dY, "dY", (M, N), dY.dtype), (positions, "positions", (M, k), torch.int32),
+                    (dYs, "dYs", (rows, N), dY.dtype)),
+                   ((Ys, "Ys", (rows, N), dY.dtype), (topk_w, "topk_w", (M, k), f32), (dw, "dw", (M, k), f32)))
+    _check(lib().moe_combine_backward(dY.data_ptr(), _ptr(Ys), positions.data_ptr(), _ptr(topk_w), dYs.data_ptr(),
+                                      _ptr(dw), M, N, k, rows, dt, _stream_of(stream, dev)))
 
 
 def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None):
@@ -788,12 +797,10 @@ def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None):
     M, E = _dims(dlogits, "dlogits", 2)
     k = _dims(topk_ids, "topk_ids", 2)[1]
     f32 = torch.float32
-    _arg(topk_ids, "topk_ids", (M, k), torch.int32)
-    _arg(topk_w, "topk_w", (M, k), f32)
-    _arg(dw, "dw", (M, k), f32)
-    _arg(dlogits, "dlogits", (M, E), f32)
-    _on_device(topk_ids, topk_w, dw, dlogits)
-    _check(lib().moe_route_backward(_ptr(topk_ids), _ptr(topk_w), _ptr(dw), _ptr(dlogits), M, E, k, _stream(stream)))
+    dev = _tensors(((topk_ids, "topk_ids", (M, k), torch.int32), (topk_w, "topk_w", (M, k), f32),
+                    (dw, "dw", (M, k), f32), (dlogits, "dlogits", (M, E), f32)))
+    _check(lib().moe_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), dw.data_ptr(), dlogits.data_ptr(), M, E,
+                                    k, _stream_of(stream, dev)))
     return dlogits
 
 
@@ -819,17 +826,16 @@ def _q4_code(code):
     return Q4_CODES[code] if isinstance(code, str) else int(code)
 
 
-def _q4_weight(Wq, scale, zero, lead, K, C, names):
-    """Checks one packed weight; returns its group size."""
+def _q4_weight(Wq, scale, zero, lead, K, C, names=("Wq", "scale", "zero")):
+    """The group size of one packed weight, and what ``_tensors`` checks of it: (needed, optional)."""
     import torch
     ct, kt = -(-C // 16), -(-K // 128)
-    _arg(Wq, names[0], (*lead, ct, kt, 1024), torch.uint8)
     per = _dims(scale, names[1], 4 + len(lead))[-1]
     if per not in (1, 2, 4):
         raise ValueError(f"{names[1]} must have 1, 2 or 4 groups per 128 rows (got {per})")
-    _arg(scale, names[1], (*lead, ct, kt, 16, per), torch.bfloat16)
-    _arg(zero, names[2], scale.shape, torch.bfloat16, optional=True)
-    return 128 // per
+    groups = (*lead, ct, kt, 16, per)
+    return 128 // per, ((Wq, names[0], (*lead, ct, kt, 1024), torch.uint8),
+                        (scale, names[1], groups, torch.bfloat16)), (zero, names[2], groups, torch.bfloat16)
 
 
 def ffn_q4_quantize(W, Wq, scale, zero=None, code="int4", stream=None):
@@ -837,11 +843,10 @@ def ffn_q4_quantize(W, Wq, scale, zero=None, code="int4", stream=None):
     (``ffn_q4_empty`` makes the buffers; the group size is the scales'), written in place."""
     K, C = _dims(W, "W", 2)
     dt = _dtype_code(W)
-    _arg(W, "W", (K, C), W.dtype)
-    group = _q4_weight(Wq, scale, zero, (), K, C, ("Wq", "scale", "zero"))
-    _on_device(W, Wq, scale, zero)
-    _check(lib().ffn_q4_quantize(_ptr(W), _ptr(Wq), _ptr(scale), _ptr(zero), K, C, dt, _q4_code(code), group,
-                                 _stream(stream)))
+    group, packed, z = _q4_weight(Wq, scale, zero, (), K, C)
+    dev = _tensors(((W, "W", (K, C), W.dtype), *packed), (z,))
+    _check(lib().ffn_q4_quantize(W.data_ptr(), Wq.data_ptr(), scale.data_ptr(), _ptr(zero), K, C, dt, _q4_code(code),
+                                 group, _stream_of(stream, dev)))
     return Wq
 
 
@@ -850,15 +855,14 @@ def ffn_q4_pack(codes, scale_in, Wq, scale, zero_in=None, zero=None, code="int4"
     layout, written in place."""
     import torch
     K, C = _dims(codes, "codes", 2)
-    _arg(codes, "codes", (K, C), torch.uint8)
-    group = _q4_weight(Wq, scale, zero, (), K, C, ("Wq", "scale", "zero"))
+    group, packed, z = _q4_weight(Wq, scale, zero, (), K, C)
     if (zero_in is None) != (zero is None):
         raise ValueError("give zero_in and zero together or neither")
-    _arg(scale_in, "scale_in", (-(-K // group), C), torch.bfloat16)
-    _arg(zero_in, "zero_in", (-(-K // group), C), torch.bfloat16, optional=True)
-    _on_device(codes, scale_in, Wq, scale, zero_in, zero)
-    _check(lib().ffn_q4_pack(_ptr(codes), _ptr(scale_in), _ptr(zero_in), _ptr(Wq), _ptr(scale), _ptr(zero), K, C,
-                             _q4_code(code), group, _stream(stream)))
+    rows = (-(-K // group), C)
+    dev = _tensors(((codes, "codes", (K, C), torch.uint8), (scale_in, "scale_in", rows, torch.bfloat16), *packed),
+                   ((zero_in, "zero_in", rows, torch.bfloat16), z))
+    _check(lib().ffn_q4_pack(codes.data_ptr(), scale_in.data_ptr(), _ptr(zero_in), Wq.data_ptr(), scale.data_ptr(),
+                             _ptr(zero), K, C, _q4_code(code), group, _stream_of(stream, dev)))
     return Wq
 
 
@@ -869,23 +873,21 @@ def ffn_q4_matvec(X, Wq, scale, Y, zero=None, bias=None, act="none", code="int4"
     M, K = _dims(X, "X", 2)
     C = _dims(Y, "Y", 2)[1]
     bf = torch.bfloat16
-    _arg(X, "X", (M, K), bf)
-    group = _q4_weight(Wq, scale, zero, (), K, C, ("Wq", "scale", "zero"))
-    _arg(bias, "bias", (C,), bf, optional=True)
-    _arg(Y, "Y", (M, C), bf)
-    _on_device(X, Wq, scale, zero, bias, Y)
-    _check(lib().ffn_q4_matvec(_ptr(X), _ptr(Wq), _ptr(scale), _ptr(zero), _ptr(bias), _ptr(Y), M, K, C,
-                               _q4_code(code), group, _act(act), _stream(stream)))
+    group, packed, z = _q4_weight(Wq, scale, zero, (), K, C)
+    dev = _tensors(((X, "X", (M, K), bf), (Y, "Y", (M, C), bf), *packed), (z, (bias, "bias", (C,), bf)))
+    _check(lib().ffn_q4_matvec(X.data_ptr(), Wq.data_ptr(), scale.data_ptr(), _ptr(zero), _ptr(bias), Y.data_ptr(), M,
+                               K, C, _q4_code(code), group, _act(act), _stream_of(stream, dev)))
     return Y
 
 
 def _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, lead, K, C):
-    group = _q4_weight(Wg, scale_g, zero_g, lead, K, C, ("Wg", "scale_g", "zero_g"))
-    if _q4_weight(Wu, scale_u, zero_u, lead, K, C, ("Wu", "scale_u", "zero_u")) != group:
-        raise ValueError("both matrices must have the same group size")
     if (zero_g is None) != (zero_u is None):
         raise ValueError("give both zero points or neither")
-    return group
+    group, g, zg = _q4_weight(Wg, scale_g, zero_g, lead, K, C, ("Wg", "scale_g", "zero_g"))
+    group_u, u, zu = _q4_weight(Wu, scale_u, zero_u, lead, K, C, ("Wu", "scale_u", "zero_u"))
+    if group_u != group:
+        raise ValueError("both matrices must have the same group size")
+    return group, (*g, *u), (zg, zu)
 
 
 def ffn_q4_swiglu(X, Wg, scale_g, Wu, scale_u, H, zero_g=None, zero_u=None, code="int4", stream=None):
@@ -894,12 +896,12 @@ def ffn_q4_swiglu(X, Wg, scale_g, Wu, scale_u, H, zero_g=None, zero_u=None, code
     import torch
     M, K = _dims(X, "X", 2)
     C = _dims(H, "H", 2)[1]
-    _arg(X, "X", (M, K), torch.bfloat16)
-    group = _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, (), K, C)
-    _arg(H, "H", (M, C), torch.bfloat16)
-    _on_device(X, Wg, scale_g, zero_g, Wu, scale_u, zero_u, H)
-    _check(lib().ffn_q4_swiglu(_ptr(X), _ptr(Wg), _ptr(scale_g), _ptr(zero_g), _ptr(Wu), _ptr(scale_u), _ptr(zero_u),
-                               _ptr(H), M, K, C, _q4_code(code), group, _stream(stream)))
+    bf = torch.bfloat16
+    group, packed, z = _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, (), K, C)
+    dev = _tensors(((X, "X", (M, K), bf), (H, "H", (M, C), bf), *packed), z)
+    _check(lib().ffn_q4_swiglu(X.data_ptr(), Wg.data_ptr(), scale_g.data_ptr(), _ptr(zero_g), Wu.data_ptr(),
+                               scale_u.data_ptr(), _ptr(zero_u), H.data_ptr(), M, K, C, _q4_code(code), group,
+                               _stream_of(stream, dev)))
     return H
 
 
@@ -912,14 +914,13 @@ def moe_q4_matvec(X, expert_offsets, Wq, scale, Y, zero=None, bias=None, act="no
     C = _dims(Y, "Y", 2)[1]
     E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
     bf = torch.bfloat16
-    _arg(X, "X", (rows, K), bf)
-    _arg(expert_offsets, "expert_offsets", (E + 1,), torch.int32)
-    group = _q4_weight(Wq, scale, zero, (E,), K, C, ("Wq", "scale", "zero"))
-    _arg(bias, "bias", (E, C), bf, optional=True)
-    _arg(Y, "Y", (rows, C), bf)
-    _on_device(X, expert_offsets, Wq, scale, zero, bias, Y)
-    _check(lib().moe_q4_matvec(_ptr(X), _ptr(expert_offsets), _ptr(Wq), _ptr(scale), _ptr(zero), _ptr(bias), _ptr(Y),
-                               rows, E, K, C, _q4_code(code), group, _act(act), _stream(stream)))
+    group, packed, z = _q4_weight(Wq, scale, zero, (E,), K, C)
+    dev = _tensors(((X, "X", (rows, K), bf), (Y, "Y", (rows, C), bf),
+                    (expert_offsets, "expert_offsets", (E + 1,), torch.int32), *packed),
+                   (z, (bias, "bias", (E, C), bf)))
+    _check(lib().moe_q4_matvec(X.data_ptr(), expert_offsets.data_ptr(), Wq.data_ptr(), scale.data_ptr(), _ptr(zero),
+                               _ptr(bias), Y.data_ptr(), rows, E, K, C, _q4_code(code), group, _act(act),
+                               _stream_of(stream, dev)))
     return Y
 
 
@@ -930,14 +931,13 @@ def moe_q4_swiglu(X, expert_offsets, Wg, scale_g, Wu, scale_u, H, zero_g=None, z
     rows, K = _dims(X, "X", 2)
     C = _dims(H, "H", 2)[1]
     E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
-    _arg(X, "X", (rows, K), torch.bfloat16)
-    _arg(expert_offsets, "expert_offsets", (E + 1,), torch.int32)
-    group = _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, (E,), K, C)
-    _arg(H, "H", (rows, C), torch.bfloat16)
-    _on_device(X, expert_offsets, Wg, scale_g, zero_g, Wu, scale_u, zero_u, H)
-    _check(lib().moe_q4_swiglu(_ptr(X), _ptr(expert_offsets), _ptr(Wg), _ptr(scale_g), _ptr(zero_g), _ptr(Wu),
-                               _ptr(scale_u), _ptr(zero_u), _ptr(H), rows, E, K, C, _q4_code(code), group,
-                               _stream(stream)))
+    bf = torch.bfloat16
+    group, packed, z = _q4_pair(Wg, scale_g, zero_g, Wu, scale_u, zero_u, (E,), K, C)
+    dev = _tensors(((X, "X", (rows, K), bf), (H, "H", (rows, C), bf),
+                    (expert_offsets, "expert_offsets", (E + 1,), torch.int32), *packed), z)
+    _check(lib().moe_q4_swiglu(X.data_ptr(), expert_offsets.data_ptr(), Wg.data_ptr(), scale_g.data_ptr(),
+                               _ptr(zero_g), Wu.data_ptr(), scale_u.data_ptr(), _ptr(zero_u), H.data_ptr(), rows, E,
+                               K, C, _q4_code(code), group, _stream_of(stream, dev)))
     return H
 
 

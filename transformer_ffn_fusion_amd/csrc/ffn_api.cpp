@@ -830,7 +830,7 @@ static int rmsnorm_forward(const void* X, const void* R, const void* gamma, void
     const Span out[] = {{S, eb * M * N, "S"}, {Y, (q8 ? 1 : eb) * M * N, q8 ? "Q" : "Y"}, {rstd, 4 * M, "rstd"},
                        {scale, q8 ? 4 * M * scales : 0, "scale"}};
     const uint32_t none = M == 0 ? 15u : 0u;   // an empty tensor's pointer
-    if ((rc = check_arrays(in, 3, none | 2u))) return rc;
+    if ((rc = check_arrays(in, 3, M == 0 ? 3u : 2u))) return rc;
     if ((rc = check_arrays(out, 4, none | 1u | 4u | (q8 ? 0u : 8u)))) return rc;
     // a lane reads its columns of a row before it writes them
     const uint32_t same[] = {3u, q8 || R ? 0u : 1u, 0u, 0u};
