@@ -275,7 +275,7 @@ int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, con
  * The norm in front of the FFN without a mean, with the residual's addition in
  * front of it, and its gradients:
  *
- *   s = x + r, rounded once to the data's type (s = x where R is NULL)
+ *   s = x + r, added in fp32 and rounded to the data's type (s = x where R is NULL)
  *   rstd = 1 / sqrt(sum_j s_j^2 / N + eps),  y_j = s_j rstd gamma_j
  *
  *   z = s rstd, t = dy gamma

@@ -222,3 +222,41 @@ def test_workspace_contents_do_not_matter():
     ws = ffn.workspace(ffn.moe_dispatch_workspace_size(M, E, k))
     ws.fill_(0xFF)
     check_dispatch(dispatch(X, ids, E, ws=ws), X, ids, E)
+
+
+def test_rows_past_32_bit_offsets_and_more_tokens_than_a_launch():
+    """9 x 10^9 values a side: 64-bit offsets, and the tokens in two slices of launches.  Checked at both
+    ends, around the slices' border and where 2^31 and 2^32 values or bytes end."""
+    import torch
+    M, N = (1 << 22) + 77, 2048
+    print(f"case dispatch and combine of {M} x {N}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, M, 1 << 19):       # (a generator's call on all of it at once would need twice the memory)
+        part = X[lo:lo + (1 << 19)]
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda", dtype=torch.bfloat16))
+    ids = torch.randint(-1, 3, (M, 1), generator=g, device="cuda", dtype=torch.int32)
+    Xs = torch.zeros_like(X)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    off, entries, pos = torch.empty(4, **i32), torch.empty(M, **i32), torch.empty(M, 1, **i32)
+    ffn.moe_dispatch(X, ids, Xs, off, entries, pos)
+    w = torch.rand(M, 1, generator=g, device="cuda")
+    at = torch.cat([torch.arange(b - 200, b + 200) for b in (200, 1 << 19, 1 << 20, 1 << 21, 1 << 22)] +
+                   [torch.arange(M - 300, M)]).unique()
+    at = at[at < M].cuda()
+    kept = pos[at, 0] >= 0
+    assert torch.equal(kept, ids[at, 0] >= 0)
+    p = pos[at, 0].clamp(min=0).long()
+    assert torch.equal(Xs[p][kept], X[at][kept])
+    n = int(off[-1])
+    assert n == int((ids >= 0).sum()) and not bool(Xs[n:].any())
+    Y = torch.empty_like(X)
+    ffn.moe_combine(Xs, pos, Y, topk_w=w, R=X)
+    ref.check({"Y": Y[at]}, ref.combine(Xs[p], torch.where(kept, torch.arange(len(at), device="cuda"), -1)[:, None], w[at], X[at]),
+              "combine")
+    dw = torch.full_like(w, float("nan"))
+    ffn.moe_combine_backward(X, Xs, pos, w, Xs, dw)        # in place
+    want = (X[at].float() * w[at]).to(torch.bfloat16)
+    assert torch.equal(Xs[p][kept], want[kept])
+    ref.check({"dw": dw[at]}, ref.combine_backward(X[at], X[at], torch.where(kept, torch.arange(len(at), device="cuda"), -1)[:, None],
+                                                   w[at])[0], "combine's gradients")

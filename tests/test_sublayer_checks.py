@@ -165,6 +165,8 @@ def test_binding_refuses_unknown_names():
         a = CALLS[call]()
         with pytest.raises(ValueError):
             call(**a, code="int3")
+    with pytest.raises(ValueError, match="group"):
+        ffn.ffn_q4_empty(264, 40, 48, device="cpu")
     assert [tuple(t.shape) for t in ffn.ffn_q4_empty(264, 40, 32, True, device="cpu")] == \
         [(3, 3, 1024), (3, 3, 16, 4), (3, 3, 16, 4)]
     assert ffn.ffn_q4_empty(264, 40, experts=5, device="cpu")[0].shape == (5, 3, 3, 1024)

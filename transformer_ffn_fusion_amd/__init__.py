@@ -532,7 +532,7 @@ def ffn_rmsnorm_forward(X, gamma, Y, R=None, S=None, rstd=None, eps=1e-5, stream
     (M x N, bf16 or fp32); ``S``, ``Y`` and, when given, ``rstd`` (M, fp32) are written in place."""
     M, N, dt, dev = _rmsnorm_args(X, gamma, R, S, rstd, (Y, "Y", X.shape, X.dtype))
     _check(lib().ffn_rmsnorm_forward(X.data_ptr(), _ptr(R), gamma.data_ptr(), _ptr(S), Y.data_ptr(), _ptr(rstd), M, N,
-                                     dt, eps, _stream_of(stream, dev)))
+                                     dt, float(eps), _stream_of(stream, dev)))
     return Y
 
 
@@ -546,7 +546,8 @@ def ffn_rmsnorm_q8_forward(X, gamma, Q, scale, R=None, S=None, rstd=None, group=
     M, N, dt, dev = _rmsnorm_args(X, gamma, R, S, rstd, (Q, "Q", X.shape, torch.float8_e4m3fn),
                                   (scale, "scale", (M, -(-N // group) if group else 1), torch.float32))
     _check(lib().ffn_rmsnorm_q8_forward(X.data_ptr(), _ptr(R), gamma.data_ptr(), _ptr(S), Q.data_ptr(),
-                                        scale.data_ptr(), _ptr(rstd), M, N, dt, group, eps, _stream_of(stream, dev)))
+                                        scale.data_ptr(), _ptr(rstd), M, N, dt, group, float(eps),
+                                        _stream_of(stream, dev)))
     return Q
 
 
@@ -813,6 +814,8 @@ def ffn_q4_bytes(K, C) -> int:
 def ffn_q4_empty(K, C, group=128, zero=False, experts=None, device="cuda"):
     """Buffers ``(Wq, scale, zero or None)`` of the packed layout of a K x C matrix, or of ``experts`` of them."""
     import torch
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128 (got {group})")
     lead = () if experts is None else (experts,)
     ct, kt = -(-C // 16), -(-K // 128)
     scale = torch.zeros(*lead, ct, kt, 16, 128 // group, dtype=torch.bfloat16, device=device)

@@ -311,7 +311,8 @@ struct CombineArgs {
     const float* w;
     const void* res;
     void* Y;
-    int64_t M, R;
+    int64_t M;
+    unsigned R;      // below 2^31
     int N;
 };
 
@@ -328,7 +329,7 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineArgs a, i
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         const int p = a.pos[t * K + s];
-        at[s] = (unsigned)p < (uint64_t)a.R && p >= 0 ? (int64_t)p * a.N : -1;
+        at[s] = (unsigned)p < a.R ? (int64_t)p * a.N : -1;   // (a negative one is past 2^31)
         w[s] = a.w ? a.w[t * K + s] : 1.f;
     }
     for (int c = c0; c < a.N; c += 8 * tpr) {
@@ -360,7 +361,8 @@ struct CombineBackwardArgs {
     const float* w;
     void* drows;
     float* dw;
-    int64_t M, R;
+    int64_t M;
+    unsigned R;      // below 2^31
     int N, W, G;     // W waves per token, G tokens per workgroup
 };
 
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         const int p = on ? a.pos[t * K + s] : -1;
-        at[s] = (unsigned)p < (uint64_t)a.R && p >= 0 ? (int64_t)p * a.N : -1;
+        at[s] = (unsigned)p < a.R ? (int64_t)p * a.N : -1;   // (a negative one is past 2^31)
         wt[s] = on && a.w ? a.w[t * K + s] : 1.f;
         dot[s] = 0.f;
     }
@@ -442,20 +444,33 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t*
     }
 }
 
+// A launch holds fewer than 2^32 threads: M tokens, `per` to a workgroup, in slices of at most
+// 2^22 workgroups.  go(t0, tokens, grid) launches one.
+template <typename F>
+hipError_t in_slices(int64_t M, int64_t per, F&& go) {
+    const int64_t most = per << 22;
+    for (int64_t t0 = 0; t0 < M; t0 += most) {
+        const int64_t n = M - t0 < most ? M - t0 : most;
+        go(t0, n, dim3((unsigned)((n + per - 1) / per)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <typename F>
 hipError_t with_k(int k, F&& f) {
     switch (k) {
-        case 1: f(std::integral_constant<int, 1>()); break;
-        case 2: f(std::integral_constant<int, 2>()); break;
-        case 3: f(std::integral_constant<int, 3>()); break;
-        case 4: f(std::integral_constant<int, 4>()); break;
-        case 5: f(std::integral_constant<int, 5>()); break;
-        case 6: f(std::integral_constant<int, 6>()); break;
-        case 7: f(std::integral_constant<int, 7>()); break;
-        case 8: f(std::integral_constant<int, 8>()); break;
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 3: return f(std::integral_constant<int, 3>());
+        case 4: return f(std::integral_constant<int, 4>());
+        case 5: return f(std::integral_constant<int, 5>());
+        case 6: return f(std::integral_constant<int, 6>());
+        case 7: return f(std::integral_constant<int, 7>());
+        case 8: return f(std::integral_constant<int, 8>());
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
 }  // namespace
@@ -505,55 +520,64 @@ hipError_t launch_moe_dispatch(const DispatchIO& io, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int l = threads_per_row_log(a.chunks, 8);
-    const dim3 grid((unsigned)((io.M + (kThreads >> l) - 1) / (kThreads >> l)));
-    if (wide) hipLaunchKernelGGL(dispatch_rows_kernel<uint4>, grid, dim3(kThreads), 0, stream, a, l);
-    else hipLaunchKernelGGL(dispatch_rows_kernel<uint2>, grid, dim3(kThreads), 0, stream, a, l);
-    return hipGetLastError();
+    return in_slices(io.M, kThreads >> l, [&](int64_t t0, int64_t n, dim3 grid) {
+        DispatchArgs s = a;
+        s.X += t0 * a.row_bytes;
+        s.positions += t0 * a.k;
+        if (a.scale) s.scale += t0 * a.scale_cols;
+        s.M = n;
+        if (wide) hipLaunchKernelGGL(dispatch_rows_kernel<uint4>, grid, dim3(kThreads), 0, stream, s, l);
+        else hipLaunchKernelGGL(dispatch_rows_kernel<uint2>, grid, dim3(kThreads), 0, stream, s, l);
+    });
 }
 
 hipError_t launch_moe_combine_rows(const void* rows, int64_t R, const int32_t* pos, const float* w,
                                    const void* res, void* Y, int64_t M, int64_t N, int k, bool f32,
                                    hipStream_t stream) {
-    CombineArgs a;
-    a.rows = rows;
-    a.pos = pos;
-    a.w = w;
-    a.res = res;
-    a.Y = Y;
-    a.M = M;
-    a.R = R;
-    a.N = (int)N;
     const int l = threads_per_row_log(N / 8, 8);
-    const dim3 grid((unsigned)((M + (kThreads >> l) - 1) / (kThreads >> l)));
+    const int64_t row = N * (f32 ? 4 : 2);
     return with_k(k, [&](auto K) {
-        if (f32)
-            hipLaunchKernelGGL((combine_rows_kernel<true, K.value>), grid, dim3(kThreads), 0, stream, a, l);
-        else
-            hipLaunchKernelGGL((combine_rows_kernel<false, K.value>), grid, dim3(kThreads), 0, stream, a, l);
+        return in_slices(M, kThreads >> l, [&](int64_t t0, int64_t n, dim3 grid) {
+            CombineArgs a;
+            a.rows = rows;
+            a.pos = pos + t0 * k;
+            a.w = w ? w + t0 * k : nullptr;
+            a.res = res ? static_cast<const char*>(res) + t0 * row : nullptr;
+            a.Y = static_cast<char*>(Y) + t0 * row;
+            a.M = n;
+            a.R = (unsigned)R;
+            a.N = (int)N;
+            if (f32)
+                hipLaunchKernelGGL((combine_rows_kernel<true, K.value>), grid, dim3(kThreads), 0, stream, a, l);
+            else
+                hipLaunchKernelGGL((combine_rows_kernel<false, K.value>), grid, dim3(kThreads), 0, stream, a, l);
+        });
     });
 }
 
 hipError_t launch_moe_combine_backward(const void* dY, const void* rows, int64_t R, const int32_t* pos,
                                        const float* w, void* drows, float* dw, int64_t M, int64_t N,
                                        int k, bool f32, hipStream_t stream) {
-    CombineBackwardArgs a;
-    a.dY = dY;
-    a.rows = rows;
-    a.pos = pos;
-    a.w = w;
-    a.drows = drows;
-    a.dw = dw;
-    a.M = M;
-    a.R = R;
-    a.N = (int)N;
-    a.W = N > 2 * kLnCols ? 4 : N > kLnCols ? 2 : 1;
-    a.G = kThreads / 64 / a.W;
-    const dim3 grid((unsigned)((M + a.G - 1) / a.G));
+    const int W = N > 2 * kLnCols ? 4 : N > kLnCols ? 2 : 1, G = kThreads / 64 / W;
     return with_k(k, [&](auto K) {
-        if (f32)
-            hipLaunchKernelGGL((combine_backward_kernel<true, K.value>), grid, dim3(kThreads), 0, stream, a);
-        else
-            hipLaunchKernelGGL((combine_backward_kernel<false, K.value>), grid, dim3(kThreads), 0, stream, a);
+        return in_slices(M, G, [&](int64_t t0, int64_t n, dim3 grid) {
+            CombineBackwardArgs a;
+            a.dY = static_cast<const char*>(dY) + t0 * N * (f32 ? 4 : 2);
+            a.rows = rows;
+            a.pos = pos + t0 * k;
+            a.w = w ? w + t0 * k : nullptr;
+            a.drows = drows;
+            a.dw = dw ? dw + t0 * k : nullptr;
+            a.M = n;
+            a.R = (unsigned)R;
+            a.N = (int)N;
+            a.W = W;
+            a.G = G;
+            if (f32)
+                hipLaunchKernelGGL((combine_backward_kernel<true, K.value>), grid, dim3(kThreads), 0, stream, a);
+            else
+                hipLaunchKernelGGL((combine_backward_kernel<false, K.value>), grid, dim3(kThreads), 0, stream, a);
+        });
     });
 }
 

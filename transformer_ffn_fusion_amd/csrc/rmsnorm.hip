@@ -2,7 +2,7 @@
 // residual's addition in front, its gradients, and its output in 8 bits with
 // scales; bf16 or fp32 data, fp32 statistics and sums.
 //
-//   forward:   s = x + r (rounded once to the data's type; x alone without r)
+//   forward:   s = x + r (in fp32, rounded to the data's type; x alone without r)
 //              rstd = 1 / sqrt(sum_j s_j^2 / N + eps),  y_j = s_j rstd gamma_j
 //   8 bits:    per row and group of 128 columns (or the whole row), from the
 //              unrounded y: scale = max(max |y|, 2^-100) / 448, q_j = e4m3(y_j / scale)
