@@ -271,18 +271,19 @@ def _tensors(need, may=()):
     microseconds; ``may``: those that may be None.  Returns the device's index."""
     import torch
     dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
-    elsewhere = dev < 0
-    for spec in (need, may) if may else (need,):
-        for t, name, shape, dtype in spec:
-            if t is None:
-                if spec is need:
-                    raise ValueError(f"{name} must not be None")
-                continue
-            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
-                _arg(t, name, shape, dtype)
-            if t.get_device() != dev:
-                elsewhere = True
-    if elsewhere:
+    good = dev >= 0
+    for t, name, shape, dtype in need:
+        if t is None or t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+            good = False
+    for t, name, shape, dtype in may:
+        if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                              or t.get_device() != dev):
+            good = False
+    if not good:      # which one, and why
+        for spec in need:
+            _arg(*spec)
+        for spec in may:
+            _arg(*spec, optional=True)
         _on_device(*(s[0] for s in (*need, *may)))
     return dev
 
