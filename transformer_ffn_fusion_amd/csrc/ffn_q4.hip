@@ -74,9 +74,9 @@ __device__ __forceinline__ void lanes_meet() {
 }
 
 // kZero: integers with zero points; kPer groups per tile; kTiles column tiles per wave
-// (of each matrix; a pair's two take 128 registers a lane, two plain ones more).
+// (of each matrix).
 template <int kCode, bool kZero, int kPer, bool kGated, int kTiles>
-__global__ __launch_bounds__(64 * kMaxWaves, kTiles == 1 ? 4 : 2) void q4_kernel(Q4Args a) {
+__global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
     constexpr int kMats = kGated ? 2 : 1, kNT = kTiles * kMats;
     constexpr int kSteps = 4 / kPer;              // matrix instructions per group
     static_assert(1024 * kNT <= kWaveLds, "a wave's sums take the place of its rows");
@@ -95,11 +95,11 @@ __global__ __launch_bounds__(64 * kMaxWaves, kTiles == 1 ? 4 : 2) void q4_kernel
         hi = q < lo ? lo : q > a.rows ? a.rows : q;
     }
     if (lo >= hi) return;
-    // Loads go through buffer resources made for their tile by scalar instructions, with
-    // per-lane offsets that never change.  One of a tile past the last is empty: its loads
-    // read zeros and move nothing, so the loop's loads need no branch (behind one, the wait
-    // for a stage would be a wait for every load).
-    const char *wp[kNT], *sp[kNT], *zp[kNT];   // codes, scales, zero points of the column tiles
+    // Loads go through one buffer resource per column tile, with per-lane offsets that never
+    // change and the k tile in the scalar offset.  For a tile past the last the per-lane offset
+    // is past the resource: the load reads zeros and moves nothing, so the loop's loads need no
+    // branch (behind one, the wait for a stage would be a wait for every load).
+    __amdgpu_buffer_rsrc_t rw[kNT], rs[kNT], rz[kNT];   // codes, scales, zero points
 #pragma unroll
     for (int m = 0; m < kMats; ++m)
 #pragma unroll
@@ -107,21 +107,19 @@ __global__ __launch_bounds__(64 * kMaxWaves, kTiles == 1 ? 4 : 2) void q4_kernel
             // (a tile past the last column repeats it and is not stored)
             const int64_t ct = ct0 + t < tiles ? ct0 + t : tiles - 1;
             const int i = m * kTiles + t;
-            wp[i] = a.W[m] + e * a.w_stride + ct * a.kt * 1024;
-            sp[i] = a.S[m] + e * a.s_stride + ct * a.kt * (32 * kPer);
-            if constexpr (kZero) zp[i] = a.Z[m] + e * a.s_stride + ct * a.kt * (32 * kPer);
+            const int64_t groups = e * a.s_stride + ct * a.kt * (32 * kPer);
+            rw[i] = make_rsrc(a.W[m] + e * a.w_stride + ct * a.kt * 1024, (int64_t)a.kt * 1024);
+            rs[i] = make_rsrc(a.S[m] + groups, (int64_t)a.kt * (32 * kPer));
+            if constexpr (kZero) rz[i] = make_rsrc(a.Z[m] + groups, (int64_t)a.kt * (32 * kPer));
         }
-    auto part = [&](const char* p, int kt, int bytes) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p) + (int64_t)kt * bytes, (short)0,
-                                                 kt < a.kt ? bytes : 0, kRsrcWord3);
+    auto load16 = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, int at) {
+        return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, at, 0));
     };
-    auto groups = [&](const char* p, int kt, uint32_t (&v)[(kPer + 1) / 2]) {
-        const __amdgpu_buffer_rsrc_t r = part(p, kt, 32 * kPer);
-        const uint32_t off = (uint32_t)(c * 2 * kPer);
-        if constexpr (kPer == 1) v[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
-        else if constexpr (kPer == 2) v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    auto groups = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, int at, uint32_t (&v)[(kPer + 1) / 2]) {
+        if constexpr (kPer == 1) v[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, at, 0);
+        else if constexpr (kPer == 2) v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, at, 0);
         else {
-            const uint2 u = bload8(r, off);
+            const uint2 u = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, off, at, 0));
             v[0] = u.x;
             v[1] = u.y;
         }
@@ -143,26 +141,25 @@ __global__ __launch_bounds__(64 * kMaxWaves, kTiles == 1 ? 4 : 2) void q4_kernel
         // A load takes 256 B of each of four rows, 16 lanes in order: the operand's own order (64 B
         // of 16 rows, neighbours in lanes 16 apart) is 64 accesses instead of eight lines.  Rows
         // past the last one and, in the last tile, k past K read zeros.
-        uint32_t xin[kXLoads], xlast[kXLoads];
+        const uint32_t xin = (uint32_t)((lane >> 4) * a.K * 2 + 16 * c);
+        const uint32_t xtail = (a.kt - 1) * kQ4TileK + 8 * c < a.K ? 0u : kOOB;
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X + (int64_t)r0 * a.K, have * a.K * 2);
+        auto load = [&](Stage& st, int tile) {
+            // Past the resource by one bit of the offset, not by a choice of offsets: the compiler
+            // makes a branch of that.  The scalar offset stays inside in any case.
+            const uint32_t out = tile < a.kt ? 0u : kOOB;
+            const int kt = tile < a.kt ? tile : a.kt - 1;
 #pragma unroll
-        for (int j = 0; j < kXLoads; ++j) {
-            xin[j] = (uint32_t)((4 * j + (lane >> 4)) * a.K * 2 + 16 * c);
-            xlast[j] = (a.kt - 1) * kQ4TileK + 8 * c < a.K ? xin[j] : kOOB;
-        }
-        const int xbytes = (int)(have * a.K * 2);
-        auto load = [&](Stage& st, int kt) {
+            for (int i = 0; i < kNT; ++i) st.w[i] = load16(rw[i], (uint32_t)(lane * 16) | out, kt * 1024);
+            const uint32_t xout = (xtail & (kt == a.kt - 1 ? ~0u : 0u)) | out;
 #pragma unroll
-            for (int i = 0; i < kNT; ++i) st.w[i] = bload16(part(wp[i], kt, 1024), (uint32_t)(lane * 16));
-            const int past = kt * kQ4TileK * 2;
-            const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<uint16_t*>(a.X) + (int64_t)r0 * a.K + (int64_t)kt * kQ4TileK, (short)0,
-                kt < a.kt ? xbytes - past : 0, kRsrcWord3);
-#pragma unroll
-            for (int j = 0; j < kXLoads; ++j) st.x[j] = bload16(rx, kt < a.kt - 1 ? xin[j] : xlast[j]);
+            for (int j = 0; j < kXLoads; ++j)
+                st.x[j] = load16(rx, (xin + (uint32_t)(4 * j * a.K * 2)) | xout, kt * (kQ4TileK * 2));
+            const uint32_t off = (uint32_t)(c * 2 * kPer) | out;
 #pragma unroll
             for (int i = 0; i < kNT; ++i) {
-                groups(sp[i], kt, st.s[i]);
-                if constexpr (kZero) groups(zp[i], kt, st.z[i]);
+                groups(rs[i], off, kt * (32 * kPer), st.s[i]);
+                if constexpr (kZero) groups(rz[i], off, kt * (32 * kPer), st.z[i]);
             }
         };
         // The operands of a tile's four steps, through the wave's own LDS (a wave's LDS accesses

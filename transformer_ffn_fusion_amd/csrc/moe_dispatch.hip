@@ -88,13 +88,20 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
         for (int u = 0; u < kEach; ++u)
             if (id[u] < E) atomicAdd(&s_hist[id[u]], 1);   // a count: the order does not matter
         __syncthreads();
-        int off = 0, all = 0;
-        for (int e = 0; e < E; ++e) {
-            if (e < tid) off += s_hist[e];
-            all += s_hist[e];
+        // exclusive prefix over the experts, one a thread: within the waves, then between them
+        const int mine_e = tid < E ? s_hist[tid] : 0;
+        int run = mine_e;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(run, d);
+            if (lane >= d) run += v;
         }
-        if (tid < E) a.offsets[tid] = off;
-        if (tid == 0) a.offsets[E] = all;
+        __syncthreads();            // (read before it is written again)
+        if (lane == 63) s_hist[wave] = run;
+        __syncthreads();
+        for (int q = 0; q < wave; ++q) run += s_hist[q];
+        if (tid < E) a.offsets[tid] = run - mine_e;
+        if (tid == E - 1) a.offsets[E] = run;
     }
 #pragma unroll
     for (int s = 0; s < kMaxK; ++s) {
