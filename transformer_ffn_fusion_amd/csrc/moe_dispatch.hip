@@ -12,7 +12,12 @@
 //
 // Bound: HBM bytes for many tokens (each row is read once and written where it goes,
 // whole 16-byte pieces), launches for few.  Positions come from counts, not from
-// atomics on lists, so they never depend on the order of arrival.
+// atomics on lists, so they never depend on the order of arrival.  Measured: combine's
+// gradient of 16384 x 4096 bf16, top 2, 125 us (671 MB, 5.4 TB/s); dispatch of 16384 rows of
+// 2048 e4m3 codes to 86000 places 54 us, of which 44 move rows (216 MB, most of them written:
+// 4.9 TB/s) and 10 are the two launches of the sort.  (Non-temporal stores of the rows: 44 us
+// in all, but what reads the rows next then takes longer than that saves: 98 -> 105 us for
+// norm, dispatch, a pass over the rows and combine of 4096 x 2048, top 6.)
 #include <type_traits>
 
 #include "ffn_device.h"

@@ -14,6 +14,11 @@
 // and its one write, eight consecutive columns per lane and step; workgroups walk
 // many rows with the next rows' loads in flight.  A group of 128 columns is one
 // 16-lane row of a wave, so its largest magnitude needs neither LDS nor a barrier.
+// Measured, bf16 with a residual: 8192 x 8192 forward 98 us, backward 105 us (537 MB each,
+// 5.1 to 5.5 TB/s, the rate of a large copy); 4096 x 4096 into 8 bits 25 us (117 MB).
+// Stores that pass the caches by (non-temporal) make a single call faster (8 bits 20 us,
+// forward of 4096 x 4096 27 -> 22 us) and the call that reads the rows slower by more: a
+// chain of norm, dispatch and combine of 16384 x 4096 takes 374 us with them, 362 without.
 #include <type_traits>
 
 #include "ffn_device.h"
