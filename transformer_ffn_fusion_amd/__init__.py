@@ -270,8 +270,8 @@ def _tensors(need, may=()):
     """Checks (tensor, name, shape, dtype) as ``_arg`` and ``_on_device`` do, in one pass for calls of a few
     microseconds; ``may``: those that may be None.  Returns the device's index."""
     import torch
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
-    good = dev >= 0
+    good = torch.cuda.is_initialized()
+    dev = torch._C._cuda_getDevice() if good else -1
     for t, name, shape, dtype in need:
         if t is None or t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
             good = False

@@ -331,12 +331,16 @@ __global__ __launch_bounds__(1024) void rms_finish_kernel(const float* __restric
     dgamma[col] = t;
 }
 
-// Few rows: no more of them at once than keep one turn over all workgroups (16 x 4096 bf16
-// one row each 5.1 us, two 6.4).
+// Rows at once.  Two turns and more, so that loads run behind sums: half of a workgroup's
+// rows at most (1000 x 256 bf16 7.3 us with four at once, one turn, 6.0 with two).  Eight waves:
+// a barrier holds up fewer of them and the columns' sums are joined from fewer rows (2000 x 4096
+// bf16: one row 16.3 us, two 18.9; 8000 x 1024: four 16.7, eight 18.2); sixteen rows where a wave
+// holds one (8000 x 256: 8.7 us, four 10.5).
 LnShape rms_backward_shape(int64_t M, int64_t N) {
     LnShape s = ln_shape(N, kRmsThreads);
-    const int64_t each = (M + kLnBackwardBlocks - 1) / kLnBackwardBlocks;
-    if (each < s.G) s.G = each > 0 ? (int)each : 1;
+    if (s.W > 1) s.G = s.W < 8 ? 8 / s.W : 1;
+    const int64_t half = (M + kLnBackwardBlocks - 1) / kLnBackwardBlocks / 2;
+    if (half < s.G) s.G = half > 0 ? (int)half : 1;
     return s;
 }
 
