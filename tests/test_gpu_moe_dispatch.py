@@ -73,6 +73,26 @@ def test_dispatch(case, dtype):
     check_dispatch(dispatch(X, ids, E, scale), X, ids, E, scale)
 
 
+@pytest.mark.parametrize("M,E,k", [(600000, 256, 8), (1000001, 5, 1), (300001, 9, 7)])
+def test_dispatch_of_many_turns(M, E, k):
+    """More than 262144 entries: a workgroup ranks its tokens in several turns, whose counts lie in the
+    same place.  Against a stable sort."""
+    import torch
+    print(f"case many turns {M} {E} {k}", flush=True)
+    ids = torch.randint(-1, E + 1, (M, k), generator=torch.Generator().manual_seed(M), dtype=torch.int32).cuda()
+    X = torch.arange(M, device="cuda").float()[:, None].repeat(1, 8)
+    key, order = torch.sort(torch.where((ids < 0) | (ids >= E), E, ids).reshape(-1), stable=True)
+    n = int((key < E).sum())
+    pos = torch.full((M * k,), -1, dtype=torch.int32, device="cuda")
+    pos[order[:n]] = torch.arange(n, dtype=torch.int32, device="cuda")
+    off = torch.searchsorted(key, torch.arange(E + 1, dtype=torch.int32, device="cuda"))
+    for _ in range(3):
+        o = dispatch(X, ids, E)
+        assert torch.equal(o["off"].long(), off) and torch.equal(o["pos"].reshape(-1), pos)
+        assert torch.equal(o["entries"][:n].long(), order[:n]) and bool((o["entries"][n:] == -9).all())
+        assert torch.equal(o["Xs"][:n], X[order[:n] // k]) and bool((o["Xs"][n:] == 7.0).all())
+
+
 @pytest.mark.parametrize("M", [100, 3000])
 def test_dispatch_of_unusual_ids(M):
     """All dropped, all to one expert, the same expert twice in a token, ids far outside."""

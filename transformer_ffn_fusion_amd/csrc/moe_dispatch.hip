@@ -252,7 +252,8 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_sort_kernel(DispatchArg
         const bool have = tid < tokens * k;
         const int e = have ? a.ids[i] : -1;
         const bool kept = (unsigned)e < (unsigned)E;
-        for (int q = tid; q < kWaves * kMaxExperts; q += kSortThreads) (&s_w[0][0])[q] = 0;
+        // (a wave clears its own counts: slower waves still read theirs of the last turn)
+        for (int q = lane; q < kMaxExperts; q += 64) s_w[wave][q] = 0;
         uint64_t peers = __ballot(kept);
         for (int b = 0; b < bits; ++b) {
             const bool one = (e >> b) & 1;
