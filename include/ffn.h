@@ -427,7 +427,8 @@ int moe_ffn_forward_router(const void* X, const void* Wr, const float* br, int64
  * Combine's gradients: dYs[positions[t][s]] = topk_w[t][s] dY[t] (topk_w NULL: dY[t]),
  * dw[t][s] = <Ys[positions[t][s]], dY[t]> in fp32 (0 for dropped entries; dw and Ys may
  * both be NULL).  Rows of dYs that no position names are left as they were; positions
- * that name one row twice leave either's value there.
+ * that name one row twice leave either's value there (and with dYs in Ys' place their dw
+ * may be taken from it).
  *
  * Routing's gradient: with w the softmax over a token's k chosen logits,
  * dlogits[t][topk_ids[t][s]] = w_s (dw_s - sum_j w_j dw_j), all else 0.  Takes the ids that

@@ -185,6 +185,23 @@ def test_quantize(shape, kind, dtype):
         assert torch.equal(q.float(), want_q)
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_quantize_of_the_largest_values(dtype):
+    """A group from -2^127 to 2^127 is finite, though its range is not: the scale is 2^128 / 15."""
+    import torch
+    K, C = 136, 24
+    W = (torch.rand(K, C, generator=torch.Generator().manual_seed(1)) - 0.5).mul(2.0 ** 126).to(getattr(torch, dtype))
+    W[0], W[1] = 2.0 ** 127, -2.0 ** 127
+    Wq, s, z = ffn.ffn_q4_empty(K, C, 128, True)
+    ffn.ffn_q4_quantize(W.cuda(), Wq, s, zero=z)
+    want = torch.tensor(2.0 ** 128 / 15, dtype=torch.float64).to(torch.bfloat16).double()
+    assert torch.equal(ref.q4_groups(s, K, C)[:128], want.expand(128, C))
+    zero = torch.round(2.0 ** 127 / want.float()).double()
+    assert torch.equal(ref.q4_groups(z, K, C)[:128], zero.expand(128, C))
+    back = ref.q4_weights(Wq, s, z, K, C, "int4")[0][:128]
+    assert bool(((back - W[:128].double()).abs() <= want).all())
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("shape", [(8, 8), (136, 24), (520, 200)])
 def test_pack(shape, kind):

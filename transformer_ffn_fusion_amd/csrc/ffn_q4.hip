@@ -316,7 +316,8 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const void* W, uint8_t
             hi = fmaxf(hi, s_w[p * len + k][col]);
         }
         const float top = fmaxf(-lo, hi);
-        float s = code == kQ4E2m1 ? top / 6.f : zero ? (hi - lo) / 15.f : top / 7.f;
+        // (half the range: hi - lo may leave fp32 where hi and lo do not)
+        float s = code == kQ4E2m1 ? top / 6.f : zero ? (0.5f * hi - 0.5f * lo) / 7.5f : top / 7.f;
         if (top < 0x1p-100f) s = 0.f;         // nothing to keep
         s = (float)(__bf16)s;                 // codes are taken under the scale as it is kept
         float z = 8.f;
