@@ -310,24 +310,25 @@ __global__ __launch_bounds__(kRmsThreads) void rms_backward_kernel(
     }
 }
 
-// dgamma from the workgroups' partial rows, in a fixed order: 16 threads per column add
-// every 16th partial, then one adds the 16 sums.
+// dgamma from the workgroups' partial rows, in a fixed order: 32 threads per column add
+// every 32nd partial, eight loads at most, then one adds the 32 sums (call of 1000 x 256 bf16
+// 5.7 us; with 16 threads per column 6.05, with 64 and half the line of a load 5.95).
 __global__ __launch_bounds__(1024) void rms_finish_kernel(const float* __restrict__ part, int rows,
                                                           int N, float* __restrict__ dgamma) {
-    __shared__ float s[16][64 + 1];
-    const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
-    const int col = blockIdx.x * 64 + c;
+    __shared__ float s[32][32 + 1];
+    const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + c;
     float v = 0.f;
     if (col < N) {
 #pragma unroll 8
-        for (int r = k; r < rows; r += 16) v += part[(int64_t)r * N + col];
+        for (int r = k; r < rows; r += 32) v += part[(int64_t)r * N + col];
     }
     s[k][c] = v;
     __syncthreads();
     if (k || col >= N) return;
     float t = 0.f;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) t += s[q][c];
+    for (int q = 0; q < 32; ++q) t += s[q][c];
     dgamma[col] = t;
 }
 
@@ -426,7 +427,7 @@ hipError_t launch_rmsnorm_backward(const void* S, const void* dY, const void* dS
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(rms_finish_kernel, dim3((unsigned)((N + 63) / 64)), dim3(1024), 0, stream, part,
+    hipLaunchKernelGGL(rms_finish_kernel, dim3((unsigned)((N + 31) / 32)), dim3(1024), 0, stream, part,
                        (int)blocks, (int)N, dgamma);
     return hipGetLastError();
 }
