@@ -11,7 +11,7 @@ import sublayer_ref as ref
 pytestmark = pytest.mark.gpu
 SHAPES = [(1, 8), (1, 4096), (3, 72), (5, 512), (7, 520), (13, 1032), (33, 2056), (6, 4104), (5, 8192), (3, 8200),
           (2, 16384), (3, 12296), (700, 9000), (1030, 136), (1100, 8192), (1025, 4104), (1030, 12296), (2053, 24),
-          (4100, 264), (300, 16376)]
+          (4100, 264), (300, 16376), (1040, 8200), (1030, 16384), (1100, 2056), (1030, 6008)]
 
 
 def make(M, N, dtype, seed=0):

@@ -71,7 +71,7 @@ struct RmsArgs {
 // by the grid.  Waves past the last whole row group (W does not divide the workgroup)
 // do not exist: the workgroup has W G waves.
 template <bool kF32, bool kQ8, int V, int kThreads>
-__global__ __launch_bounds__(kThreads) void rms_forward_kernel(RmsArgs a) {
+__global__ __launch_bounds__(kThreads, V == 4 && kThreads == 512 ? 4 : 1) void rms_forward_kernel(RmsArgs a) {
     __shared__ float s_part[2][2][kThreads / 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int W = a.W, N = a.N;
@@ -351,12 +351,26 @@ int64_t rms_backward_blocks(int64_t M, int64_t N) {
     return need < kLnBackwardBlocks ? need : kLnBackwardBlocks;
 }
 
+// Largest workgroup of the forward.  Few rows: up to sixteen waves a row, one step a lane as far
+// as they reach: one round trip.  Many rows of fp32 likewise (8192 columns: 96 us, with four waves
+// of four steps 100; 5824: 98, 105); of bf16 in four waves, several workgroups per CU (8192
+// columns into 8 bits: 42 us, with sixteen waves 50).  Past 8192 columns two steps a lane, while
+// two workgroups of them fit a CU (12288 bf16 into 8 bits: 45 us, with eight waves of four steps 69);
+// past 12288 one would be alone, and bf16 takes four steps in eight waves, within 128 registers
+// (16384 bf16: 50 us, with sixteen waves 54; into 8 bits 53, 56).
+constexpr int64_t kManyRows = 1024;
+int forward_threads(int64_t M, int64_t N, bool f32) {
+    if (M < kManyRows) return kRmsThreads;
+    if (f32) return N <= 4 * kLnCols ? 256 : N <= 8 * kLnCols ? 512 : kRmsThreads;
+    return N <= 16 * kLnCols ? 256 : N <= 24 * kLnCols ? kRmsThreads : 512;
+}
+
 template <bool kF32, bool kQ8, int kThreads>
 void start_forward(const LnShape& s, dim3 grid, hipStream_t stream, const RmsArgs& a) {
     const dim3 block(64 * s.W * s.G);
     if (s.V == 1) hipLaunchKernelGGL((rms_forward_kernel<kF32, kQ8, 1, kThreads>), grid, block, 0, stream, a);
     else if (s.V == 2) hipLaunchKernelGGL((rms_forward_kernel<kF32, kQ8, 2, kThreads>), grid, block, 0, stream, a);
-    else if constexpr (kThreads < kRmsThreads)
+    else if constexpr (!kF32 && kThreads < kRmsThreads)
         hipLaunchKernelGGL((rms_forward_kernel<kF32, kQ8, 4, kThreads>), grid, block, 0, stream, a);
 }
 
@@ -366,12 +380,9 @@ size_t rmsnorm_partial_floats(int64_t M, int64_t N) { return (size_t)rms_backwar
 
 hipError_t launch_rmsnorm_forward(const RmsForwardIO& io, hipStream_t stream) {
     const int64_t M = io.M, N = io.N;
-    // Many rows: workgroups of four waves (eight past N = 8192), several per CU.  Few rows:
-    // up to sixteen waves a row, one step a lane as far as they reach: one round trip.
-    const bool many = M >= 1024;
-    const int threads = !many ? kRmsThreads : N <= 16 * kLnCols ? 256 : 512;
+    const int threads = forward_threads(M, N, io.f32);
     const LnShape s = ln_shape(N, threads);
-    const int64_t need = (M + s.G - 1) / s.G, most = many ? kLnForwardBlocks : 1 << 20;
+    const int64_t need = (M + s.G - 1) / s.G, most = M >= kManyRows ? kLnForwardBlocks : 1 << 20;
     const dim3 grid((unsigned)(need < most ? need : most));
     RmsArgs a;
     a.X = io.X;
