@@ -376,30 +376,47 @@ struct CombineBackwardArgs {
     float* dw;
     int64_t M;
     unsigned R;      // below 2^31
-    int N, W, G;     // W waves per token, G tokens per workgroup
+    int N, W, G;     // W waves per token, G tokens per workgroup; short rows: W lanes per token
 };
+
+// Sum over each W neighbouring lanes (a power of two up to 32), in the last of them: within
+// fours, eights and rows of 16 lanes by exchange, into the second of two rows by a copy.
+__device__ __forceinline__ float part_sum(float v, int W) {
+    if (W > 1) v = dpp_add<0xb1, 0xf>(v);     // quad_perm 1 0 3 2
+    if (W > 2) v = dpp_add<0x4e, 0xf>(v);     // quad_perm 2 3 0 1
+    if (W > 4) v = dpp_add<0x141, 0xf>(v);    // row_half_mirror
+    if (W > 8) v = dpp_add<0x140, 0xf>(v);    // row_mirror
+    if (W > 16) v = dpp_add<0x142, 0xa>(v);   // row_bcast:15 into rows 1 and 3
+    return v;
+}
 
 // dY is read once: every piece is multiplied into the k dot products and written,
 // weighted, to the k rows.  The dots are fp32 lane sums over a lane's pieces, then over
-// the wave, then over the W waves, in a fixed order.
-template <bool kF32, int K>
+// the wave, then over the W waves, in a fixed order.  Rows of up to 256 columns (kShort)
+// take as many lanes as they have pieces, several tokens to a wave (28000 x 104 fp32, top
+// 7, three quarters dropped: 16 us, a wave each 26).  A token without entries is not read
+// (8000 x 5456 fp32, top 4, three quarters dropped: 110 -> 101 us).
+template <bool kF32, int K, bool kShort>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackwardArgs a) {
     __shared__ float s_part[kThreads / 64][K];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = wave / a.W, w = wave % a.W;
+    const int g = kShort ? threadIdx.x / a.W : wave / a.W, w = kShort ? 0 : wave % a.W;
+    const int piece = kShort ? threadIdx.x % a.W : w * 64 + lane;
     const int64_t t = (int64_t)blockIdx.x * a.G + g;
     const bool on = t < a.M;
     int64_t at[K];
     float wt[K], dot[K];
+    bool any = false;
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         const int p = on ? a.pos[t * K + s] : -1;
         at[s] = (unsigned)p < a.R ? (int64_t)p * a.N : -1;   // (a negative one is past 2^31)
         wt[s] = on && a.w ? a.w[t * K + s] : 1.f;
         dot[s] = 0.f;
+        any |= at[s] >= 0;
     }
-    if (on)
-        for (int c = (w * 64 + lane) * 8; c < a.N; c += a.W * kLnCols) {
+    if (any)
+        for (int c = piece * 8; c < a.N; c += a.W * kLnCols) {
             Ln8<kF32> d, in[K];
             d.load(a.dY, t * a.N + c);
             if (a.dw) {
@@ -426,6 +443,14 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
             }
         }
     if (!a.dw) return;
+    if constexpr (kShort) {
+#pragma unroll
+        for (int s = 0; s < K; ++s) dot[s] = part_sum(dot[s], a.W);
+        if (!on || piece != a.W - 1) return;
+#pragma unroll
+        for (int s = 0; s < K; ++s) a.dw[t * K + s] = dot[s];
+        return;
+    }
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         const float v = wave_sum(dot[s]);
@@ -571,7 +596,9 @@ hipError_t launch_moe_combine_rows(const void* rows, int64_t R, const int32_t* p
 hipError_t launch_moe_combine_backward(const void* dY, const void* rows, int64_t R, const int32_t* pos,
                                        const float* w, void* drows, float* dw, int64_t M, int64_t N,
                                        int k, bool f32, hipStream_t stream) {
-    const int W = N > 2 * kLnCols ? 4 : N > kLnCols ? 2 : 1, G = kThreads / 64 / W;
+    const bool part = N <= kLnCols / 2;     // lanes of a wave
+    const int W = part ? 1 << threads_per_row_log(N / 8, 5) : N > 2 * kLnCols ? 4 : N > kLnCols ? 2 : 1;
+    const int G = (part ? kThreads : kThreads / 64) / W;
     return with_k(k, [&](auto K) {
         return in_slices(M, G, [&](int64_t t0, int64_t n, dim3 grid) {
             CombineBackwardArgs a;
@@ -586,10 +613,11 @@ hipError_t launch_moe_combine_backward(const void* dY, const void* rows, int64_t
             a.N = (int)N;
             a.W = W;
             a.G = G;
-            if (f32)
-                hipLaunchKernelGGL((combine_backward_kernel<true, K.value>), grid, dim3(kThreads), 0, stream, a);
-            else
-                hipLaunchKernelGGL((combine_backward_kernel<false, K.value>), grid, dim3(kThreads), 0, stream, a);
+            const dim3 block(kThreads);
+            if (f32 && part) hipLaunchKernelGGL((combine_backward_kernel<true, K.value, true>), grid, block, 0, stream, a);
+            else if (f32) hipLaunchKernelGGL((combine_backward_kernel<true, K.value, false>), grid, block, 0, stream, a);
+            else if (part) hipLaunchKernelGGL((combine_backward_kernel<false, K.value, true>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((combine_backward_kernel<false, K.value, false>), grid, block, 0, stream, a);
         });
     });
 }
