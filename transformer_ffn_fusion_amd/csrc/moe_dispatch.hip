@@ -63,6 +63,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
     Vec row{};
     if (chunk < a.chunks)
         row = *reinterpret_cast<const Vec*>(a.X + t * a.row_bytes + (int64_t)chunk * sizeof(Vec));
+    const bool scales = a.scale && blockIdx.y == 0;
+    float sc = 0.f;
+    if (scales && tid < a.scale_cols) sc = a.scale[t * a.scale_cols + tid];
     int id[kEach];
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
@@ -122,9 +125,10 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
         if (!kept) continue;
         if (chunk < a.chunks)
             *reinterpret_cast<Vec*>(a.Xs + (int64_t)pos * a.row_bytes + (int64_t)chunk * sizeof(Vec)) = row;
-        if (a.scale && blockIdx.y == 0)
-            for (int64_t c = tid; c < a.scale_cols; c += kThreads)
-                a.scale_sorted[pos * a.scale_cols + c] = a.scale[t * a.scale_cols + c];
+        if (!scales) continue;
+        if (tid < a.scale_cols) a.scale_sorted[pos * a.scale_cols + tid] = sc;
+        for (int64_t c = tid + kThreads; c < a.scale_cols; c += kThreads)
+            a.scale_sorted[pos * a.scale_cols + c] = a.scale[t * a.scale_cols + c];
     }
 }
 
@@ -181,7 +185,7 @@ template <typename Vec, bool kAll>
 __global__ __launch_bounds__(kSortThreads) void dispatch_sort_kernel(DispatchArgs a, int tpr_log) {
     constexpr int kWaves = kSortThreads / 64;
     __shared__ int s_one[kSortThreads], s_two[kSortThreads];   // then: the positions of a turn
-    __shared__ int s_base[kMaxExperts], s_scan[kMaxExperts];
+    __shared__ int s_base[kMaxExperts], s_scan[kWaves];
     __shared__ int s_w[kWaves][kMaxExperts];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.E, k = a.k;
     const int64_t t0 = blockIdx.x * a.per, t1 = t0 + a.per < a.M ? t0 + a.per : a.M;
@@ -225,17 +229,18 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_sort_kernel(DispatchArg
                 total = s_two[tid];
             }
         }
-        // exclusive prefix of the totals over the experts
-        if (tid < kMaxExperts) s_scan[tid] = tid < epow ? total : 0;
-        __syncthreads();
-        for (int d = 1; d < epow; d <<= 1) {
-            const int v = tid < epow && tid >= d ? s_scan[tid - d] : 0;
-            __syncthreads();
-            if (tid < epow) s_scan[tid] += v;
-            __syncthreads();
+        // prefix of the totals over the experts, one a thread: within the waves, then between them
+        int run = tid < epow ? total : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(run, d);
+            if (lane >= d) run += v;
         }
+        if (lane == 63) s_scan[wave] = run;
+        __syncthreads();
         if (tid < E) {
-            const int off = s_scan[tid] - total;
+            int off = run - total;
+            for (int q = 0; q < wave; ++q) off += s_scan[q];
             s_base[tid] = off + before;
             if (blockIdx.x == 0) {
                 a.offsets[tid] = off;
