@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxK = 8, kMaxExperts = 256;
-constexpr int kSmallEntries = 1024;     // most entries that every workgroup counts by itself
+constexpr int kSmallEntries = 2048, kSmallTokens = 1024;   // most of one launch that sorts nothing
 constexpr int kSortThreads = 1024;      // most entries of one turn of a workgroup that sorts
 constexpr int kSortBlocks = 256;        // most workgroups that sort
 
@@ -49,11 +49,13 @@ struct DispatchArgs {
 };
 
 // Few entries: one launch.  A workgroup takes 256 pieces of one token's row and counts
-// the entries before each of the token's k by itself, over all ids (at most 1024, from
-// the L2): no launch for a sort, and the row's load is under way meanwhile.
-template <typename Vec>
+// the entries before each of the token's k by itself, over all ids (from the L2): nothing
+// is sorted, and the row's load is under way meanwhile (1000 tokens of 256, top 2: 4.6 us, by
+// the next kernel 5.9; 2000 of 4096, top 1: 11.4, 10.4, since each token counts all).
+template <typename Vec, int kEach>
 __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a) {
-    constexpr int kEach = kSmallEntries / kThreads;
+    constexpr int kBits = 11;      // of an entry: (expert, entry) is one number to compare
+    static_assert(kEach * kThreads <= 1 << kBits && kMaxExperts < 1 << (31 - kBits), "keys of 32 bits");
     __shared__ int s_cnt[kThreads / 64][kMaxK];
     __shared__ int s_hist[kMaxExperts];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -66,12 +68,12 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
     const bool scales = a.scale && blockIdx.y == 0;
     float sc = 0.f;
     if (scales && tid < a.scale_cols) sc = a.scale[t * a.scale_cols + tid];
-    int id[kEach];
+    int key[kEach];
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
         const int i = u * kThreads + tid;
-        id[u] = i < n ? a.ids[i] : E;
-        if ((unsigned)id[u] >= (unsigned)E) id[u] = E;   // dropped: after all experts
+        const int id = i < n ? a.ids[i] : E;
+        key[u] = ((unsigned)id < (unsigned)E ? id : E) << kBits | i;   // dropped: after all experts
     }
     int mine[kMaxK];
 #pragma unroll
@@ -79,12 +81,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
         mine[s] = s < k ? a.ids[t * k + s] : -1;
         int before = 0;
         if (s < k) {
+            const int me = (int)((unsigned)mine[s] << kBits) | ((int)t * k + s);   // (a dropped one's is not used)
 #pragma unroll
-            for (int u = 0; u < kEach; ++u) {
-                const int i = u * kThreads + tid;
-                const bool ahead = id[u] < mine[s] || (id[u] == mine[s] && i < (int)t * k + s);
-                before += __popcll(__ballot(ahead));
-            }
+            for (int u = 0; u < kEach; ++u) before += __popcll(__ballot(key[u] < me));
         }
         if (lane == 0) s_cnt[wave][s] = before;
     }
@@ -94,7 +93,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
     if (first) {     // the same for the whole workgroup
 #pragma unroll
         for (int u = 0; u < kEach; ++u)
-            if (id[u] < E) atomicAdd(&s_hist[id[u]], 1);   // a count: the order does not matter
+            if (key[u] >> kBits < E) atomicAdd(&s_hist[key[u] >> kBits], 1);   // a count: the order does not matter
         __syncthreads();
         // exclusive prefix over the experts, one a thread: within the waves, then between them
         const int mine_e = tid < E ? s_hist[tid] : 0;
@@ -543,10 +542,14 @@ hipError_t launch_moe_dispatch(const DispatchIO& io, hipStream_t stream) {
     a.blocks = (int)sort_blocks(io.M, io.k);
     const bool wide = io.row_bytes % 16 == 0;   // e4m3 rows of odd multiples of 8: 8-byte pieces
     a.chunks = (int)(io.row_bytes / (wide ? 16 : 8));
-    if (a.n <= kSmallEntries) {
+    if (a.n <= kSmallEntries && io.M <= kSmallTokens) {
         const dim3 grid((unsigned)io.M, (unsigned)((a.chunks + kThreads - 1) / kThreads));
-        if (wide) hipLaunchKernelGGL(dispatch_small_kernel<uint4>, grid, dim3(kThreads), 0, stream, a);
-        else hipLaunchKernelGGL(dispatch_small_kernel<uint2>, grid, dim3(kThreads), 0, stream, a);
+        auto go = [&](auto each) {
+            if (wide) hipLaunchKernelGGL((dispatch_small_kernel<uint4, each.value>), grid, dim3(kThreads), 0, stream, a);
+            else hipLaunchKernelGGL((dispatch_small_kernel<uint2, each.value>), grid, dim3(kThreads), 0, stream, a);
+        };
+        if (a.n <= 4 * kThreads) go(std::integral_constant<int, 4>());
+        else go(std::integral_constant<int, kSmallEntries / kThreads>());
         return hipGetLastError();
     }
     const dim3 blocks((unsigned)a.blocks), threads(kSortThreads);
