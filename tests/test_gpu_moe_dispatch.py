@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 CASES = [(1, 8, 1, 1), (1, 4096, 8, 2), (16, 4096, 8, 2), (3, 72, 5, 5), (128, 24, 256, 8), (341, 136, 24, 3),
          (342, 136, 24, 3), (513, 264, 7, 2), (1013, 2056, 64, 6), (257, 8200, 100, 4), (4099, 16, 33, 7),
          (40000, 8, 256, 8), (140001, 8, 3, 2), (999, 56, 9, 4), (2001, 256, 16, 8),
-         (1024, 136, 24, 2), (1025, 136, 24, 1), (683, 64, 256, 3), (256, 4104, 8, 8)]
+         (1024, 136, 24, 2), (1025, 136, 24, 1), (683, 64, 256, 3), (256, 4104, 8, 8), (1536, 136, 16, 8), (1537, 72, 16, 8), (12288, 24, 200, 1)]
 
 
 def route(M, E, k, seed, drop=0.2):

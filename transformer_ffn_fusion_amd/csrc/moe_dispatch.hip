@@ -178,8 +178,9 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_count_kernel(DispatchAr
 // of the expert (lanes that agree in every bit are peers), between waves by their counts.
 //
 // kAll, for up to kCountAll entries, is the only step: every block counts all ids itself and
-// moves its rows too (2048 entries, 4096 columns: 9 us instead of 13 in three launches; with
-// more entries the counting grows, and 256 workgroups move rows at 3/4 of the rate of many).
+// moves its rows too (12288 entries, 2048 columns: 15.3 us instead of 17.3 in three launches;
+// 16384 of 7168 bytes: 42.1, 40.6: the counting grows with them, and 256 workgroups move rows at
+// 3/4 of the rate of many).
 template <typename Vec, bool kAll>
 __global__ __launch_bounds__(kSortThreads) void dispatch_sort_kernel(DispatchArgs a, int tpr_log) {
     constexpr int kWaves = kSortThreads / 64;
@@ -188,6 +189,11 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_sort_kernel(DispatchArg
     __shared__ int s_w[kWaves][kMaxExperts];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.E, k = a.k;
     const int64_t t0 = blockIdx.x * a.per, t1 = t0 + a.per < a.M ? t0 + a.per : a.M;
+    const int turn = kSortThreads / k;     // tokens of one turn
+    auto expert = [&](int64_t base) {      // of this thread's entry in the turn from token `base` on
+        return tid < (t1 - base < turn ? (int)(t1 - base) : turn) * k ? a.ids[base * k + tid] : -1;
+    };
+    int next = expert(t0);                 // (under way while the counts are added)
     int epow = 1, bits = 0;
     while (epow < E) {
         epow <<= 1;
@@ -216,16 +222,23 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_sort_kernel(DispatchArg
         } else {
             if (tid < kMaxExperts) s_one[tid] = s_two[tid] = 0;
             __syncthreads();
-            for (int i = tid; i < (int)a.n; i += kSortThreads) {
-                const int e = a.ids[i];
-                if ((unsigned)e >= (unsigned)E) continue;
-                atomicAdd(&s_two[e], 1);                       // counts: the order does not matter
-                if (i < (int)t0 * k) atomicAdd(&s_one[e], 1);
+            constexpr int kBatch = 8;      // loads under way at once
+            for (int i0 = tid; i0 < (int)a.n; i0 += kBatch * kSortThreads) {
+                int id[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = i0 + u * kSortThreads;
+                    id[u] = i < (int)a.n ? a.ids[i] : -1;
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)     // counts: the order does not matter
+                    if ((unsigned)id[u] < (unsigned)E)
+                        atomicAdd(i0 + u * kSortThreads < (int)t0 * k ? &s_one[id[u]] : &s_two[id[u]], 1);
             }
             __syncthreads();
             if (tid < epow) {
                 before = s_one[tid];
-                total = s_two[tid];
+                total = before + s_two[tid];
             }
         }
         // prefix of the totals over the experts, one a thread: within the waves, then between them
@@ -248,13 +261,13 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_sort_kernel(DispatchArg
         }
     }
     const uint64_t lt = lane == 0 ? 0ull : ~0ull >> (64 - lane);
-    const int turn = kSortThreads / k;     // tokens of one turn
     const int tpr = 1 << tpr_log, c0 = tid & (tpr - 1), r0 = tid >> tpr_log, step = kSortThreads >> tpr_log;
     for (int64_t base = t0; base < t1; base += turn) {
         const int tokens = t1 - base < turn ? (int)(t1 - base) : turn;
         const int64_t i = base * k + tid;
         const bool have = tid < tokens * k;
-        const int e = have ? a.ids[i] : -1;
+        const int e = next;
+        if (base + turn < t1) next = expert(base + turn);
         const bool kept = (unsigned)e < (unsigned)E;
         // (a wave clears its own counts: slower waves still read theirs of the last turn)
         for (int q = lane; q < kMaxExperts; q += 64) s_w[wave][q] = 0;
@@ -312,7 +325,7 @@ int threads_per_row_log(int64_t pieces, int most) {
 
 // Tokens per workgroup of the sort, and its workgroups.  With all ids counted by each the rows
 // are spread as far as they go; otherwise whole turns, for fewer counts to add.
-constexpr int64_t kCountAll = 8192;   // most entries that every workgroup counts by itself
+constexpr int64_t kCountAll = 12288;   // most entries that every workgroup counts by itself
 int64_t sort_tokens(int64_t M, int k) {
     const int64_t even = (M + kSortBlocks - 1) / kSortBlocks, turn = kSortThreads / k;
     if (M * k <= kCountAll) return even > 0 ? even : 1;
