@@ -311,24 +311,32 @@ __global__ __launch_bounds__(kRmsThreads) void rms_backward_kernel(
 }
 
 // dgamma from the workgroups' partial rows, in a fixed order: 32 threads per column add
-// every 32nd partial, eight loads at most, then one adds the 32 sums (call of 1000 x 256 bf16
-// 5.7 us; with 16 threads per column 6.05, with 64 and half the line of a load 5.95).
+// every 32nd partial, whose eight loads are under way at once however many there are, then one
+// adds the 32 sums (call of 1000 x 256 bf16 5.7 us; with 16 threads per column 6.05, with 64
+// and half the line of a load 5.95).
 __global__ __launch_bounds__(1024) void rms_finish_kernel(const float* __restrict__ part, int rows,
                                                           int N, float* __restrict__ dgamma) {
-    __shared__ float s[32][32 + 1];
+    constexpr int kSlices = 32, kEach = kLnBackwardBlocks / kSlices;
+    __shared__ float s[kSlices][32 + 1];
     const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + c;
     float v = 0.f;
     if (col < N) {
-#pragma unroll 8
-        for (int r = k; r < rows; r += 32) v += part[(int64_t)r * N + col];
+        float x[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int r = k + u * kSlices;
+            x[u] = part[(int64_t)(r < rows ? r : rows - 1) * N + col];
+        }
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) v += k + u * kSlices < rows ? x[u] : 0.f;
     }
     s[k][c] = v;
     __syncthreads();
     if (k || col >= N) return;
     float t = 0.f;
 #pragma unroll
-    for (int q = 0; q < 32; ++q) t += s[q][c];
+    for (int q = 0; q < kSlices; ++q) t += s[q][c];
     dgamma[col] = t;
 }
 
