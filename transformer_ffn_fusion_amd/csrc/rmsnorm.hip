@@ -359,14 +359,15 @@ int64_t rms_backward_blocks(int64_t M, int64_t N) {
     return need < kLnBackwardBlocks ? need : kLnBackwardBlocks;
 }
 
-// Largest workgroup of the forward.  Few rows: up to sixteen waves a row, one step a lane as far
-// as they reach: one round trip.  Many rows of fp32 likewise (8192 columns: 96 us, with four waves
-// of four steps 100; 5824: 98, 105); of bf16 in four waves, several workgroups per CU (8192
-// columns into 8 bits: 42 us, with sixteen waves 50).  Past 8192 columns two steps a lane, while
-// two workgroups of them fit a CU (12288 bf16 into 8 bits: 45 us, with eight waves of four steps 69);
-// past 12288 one would be alone, and bf16 takes four steps in eight waves, within 128 registers
-// (16384 bf16: 50 us, with sixteen waves 54; into 8 bits 53, 56).
-constexpr int64_t kManyRows = 1024;
+// Largest workgroup of the forward.  Few rows: one to a workgroup, of up to sixteen waves, one step
+// a lane as far as they reach: one round trip (16 x 4096 bf16: 2.9 us; two to a workgroup 3.35;
+// 520 x 4096: 5.6, by the shapes of many rows 5.0).  Many rows of fp32: as few steps a lane (8192
+// columns: 96 us, with four waves of four steps 100; 5824: 98, 105).  Of bf16: four waves, several
+// workgroups per CU (8192 columns into 8 bits: 42 us, with sixteen waves 50).  Past 8192 columns two
+// steps a lane, while two workgroups of them fit a CU (12288 bf16 into 8 bits: 45 us, with eight
+// waves of four steps 69); past 12288 one would be alone, and bf16 takes four steps in eight
+// waves, within 128 registers (16384 bf16: 50 us, with sixteen waves 54; into 8 bits 53, 56).
+constexpr int64_t kManyRows = 256;
 int forward_threads(int64_t M, int64_t N, bool f32) {
     if (M < kManyRows) return kRmsThreads;
     if (f32) return N <= 4 * kLnCols ? 256 : N <= 8 * kLnCols ? 512 : kRmsThreads;
@@ -389,7 +390,8 @@ size_t rmsnorm_partial_floats(int64_t M, int64_t N) { return (size_t)rms_backwar
 hipError_t launch_rmsnorm_forward(const RmsForwardIO& io, hipStream_t stream) {
     const int64_t M = io.M, N = io.N;
     const int threads = forward_threads(M, N, io.f32);
-    const LnShape s = ln_shape(N, threads);
+    LnShape s = ln_shape(N, threads);
+    if (M < kManyRows) s.G = 1;
     const int64_t need = (M + s.G - 1) / s.G, most = M >= kManyRows ? kLnForwardBlocks : 1 << 20;
     const dim3 grid((unsigned)(need < most ? need : most));
     RmsArgs a;
