@@ -67,6 +67,19 @@ def test_matvec(shape, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", [(136, 8712), (648, 12296), (136, 25608), (264, 28664), (72, 40)])
+def test_wide_matrices(shape, kind):
+    """Several column tiles a wave, the last of them past the matrix."""
+    K, C = shape
+    print(f"case wide 4-bit product {shape} {kind}", flush=True)
+    w = weight(K, C, kind, seed=K + C)
+    for M in (1, 6, 16):
+        X, Y = inputs(M, K, M), empty(M, C)
+        ffn.ffn_q4_matvec(X, w[0], w[1], Y, zero=w[2], code=kind[0])
+        ref.check({"Y": Y}, ref.q4_matvec(X, *cpu(w), None, "none", C, kind[0]), f"{shape} {kind} {M} rows")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("shape", SHAPES)
 def test_swiglu(shape, kind):
     K, C = shape

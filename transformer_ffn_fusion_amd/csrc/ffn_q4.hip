@@ -17,9 +17,9 @@
 //  * The waves of a workgroup share its columns and split K; their sums are joined in
 //    LDS in ascending order, so results do not depend on timing, and one launch is all.
 // Measured (kernel; 16 tokens unless said): pair of 8192 x 3584 9.5 us (30.3 MB; without its
-// loads of X 8.5), experts' pairs of 8 x 4096 x 2048 13.0-13.9 us (of 69 MB the
-// 58 of experts that have rows), 4096 x
-// 4096 with zero points, one token, 4.2 us, of which about 3 are a kernel's way in and out.
+// loads of X 8.5), experts' pairs of 8 x 4096 x 2048 13.5 us (of 69 MB the 58 of experts that
+// have rows), 8192 x 28672 30 us (118 MB, one token 25), 4096 x 4096 with zero points, one
+// token, 4.2 us, of which about 3 are a kernel's way in and out.
 // Three or four stages in flight instead of two: no faster or slower (16 x 4096 x 4096: 5.0
 // us, with three 6.4), sixteen waves likewise (16 x 14336 x 4096: 10.9, 12.1).
 #include <type_traits>
@@ -379,18 +379,26 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* codes, cons
 // Column tiles per wave and waves per workgroup.  Two tiles share a wave's rows of X, which
 // for 16 rows are more bytes than a tile's codes, and halve the workgroups: taken where at
 // least one workgroup per CU is left (16 x 8192 x 8192: 12.6 -> 10.8 us; 16 x 4096 x 4096, 128
-// workgroups: 5.3 -> 6.4 us; the gated pair shares them already).  Few workgroups take eight
-// waves each (16 rows, pair of 8192 x 3584, 224 workgroups: 10.3 us, with four 11.6), many take
-// four, of which more fit a CU while others join their sums (pair of 4096 x 14336, 896: 17.7 ->
-// 15.8 us).
+// workgroups: 5.3 -> 6.4 us; the gated pair shares them already).  Four of integers, where their
+// fewer workgroups leave no CU with more tiles than two would (16 x 8192 x 28672, eight a CU
+// either way: 34 -> 30 us; 16 x 4096 x 22016, eight instead of six: 13.0 -> 14.8; e2m1, whose
+// rows need no sums: no faster).  Up to one workgroup per CU takes eight waves (16 rows, pair of
+// 8192 x 3584, 224 workgroups: 10.3 us, with four 11.6).  More of them take four: of eight, whose
+// registers fill half a CU or more, the second waits for the first (16 x 4096 x 14336, 448
+// workgroups: 11.8 -> 9.8 us; pair of 4096 x 8192 with zero points, 512: 13.3 -> 11.4).  Experts
+// without rows have workgroups that end at once: those are not counted.
 struct Q4Shape {
     int tiles, waves;
 };
 Q4Shape q4_shape(const Q4IO& io, int64_t tiles, int kt) {
+    constexpr int64_t kCUs = 256;
+    const int64_t lists = io.rows < io.E ? io.rows : io.E;
+    auto groups = [&](int n) { return (tiles + n - 1) / n * lists; };
+    auto fullest = [&](int n) { return (groups(n) + kCUs - 1) / kCUs * n; };   // tiles of a CU
     Q4Shape s;
-    s.tiles = !io.gated && tiles * io.E >= 512 ? 2 : 1;
-    const int64_t groups = (tiles + s.tiles - 1) / s.tiles * io.E;
-    s.waves = groups >= 640 || kt <= 4 ? 4 : kMaxWaves;
+    s.tiles = io.gated || tiles * lists < 2 * kCUs ? 1 : 2;
+    if (s.tiles == 2 && io.code == kQ4Int && !io.offsets && groups(4) > kCUs && fullest(4) <= fullest(2)) s.tiles = 4;
+    s.waves = groups(s.tiles) > kCUs || kt <= 4 ? 4 : kMaxWaves;
     return s;
 }
 
@@ -402,8 +410,10 @@ void start(const Q4Args& a, const Q4Shape& s, const Q4IO& io, int64_t tiles, hip
         hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, true, 1>), grid, block, lds, stream, a);
     else if (s.tiles == 1)
         hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 1>), grid, block, lds, stream, a);
-    else
+    else if (s.tiles == 2)
         hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 2>), grid, block, lds, stream, a);
+    else if constexpr (kCode == kQ4Int)
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 4>), grid, block, lds, stream, a);
 }
 
 }  // namespace
