@@ -485,7 +485,7 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float
  * were in Y.  Offsets are read on the device and kept inside [0, rows].
  *
  * K, C multiples of 8 below 2^22, K * C below 2^31; M <= 16, and up to 4096 rows in the
- * moe_ forms, whose weights are read once per 16 rows of an expert.  A row with an
+ * moe_ forms, whose weights are read once per 16 or 32 rows of an expert.  A row with an
  * infinity, or whose integers' partial sums leave fp32 (|x| from about 1e36 on), gives
  * NaN or infinity.  With no rows nothing is done. */
 typedef enum { FFN_Q4_INT = 0, FFN_Q4_E2M1 = 1 } ffn_q4_t;

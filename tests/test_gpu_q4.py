@@ -137,6 +137,16 @@ def test_experts(shape, counts, kind):
     assert bool((Y[n:] == 7.0).all()) and bool((H[n:] == 7.0).all())
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("counts", [[32, 4, 0, 64, 9], [18, 33, 5, 8, 17, 31], [4093]])
+@pytest.mark.parametrize("shape", [(264, 72), (136, 4104)])
+def test_experts_of_many_rows(shape, counts, kind):
+    """Lists of more than ten rows on average: up to 32 at once."""
+    if len(counts) == 1 and shape[1] > 100:
+        counts = [100]
+    test_experts(shape, counts, kind)
+
+
 def test_offsets_outside_the_rows():
     """Offsets that decrease or leave the rows: every row that is written belongs to the list as it is
     kept inside the rows."""

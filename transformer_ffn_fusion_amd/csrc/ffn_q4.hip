@@ -5,7 +5,7 @@
 //   one s (and z) per column and group of 32, 64 or 128 k
 //   Y = act(X W + b)   or   H = silu(X Wg) * (X Wu);   X, Y bf16, sums fp32
 //
-// Bound: the HBM time of the codes -- every weight is used for up to 16 rows only.
+// Bound: the HBM time of the codes -- every weight is used for up to 16 rows only, or 32.
 //  * The packed layout is the matrix instruction's operand: a tile of 16 columns x 128 k
 //    is 64 lanes x 16 bytes in lane order, so a wave loads 1 KiB at once and no value
 //    changes lanes.  Lane l's word j holds the 8 codes of column l % 16, k = 32 j +
@@ -32,7 +32,7 @@ namespace ffn {
 namespace {
 
 constexpr int kMaxWaves = 8;
-constexpr int kWaveLds = kQ4Rows * kQ4TileK * 2;   // a wave's rows of one tile, then its sums
+constexpr int kBlockLds = kQ4Rows * kQ4TileK * 2;  // a wave's 16 rows of one tile, then its sums
 enum { kQ4Int = 0, kQ4E2m1 = 1 };
 
 struct Q4Args {
@@ -80,12 +80,13 @@ __device__ __forceinline__ void lanes_meet() {
 }
 
 // kZero: integers with zero points; kPer groups per tile; kTiles column tiles per wave
-// (of each matrix).
-template <int kCode, bool kZero, int kPer, bool kGated, int kTiles>
+// (of each matrix); up to kBlocks times 16 rows at once.
+template <int kCode, bool kZero, int kPer, bool kGated, int kTiles, int kBlocks>
 __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
     constexpr int kMats = kGated ? 2 : 1, kNT = kTiles * kMats;
     constexpr int kSteps = 4 / kPer;              // matrix instructions per group
-    static_assert(1024 * kNT <= kWaveLds, "a wave's sums take the place of its rows");
+    constexpr int kWaveLds = kBlocks * kBlockLds;
+    static_assert(1024 * kNT <= kBlockLds, "a wave's sums take the place of its rows");
     extern __shared__ __attribute__((aligned(16))) char s_all[];   // kWaveLds per wave
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
@@ -137,9 +138,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
     const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     const int waves = blockDim.x >> 6;
 
-    // Rows r0 .. r0 + have, loaded with kXLoads loads per tile: of 4, 8 or 16 rows.
+    // Rows r0 .. r0 + have, loaded with kXLoads loads per tile: of 4, 8, 16 or 32 rows.
     auto rows = [&](int r0, int have, auto loads) {
-        constexpr int kXLoads = loads.value;
+        constexpr int kXLoads = loads.value, kB = (kXLoads + 3) / 4;   // blocks of 16 rows
         struct Stage {
             uint4 w[kNT], x[kXLoads];
             uint32_t s[kNT][(kPer + 1) / 2], z[kNT][(kPer + 1) / 2];
@@ -169,53 +170,65 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
             }
         };
         // The operands of a tile's four steps, through the wave's own LDS (a wave's LDS accesses
-        // keep their order): row r's 16-byte piece p lies at 256 r + 16 (p ^ r), so that neither
+        // keep their order): row r's 16-byte piece p lies at 256 r + 16 (p ^ r % 16), so that neither
         // the writes (16 pieces of a row) nor the reads (one piece of 16 rows) meet in a bank.
         // Rows that no load brings hold what was there; their results are not stored.
-        auto operands = [&](const Stage& st, uint4 (&x)[4]) {
+        auto operands = [&](const Stage& st, uint4 (&x)[kB][4]) {
             lanes_meet();   // (the last tile's reads)
 #pragma unroll
             for (int j = 0; j < kXLoads; ++j) {
                 const int r = 4 * j + (lane >> 4);
-                *reinterpret_cast<uint4*>(s_wave + 256 * r + 16 * (c ^ r)) = st.x[j];
+                *reinterpret_cast<uint4*>(s_wave + 256 * r + 16 * (c ^ (r & 15))) = st.x[j];
             }
             lanes_meet();
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                x[s] = *reinterpret_cast<const uint4*>(s_wave + 256 * c + 16 * ((4 * s + g) ^ c));
-        };
-        floatx4_t acc[kNT];
+            for (int b = 0; b < kB; ++b)
 #pragma unroll
-        for (int i = 0; i < kNT; ++i) acc[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < 4; ++s)
+                    x[b][s] = *reinterpret_cast<const uint4*>(s_wave + kBlockLds * b + 256 * c + 16 * ((4 * s + g) ^ c));
+        };
+        floatx4_t acc[kB][kNT];
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+#pragma unroll
+            for (int i = 0; i < kNT; ++i) acc[b][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
         auto multiply = [&](const Stage& st, int kt) {
-            uint4 x[4];
+            uint4 x[kB][4];
             operands(st, x);
 #pragma unroll
             for (int p = 0; p < kPer; ++p) {
                 // a group past K: its scale may be anything
                 const bool real = (int64_t)kt * kQ4TileK + p * (kQ4TileK / kPer) < a.K;
-                floatx4_t xs = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (kCode == kQ4Int)
+                floatx4_t xs[kB];
 #pragma unroll
-                    for (int j = 0; j < kSteps; ++j) xs = mfma16x16x32(x[p * kSteps + j], ones, xs);
+                for (int b = 0; b < kB; ++b) {
+                    xs[b] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+                    if constexpr (kCode == kQ4Int)
+#pragma unroll
+                        for (int j = 0; j < kSteps; ++j) xs[b] = mfma16x16x32(x[b][p * kSteps + j], ones, xs[b]);
+                }
 #pragma unroll
                 for (int i = 0; i < kNT; ++i) {
                     const uint32_t words[4] = {st.w[i].x, st.w[i].y, st.w[i].z, st.w[i].w};
-                    floatx4_t sum = {0.f, 0.f, 0.f, 0.f};
+                    floatx4_t sum[kB];
 #pragma unroll
-                    for (int j = 0; j < kSteps; ++j)
-                        sum = mfma16x16x32(x[p * kSteps + j],
-                                           decode8(words[p * kSteps + j], mask, std::integral_constant<int, kCode>()), sum);
-                    const float s = real ? value(st.s[i], p) : 0.f;
-                    if constexpr (kCode == kQ4Int) {
-                        float z = 24.f;
-                        if constexpr (kZero) z = 16.f + (real ? value(st.z[i], p) : 0.f);
+                    for (int b = 0; b < kB; ++b) sum[b] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(s, fmaf(-z, xs[r], sum[r]), acc[i][r]);
-                    } else {
+                    for (int j = 0; j < kSteps; ++j) {
+                        const uint4 w = decode8(words[p * kSteps + j], mask, std::integral_constant<int, kCode>());
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(s, sum[r], acc[i][r]);
+                        for (int b = 0; b < kB; ++b) sum[b] = mfma16x16x32(x[b][p * kSteps + j], w, sum[b]);
                     }
+                    const float s = real ? value(st.s[i], p) : 0.f;
+                    float z = 24.f;
+                    if constexpr (kZero) z = 16.f + (real ? value(st.z[i], p) : 0.f);
+#pragma unroll
+                    for (int b = 0; b < kB; ++b)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float v = kCode == kQ4Int ? fmaf(-z, xs[b][r], sum[b][r]) : sum[b][r];
+                            acc[b][i][r] = fmaf(s, v, acc[b][i][r]);
+                        }
                 }
             }
         };
@@ -237,19 +250,24 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < kNT; ++i)
-            *reinterpret_cast<floatx4_t*>(s_wave + 1024 * i + 16 * lane) = acc[i];
+        for (int b = 0; b < kB; ++b)
+#pragma unroll
+            for (int i = 0; i < kNT; ++i)
+                *reinterpret_cast<floatx4_t*>(s_wave + 1024 * (b * kNT + i) + 16 * lane) = acc[b][i];
     };
 
-    for (int r0 = lo; r0 < hi; r0 += kQ4Rows) {
-        const int have = hi - r0 < kQ4Rows ? hi - r0 : kQ4Rows;
+    constexpr int kRows = kBlocks * kQ4Rows;
+    for (int r0 = lo; r0 < hi; r0 += kRows) {
+        const int have = hi - r0 < kRows ? hi - r0 : kRows;
         if (have <= 4) rows(r0, have, std::integral_constant<int, 1>());
         else if (have <= 8) rows(r0, have, std::integral_constant<int, 2>());
-        else rows(r0, have, std::integral_constant<int, 4>());
+        else if (have <= 16) rows(r0, have, std::integral_constant<int, 4>());
+        else if constexpr (kBlocks > 1) rows(r0, have, std::integral_constant<int, 8>());
         __syncthreads();
-        for (int o = threadIdx.x; o < kTiles * 256; o += blockDim.x) {
+        for (int q0 = threadIdx.x; q0 < kTiles * 256 * (have > kQ4Rows ? 2 : 1); q0 += blockDim.x) {
             // a lane's four sums are rows 4 (lane / 16) .. + 3 of column lane % 16
-            const int t = o >> 8, m = 4 * ((o >> 6) & 3) + (o & 3);
+            const int b = q0 / (kTiles * 256), o = q0 % (kTiles * 256);
+            const int t = o >> 8, m = kQ4Rows * b + 4 * ((o >> 6) & 3) + (o & 3);
             const int64_t col = (ct0 + t) * kQ4TileCols + ((o >> 2) & 15);
             float v[kMats];
 #pragma unroll
@@ -259,7 +277,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int q = 0; q < kMats; ++q)
-                        v[q] += *reinterpret_cast<const float*>(s_all + (w + u) * kWaveLds + 1024 * (q * kTiles) + 4 * o);
+                        v[q] += *reinterpret_cast<const float*>(s_all + (w + u) * kWaveLds + 1024 * (b * kNT + q * kTiles) + 4 * o);
             if (m >= have || col >= a.C) continue;
             float y;
             if constexpr (kGated) {
@@ -270,7 +288,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
             }
             a.Y[(int64_t)(r0 + m) * a.C + col] = __builtin_bit_cast(uint16_t, (__bf16)y);
         }
-        if (r0 + kQ4Rows < hi) __syncthreads();   // read before the next rows' sums
+        if (r0 + kRows < hi) __syncthreads();   // read before the next rows' sums
     }
 }
 
@@ -376,7 +394,7 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* codes, cons
     }
 }
 
-// Column tiles per wave and waves per workgroup.  Two tiles share a wave's rows of X, which
+// Column tiles per wave, waves per workgroup, rows at once.  Two tiles share a wave's rows of X, which
 // for 16 rows are more bytes than a tile's codes, and halve the workgroups: taken where at
 // least one workgroup per CU is left (16 x 8192 x 8192: 12.6 -> 10.8 us; 16 x 4096 x 4096, 128
 // workgroups: 5.3 -> 6.4 us; the gated pair shares them already).  Four of integers, where their
@@ -387,8 +405,12 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* codes, cons
 // registers fill half a CU or more, the second waits for the first (16 x 4096 x 14336, 448
 // workgroups: 11.8 -> 9.8 us; pair of 4096 x 8192 with zero points, 512: 13.3 -> 11.4).  Experts
 // without rows have workgroups that end at once: those are not counted.
+//
+// Rows at once: 32 where lists are longer than ten rows on average, so that many pass 16 (pair of
+// 8 x 4096 x 2048: 192 rows 32 -> 27 us, 128 23.1 -> 20.2, 96 19.1 -> 17.8; 60 x 2048 x 1408,
+// 512 rows, 8.5 a list: 41.2 -> 42.9, for half again as many registers).
 struct Q4Shape {
-    int tiles, waves;
+    int tiles, waves, blocks;
 };
 Q4Shape q4_shape(const Q4IO& io, int64_t tiles, int kt) {
     constexpr int64_t kCUs = 256;
@@ -397,23 +419,28 @@ Q4Shape q4_shape(const Q4IO& io, int64_t tiles, int kt) {
     auto fullest = [&](int n) { return (groups(n) + kCUs - 1) / kCUs * n; };   // tiles of a CU
     Q4Shape s;
     s.tiles = io.gated || tiles * lists < 2 * kCUs ? 1 : 2;
+    // (one matrix, so at most 16 rows)
     if (s.tiles == 2 && io.code == kQ4Int && !io.offsets && groups(4) > kCUs && fullest(4) <= fullest(2)) s.tiles = 4;
     s.waves = groups(s.tiles) > kCUs || kt <= 4 ? 4 : kMaxWaves;
+    s.blocks = io.rows > kQ4Rows && io.rows > 10 * lists ? 2 : 1;
     return s;
 }
 
-template <int kCode, bool kZero, int kPer>
-void start(const Q4Args& a, const Q4Shape& s, const Q4IO& io, int64_t tiles, hipStream_t stream) {
+template <int kCode, bool kZero, int kPer, int kBlocks>
+hipError_t start(const Q4Args& a, const Q4Shape& s, const Q4IO& io, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)((tiles + s.tiles - 1) / s.tiles), (unsigned)io.E), block(64 * s.waves);
-    const size_t lds = (size_t)s.waves * kWaveLds;
+    const size_t lds = (size_t)s.waves * kBlocks * kBlockLds;
     if (io.gated)
-        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, true, 1>), grid, block, lds, stream, a);
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, true, 1, kBlocks>), grid, block, lds, stream, a);
     else if (s.tiles == 1)
-        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 1>), grid, block, lds, stream, a);
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 1, kBlocks>), grid, block, lds, stream, a);
     else if (s.tiles == 2)
-        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 2>), grid, block, lds, stream, a);
-    else if constexpr (kCode == kQ4Int)
-        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 4>), grid, block, lds, stream, a);
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 2, kBlocks>), grid, block, lds, stream, a);
+    else if constexpr (kCode == kQ4Int && kBlocks == 1)
+        hipLaunchKernelGGL((q4_kernel<kCode, kZero, kPer, false, 4, 1>), grid, block, lds, stream, a);
+    else
+        return hipErrorInvalidValue;    // no rule gives this shape
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -440,17 +467,19 @@ hipError_t launch_q4(const Q4IO& io, hipStream_t stream) {
     a.b_stride = io.C;
     a.act = io.act;
     const Q4Shape s = q4_shape(io, tiles, a.kt);
-    auto go = [&](auto code, auto z, auto p) { start<code.value, z.value, p.value>(a, s, io, tiles, stream); };
+    auto go = [&](auto code, auto z, auto p) {
+        return s.blocks == 2 ? start<code.value, z.value, p.value, 2>(a, s, io, tiles, stream)
+                             : start<code.value, z.value, p.value, 1>(a, s, io, tiles, stream);
+    };
     auto with = [&](auto code, auto z) {
-        if (per == 1) go(code, z, std::integral_constant<int, 1>());
-        else if (per == 2) go(code, z, std::integral_constant<int, 2>());
-        else go(code, z, std::integral_constant<int, 4>());
+        if (per == 1) return go(code, z, std::integral_constant<int, 1>());
+        if (per == 2) return go(code, z, std::integral_constant<int, 2>());
+        return go(code, z, std::integral_constant<int, 4>());
     };
     using Int = std::integral_constant<int, kQ4Int>;
-    if (io.code == kQ4E2m1) with(std::integral_constant<int, kQ4E2m1>(), std::false_type());
-    else if (io.zero[0]) with(Int(), std::true_type());
-    else with(Int(), std::false_type());
-    return hipGetLastError();
+    if (io.code == kQ4E2m1) return with(std::integral_constant<int, kQ4E2m1>(), std::false_type());
+    if (io.zero[0]) return with(Int(), std::true_type());
+    return with(Int(), std::false_type());
 }
 
 hipError_t launch_q4_quantize(const void* W, bool f32, uint8_t* Wq, uint16_t* scale, uint16_t* zero,
