@@ -9,8 +9,8 @@ import transformer_ffn_fusion_amd as ffn
 import sublayer_ref as ref
 
 pytestmark = pytest.mark.gpu
-# (M, N, E, k): one token; few tokens; around 1024 entries, where the sort becomes launches of its
-# own; many entries, more than one turn of a sort workgroup; every k
+# (M, N, E, k): one token; few tokens; around 1024, 2048 and 12288 entries and 1024 tokens, where the
+# kernels change; many entries, more than one turn of a sort workgroup; rows of every width; every k
 CASES = [(1, 8, 1, 1), (1, 4096, 8, 2), (16, 4096, 8, 2), (3, 72, 5, 5), (128, 24, 256, 8), (341, 136, 24, 3),
          (342, 136, 24, 3), (513, 264, 7, 2), (1013, 2056, 64, 6), (257, 8200, 100, 4), (4099, 16, 33, 7),
          (40000, 8, 256, 8), (140001, 8, 3, 2), (999, 56, 9, 4), (2001, 256, 16, 8),
