@@ -68,6 +68,24 @@ def check_q8(Q, scale, S, gamma, eps, group, what):
     assert not bool(bad.any()), f"{what}: {int(bad.sum())} codes are not the nearest"
 
 
+def q8_codes(S, gamma, group):
+    """The codes of bf16 ``S`` and ``gamma`` by the definition, e4m3(448 w / max |w|) with w = s gamma and ties
+    to the even code: every number that decides between two codes is exact in fp64 (w: 16 bits, halfway points
+    times max |w|: 21 bits)."""
+    w = d(S) * d(gamma)
+    M, N = w.shape
+    pad = torch.nn.functional.pad(w, (0, -N % (group or N))).reshape(M, -1, group or N)
+    top = pad.abs().amax(2, keepdim=True)
+    mag = pad.abs() * E4M3_MAX
+    v = torch.where(top > 0, mag / top, 0.0)
+    _, e = torch.frexp(v)
+    step = torch.ldexp(torch.ones_like(v), (e - 1).clamp(min=-6) - 3)
+    k = torch.floor(v / step)
+    over = mag - (k + 0.5) * step * top
+    q = torch.where(top > 0, (k + ((over > 0) | ((over == 0) & (k % 2 == 1))).double()) * step, 0.0)
+    return (q * pad.sign()).reshape(M, -1)[:, :N]
+
+
 def rmsnorm_backward(S, dY, gamma, rstd, dS=None):
     M, N = S.shape
     u = u_of(S.dtype)

@@ -213,3 +213,21 @@ def test_differences():
         slack = 300 * ref.U_F32 * float((ref.d(b[grad]).abs() * v.abs()).sum() + 30)
         print(f"  {grad}: {got:.7f}, by differences {num:.7f}", flush=True)
         assert abs(got - num) <= slack + 1e-5
+
+
+@pytest.mark.parametrize("group", [128, 0])
+@pytest.mark.parametrize("M,N", [(40, 520), (1, 8), (130, 8192), (1100, 264), (300, 4104), (260, 8200), (260, 12296),
+                                 (260, 16384)])
+def test_codes_of_bf16_rows_are_exact(M, N, group):
+    """Halfway points between two codes are hit exactly by products of few bits: they go to the even code."""
+    import torch
+    print(f"case RMS norm, exact codes {M} x {N} group {group}", flush=True)
+    x = make(M, N, torch.bfloat16, seed=M + N)
+    x["X"][0] = 0
+    x["R"][0] = 0
+    x["X"][M // 2, :8] *= 2.0 ** 20
+    for residual in (True, False):
+        f = forward_q8(x, group, residual)
+        want = ref.q8_codes(f["S"] if residual else x["X"], x["gamma"], group)
+        off = int((ref.d(f["Q"].cpu().float()) != want).sum())
+        assert off == 0, f"{off} codes differ"

@@ -90,3 +90,33 @@ def test_packed_layout_round_trip(K, C, code):
     word, lane = (byte // 4) % 4, byte // 16
     k, c = torch.arange(K)[:, None].expand(K, C), torch.arange(C)[None, :].expand(K, C)
     assert torch.equal(16 * ct + lane % 16, c) and torch.equal(128 * kt + 32 * word + 8 * (lane // 16) + k % 8, k)
+
+
+def test_exact_codes():
+    """Against rational numbers, at halfway points too."""
+    from fractions import Fraction
+    g = torch.Generator().manual_seed(5)
+    S = torch.randn(6, 40, generator=g).to(torch.bfloat16)
+    S[2] = (torch.arange(40) + 1).to(torch.bfloat16) * 0.25       # 448 w / max: halves among them
+    S[3] = 0
+    S[4, 0] = 28.0                                                # quotients 16 s: every other one a halfway point
+    S[4, 1:] = (torch.arange(39) / 16 + 1).to(torch.bfloat16)
+    gamma = (1 + 0.3 * torch.randn(40, generator=g)).to(torch.bfloat16)
+    every = sorted({float(v) for v in torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()})
+    for gm in (gamma, torch.ones_like(gamma)):
+        got = ref.q8_codes(S, gm, 0)
+        ties = 0
+        for i in range(6):
+            w = [Fraction(float(a)) * Fraction(float(b)) for a, b in zip(S[i], gm)]
+            top = max(abs(v) for v in w)
+            for j, v in enumerate(w):
+                if top == 0:
+                    assert float(got[i, j]) == 0
+                    continue
+                q = abs(v) * 448 / top
+                near = min(abs(Fraction(e) - q) for e in every)
+                best = [k for k, e in enumerate(every) if abs(Fraction(e) - q) == near]
+                ties += len(best) > 1
+                want = every[best[0] if len(best) == 1 or best[0] % 2 == 0 else best[1]]
+                assert abs(float(got[i, j])) == want and (want == 0 or float(got[i, j]) * float(v) > 0)
+    assert ties > 10

@@ -6,6 +6,7 @@
 //              rstd = 1 / sqrt(sum_j s_j^2 / N + eps),  y_j = s_j rstd gamma_j
 //   8 bits:    per row and group of 128 columns (or the whole row), from the
 //              unrounded y: scale = max(max |y|, 2^-100) / 448, q_j = e4m3(y_j / scale)
+//              (of bf16 data exactly that code)
 //   backward:  z_j = s_j rstd,  t_j = dy_j gamma_j
 //              dx_j = rstd (t_j - z_j sum (t z) / N) + ds_j
 //              dgamma_j = sum_rows dy_j z_j
@@ -33,6 +34,16 @@ namespace {
 constexpr int kRmsThreads = 1024;          // largest workgroup
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleFloor = 0x1p-100f;   // of a group's largest magnitude: y / scale stays finite
+// Codes of bf16 data are those of the exact quotient 448 w / max |w|, ties to the even one.  With
+// products of 8-bit factors the quotient is often the halfway point between two codes (6664 of
+// 4096 x 4096 values in groups of 128), and the last bit of fp32 would pick one (the odd one 1592
+// times).  Let w = a 2^i, max |w| = b 2^j with integers a, b <= 255^2, and t = c 2^k a halfway
+// point, c odd below 32, 2^n <= t < 2^(n+1).  A quotient that is not t is off by at least
+// 2^n / (16 b), which is 8.06 steps of fp32 at t.  So 448 becomes 448 + 2^-14: that moves a quotient
+// up by 1.14 to 2.22 steps, while division and product move it by 1.47 at most.  One that is t
+// comes out 0 to 3 steps above it and loses those with its last two bits; one above t stays at
+// least 4 above, one below stays below.
+constexpr float kTieUp = kE4m3Max + 0x1p-14f;
 
 // Largest value over each row of 16 lanes, in every lane (rotations within the row).
 template <int kCtrl>
@@ -146,6 +157,12 @@ __global__ __launch_bounds__(kThreads, V == 4 && kThreads == 512 ? 4 : 1) void r
                 ln_store<kF32>(a.Y, row * N + column(v), y);
             }
         } else {
+            // rstd = p m, p a power of two: s p is exact, and y = w m with w = (s p) gamma, which of
+            // bf16 data is exact too.  y / scale = 448 w / max |w| needs no m, so codes do not hang
+            // on rstd's rounding.  (A NaN stays one.)
+            const uint32_t bits = __float_as_uint(rstd);
+            const float p = rstd != rstd ? rstd : __uint_as_float(bits & 0x7f800000u);
+            const float m = __uint_as_float((bits & 0x007fffffu) | 0x3f800000u);
             float top[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -154,8 +171,8 @@ __global__ __launch_bounds__(kThreads, V == 4 && kThreads == 512 ? 4 : 1) void r
                 top[v] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    // (columns past N hold zeros; 0 * rstd is 0, since rstd is finite)
-                    x[v][e] = x[v][e] * rstd * b[e];
+                    // (columns past N hold zeros; 0 * p is 0, since p is finite but in rows of NaN)
+                    x[v][e] = x[v][e] * p * b[e];
                     top[v] = fmaxf(top[v], fabsf(x[v][e]));
                 }
                 top[v] = row16_max(top[v]);
@@ -173,11 +190,15 @@ __global__ __launch_bounds__(kThreads, V == 4 && kThreads == 512 ? 4 : 1) void r
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!on || column(v) >= N) continue;
-                const float scale = fmaxf(top[v], kScaleFloor) / kE4m3Max;
-                const float inv = 1.0f / scale;
-                // |y| inv is at most 448 (1 + 2^-22), which rounds to 448
+                const float y = top[v] * m;
+                const float scale = fmaxf(y, kScaleFloor) / kE4m3Max;
+                const float inv = y >= kScaleFloor ? (kF32 ? kE4m3Max : kTieUp) / top[v] : m * (kE4m3Max / kScaleFloor);
+                // |w| inv is at most 448 (1 + 2^-22), which rounds to 448
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[v][e] *= inv;
+                for (int e = 0; e < 8; ++e) {
+                    x[v][e] *= inv;
+                    if constexpr (!kF32) x[v][e] = __uint_as_float(__float_as_uint(x[v][e]) & ~3u);
+                }
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + row * N + column(v)) = pack_e4m3x8(x[v]);
                 if (a.whole_row) {
                     if (column(v) == 0) a.scale[row] = scale;
