@@ -490,7 +490,13 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float
  * K, C multiples of 8 below 2^22, K * C below 2^31; M <= 16, and up to 4096 rows in the
  * moe_ forms, whose weights are read once per 16 or 32 rows of an expert.  A row with an
  * infinity, or whose integers' partial sums leave fp32 (|x| from about 1e36 on), gives
- * NaN or infinity.  With no rows nothing is done. */
+ * NaN or infinity.  With no rows nothing is done.
+ *
+ * Integers: a group's sum is sum x (16 + q) - (16 + z) sum x, both in fp32, and not
+ * sum x (q - z).  So an x that is much larger than the rest of its group leaves an error
+ * even where its code is the zero point: at most 2^-10 |x| s for zero points from 0 to 15 (about
+ * 2^-16 in practice: 0.07 s at |x| = 1e4, 13 s at 1e6), next to the |x| s / 2 that the rounding
+ * of its weight to 4 bits may have moved the sum by.  FFN_Q4_E2M1 has no such term. */
 typedef enum { FFN_Q4_INT = 0, FFN_Q4_E2M1 = 1 } ffn_q4_t;
 
 /* Bytes of the packed codes of one matrix (0 if the shape is invalid). */

@@ -277,3 +277,35 @@ def test_no_rows_and_repeated_calls():
         Z = empty(m, C)
         ffn.ffn_q4_matvec(X[:m], w[0], w[1], Z)
         assert torch.equal(Y[:m], Z)
+
+
+@pytest.mark.parametrize("big", [1e2, 1e4, 1e6, 1e8])
+@pytest.mark.parametrize("kind", KINDS[:4])
+def test_a_channel_much_larger_than_the_rest(kind, big):
+    """Its codes are the zero points, so that it adds nothing: what it leaves is within the stated 2^-10 |x| s."""
+    import torch
+    _, group, zero = kind
+    K, C, M, at = 520, 72, 5, 133
+    print(f"case 4-bit, a channel of {big:.0e} {kind}", flush=True)
+    g = torch.Generator().manual_seed(int(big))
+    G = -(-K // group)
+    q = torch.randint(0, 16, (K, C), generator=g).to(torch.uint8)
+    z = torch.randint(3, 13, (G, C), generator=g) if zero else torch.full((G, C), 8)
+    q[at] = z[at // group].to(torch.uint8)
+    s = (0.5 + torch.rand(G, C, generator=g)).to(torch.bfloat16)
+    Wq, sp, zp = ffn.ffn_q4_empty(K, C, group, zero)
+    ffn.ffn_q4_pack(q.cuda(), s.cuda(), Wq, sp, zero_in=z.to(torch.bfloat16).cuda() if zero else None, zero=zp)
+    X, Y = inputs(M, K, 3), empty(M, C)
+    X[:, at] = big * torch.tensor([1.0, -1.0, 0.5, 1.0, -0.5], device="cuda")
+    ffn.ffn_q4_matvec(X, Wq, sp, Y, zero=zp)
+    of = torch.arange(K) // group
+    w = (q.double() - z.double()[of]) * s.double()[of]
+    x = X.cpu().double()
+    y = x @ w
+    # of the other channels (|x| <= 5) the same, per group; then the sum of the groups and the rounding
+    top = s.double().amax(0)
+    off = (Y.cpu().double() - y).abs() - 2.0 ** -10 * (x[:, at:at + 1].abs() * s.double()[at // group] + 5 * G * top)
+    off -= 1.01 * ref.U_BF16 * y.abs() + 200 * ref.SUM * (x.abs() @ w.abs())
+    print(f"  beyond the bound by {float(off.max()):.3e}", flush=True)
+    assert bool((off <= 0).all())
+    ref.check({"Y": Y}, ref.q4_matvec(X, *cpu((Wq, sp, zp)), None, "none", C, "int4"), f"{kind} {big:.0e}")
