@@ -488,9 +488,10 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float
  * were in Y.  Offsets are read on the device and kept inside [0, rows].
  *
  * K, C multiples of 8 below 2^22, K * C below 2^31; M <= 16, and up to 4096 rows in the
- * moe_ forms, whose weights are read once per 16 or 32 rows of an expert.  A row with an
- * infinity, or whose integers' partial sums leave fp32 (|x| from about 1e36 on), gives
- * NaN or infinity.  With no rows nothing is done.
+ * moe_ forms, whose weights are read once per 16 or 32 rows of an expert.  A row with a
+ * NaN or an infinity, or whose integers' partial sums leave fp32 (|x| from about 1e36 on),
+ * has sums of NaN or infinity; ReLU keeps a NaN here, and makes 0 of a negative infinity.
+ * With no rows nothing is done.
  *
  * Integers: a group's sum is sum x (16 + q) - (16 + z) sum x, both in fp32, and not
  * sum x (q - z).  So an x that is much larger than the rest of its group leaves an error

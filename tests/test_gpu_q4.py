@@ -309,3 +309,28 @@ def test_a_channel_much_larger_than_the_rest(kind, big):
     print(f"  beyond the bound by {float(off.max()):.3e}", flush=True)
     assert bool((off <= 0).all())
     ref.check({"Y": Y}, ref.q4_matvec(X, *cpu((Wq, sp, zp)), None, "none", C, "int4"), f"{kind} {big:.0e}")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh"])
+@pytest.mark.parametrize("kind", [KINDS[1], KINDS[2], KINDS[4]])
+def test_bad_rows_are_seen_through_the_activation(kind, act):
+    """NaN, an infinity and sums past fp32 give NaN or infinity; of e2m1, ReLU makes 0 of a negative infinity."""
+    import torch
+    K, C, E = 264, 40, 2
+    w = weight(K, C, kind, 3, E)
+    X, Y, Z = inputs(9, K, 1), empty(9, C), empty(9, C)
+    off = torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda")
+    ffn.moe_q4_matvec(X, off, w[0], w[1], Y, zero=w[2], act=act, code=kind[0])
+    X[2, 5], X[5, 7], X[8, 263], X[6, 200:203] = float("nan"), float("-inf"), float("inf"), 3e38
+    ffn.moe_q4_matvec(X, off, w[0], w[1], Z, zero=w[2], act=act, code=kind[0])
+    keep = [0, 1, 3, 4, 7]
+    assert torch.equal(Y[keep], Z[keep])
+    assert bool(torch.isnan(Z[2].float()).all())
+    if kind[0] == "int4":
+        assert not bool(torch.isfinite(Z[[5, 6, 8]].float()).any())
+    elif act == "none":
+        assert not bool(torch.isfinite(Z[[5, 8]].float()).any())
+    elif act == "relu":      # a sum of either sign, or NaN where a code is 0
+        z, q = Z[[5, 8]].float(), ref.q4_codes(w[0][1], K, C, "e2m1")
+        assert bool(((z == 0) | ~torch.isfinite(z)).all())
+        assert bool(torch.isnan(z.cpu()[0][(q[7] & 7) == 0]).all())

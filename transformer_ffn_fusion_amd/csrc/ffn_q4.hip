@@ -284,7 +284,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_kernel(Q4Args a) {
                 y = silu(v[0]) * v[1];
             } else {
                 if (a.bias) v[0] += bf16_to_f32(a.bias[e * a.b_stride + col]);
-                y = apply_act(a.act, v[0]);
+                // (a NaN stays one: a bad row must not come out as zeros)
+                y = a.act == ACT_RELU ? (v[0] <= 0.f ? 0.f : v[0]) : apply_act(a.act, v[0]);
             }
             a.Y[(int64_t)(r0 + m) * a.C + col] = __builtin_bit_cast(uint16_t, (__bf16)y);
         }
