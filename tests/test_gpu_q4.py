@@ -334,3 +334,90 @@ def test_bad_rows_are_seen_through_the_activation(kind, act):
         z, q = Z[[5, 8]].float(), ref.q4_codes(w[0][1], K, C, "e2m1")
         assert bool(((z == 0) | ~torch.isfinite(z)).all())
         assert bool(torch.isnan(z.cpu()[0][(q[7] & 7) == 0]).all())
+
+
+def check_tiles(got, want, w, X, tiles, C, what):
+    """Columns of some column tiles alone: ``want(X, *weights, columns)`` of the weights cut to them."""
+    import torch
+    at = torch.tensor(tiles)
+    col = (16 * at[:, None] + torch.arange(16)).reshape(-1)
+    real = col < C
+    name, (y, bound) = next(iter(want(X, *[[None if t is None else t.cpu()[at] for t in v] for v in w], 16 * len(tiles)).items()))
+    ref.check({name: got[:, col[real].cuda()]}, {name: (y[:, real], bound[:, real])}, what)
+
+
+def some_tiles(C):
+    """The first and last column tiles, and some between."""
+    n = -(-C // 16)
+    return sorted({*range(min(n, 9)), *range(max(0, n - 9), n), *range(0, n, max(1, n // 12))})
+
+
+def matvec(code, act="none"):
+    return lambda X, w, C: ref.q4_matvec(X, *w, None, act, C, code)
+
+
+def swiglu(code):
+    return lambda X, wg, wu, C: ref.q4_swiglu(X, *wg, *wu, C, code)
+
+
+@pytest.mark.parametrize("kind", KINDS[:4] + [("int4", 64, False), ("int4", 32, True)])
+@pytest.mark.parametrize("K,C", [(2696, 25608)])
+def test_four_column_tiles_over_many_k_tiles(K, C, kind):
+    """22 k tiles between four waves: a wave's loads and products turn over five times."""
+    print(f"case 4-bit, four column tiles {K} x {C} {kind}", flush=True)
+    w = weight(K, C, kind, seed=K + C)
+    for M in (1, 6, 16):
+        X, Y = inputs(M, K, M), empty(M, C)
+        ffn.ffn_q4_matvec(X, w[0], w[1], Y, zero=w[2], code=kind[0])
+        assert not bool(Y.isnan().any())
+        check_tiles(Y, matvec(kind[0]), [w], X, some_tiles(C), C, f"{kind} {M} rows")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("K", [1032, 4104])
+def test_around_the_rules_of_tiles_and_waves(K, kind):
+    """511, 512 and 513 column tiles: one a wave, two in workgroups of eight waves, two in workgroups of four;
+    the gated pair at 256 and 257: eight waves, four.  9 and 33 k tiles."""
+    print(f"case 4-bit, around the rules, K = {K} {kind}", flush=True)
+    for C in (8176, 8192, 8200):
+        w = weight(K, C, kind, seed=K + C)
+        for M in (1, 6, 16):
+            X, Y = inputs(M, K, M), empty(M, C)
+            ffn.ffn_q4_matvec(X, w[0], w[1], Y, zero=w[2], code=kind[0])
+            assert not bool(Y.isnan().any())
+            check_tiles(Y, matvec(kind[0]), [w], X, some_tiles(C), C, f"{C} columns, {M} rows")
+    for C in (4096, 4104):
+        wg, wu = weight(K, C, kind, 1), weight(K, C, kind, 2)
+        for M in (1, 6, 16):
+            X, H = inputs(M, K, M), empty(M, C)
+            ffn.ffn_q4_swiglu(X, wg[0], wg[1], wu[0], wu[1], H, zero_g=wg[2], zero_u=wu[2], code=kind[0])
+            assert not bool(H.isnan().any())
+            check_tiles(H, swiglu(kind[0]), [wg, wu], X, some_tiles(C), C, f"pair of {C} columns, {M} rows")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("counts", [[32, 4, 0, 64, 9], [3, 0, 16, 1, 9]])
+@pytest.mark.parametrize("shape", [(2696, 72), (5256, 72), (2696, 4104)])
+def test_experts_over_many_k_tiles(shape, counts, kind):
+    """Lists of up to 32 and of up to 16 rows at once, 22 k tiles between eight and four waves, 42 between eight."""
+    import torch
+    K, C = shape
+    code, E = kind[0], len(counts)
+    print(f"case 4-bit experts over many k tiles {shape} {counts} {kind}", flush=True)
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    n = int(off[-1])
+    X, Y, H = inputs(n + 3, K, 4), empty(n + 3, C), empty(n + 3, C)     # three rows of no expert
+    wg, wu = weight(K, C, kind, 1, E), weight(K, C, kind, 2, E)
+    Y.fill_(7.0)
+    H.fill_(7.0)
+    ffn.moe_q4_matvec(X, off, wg[0], wg[1], Y, zero=wg[2], code=code)
+    ffn.moe_q4_swiglu(X, off, wg[0], wg[1], wu[0], wu[1], H, zero_g=wg[2], zero_u=wu[2], code=code)
+    assert not bool(Y.isnan().any()) and not bool(H.isnan().any())
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            continue
+        g, u = ([None if t is None else t[e] for t in w] for w in (wg, wu))
+        check_tiles(Y[lo:hi], matvec(code), [g], X[lo:hi], some_tiles(C), C, f"expert {e}")
+        check_tiles(H[lo:hi], swiglu(code), [g, u], X[lo:hi], some_tiles(C), C, f"expert {e}")
+    assert bool((Y[n:] == 7.0).all()) and bool((H[n:] == 7.0).all())
