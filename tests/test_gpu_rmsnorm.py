@@ -231,3 +231,54 @@ def test_codes_of_bf16_rows_are_exact(M, N, group):
         want = ref.q8_codes(f["S"] if residual else x["X"], x["gamma"], group)
         off = int((ref.d(f["Q"].cpu().float()) != want).sum())
         assert off == 0, f"{off} codes differ"
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("M,N", [(4100, 2056), (6200, 4104), (4100, 8200), (4100, 12296), (16500, 264), (8300, 520),
+                                 (12400, 1032)])
+def test_workgroups_that_walk_several_rows(M, N, dtype):
+    """More rows than the grid takes at once (2048 workgroups), three turns and more: the next row's loads in
+    flight, the sums' slots in turn, outputs over inputs.  Every row is bitwise that of a call whose workgroups
+    take one turn; some rows of each turn are checked in fp64."""
+    import torch
+    dt = getattr(torch, dtype)
+    print(f"case RMS norm, several turns {M} x {N} {dtype}", flush=True)
+    x = make(M, N, dt, seed=M + N)
+    x["X"][M - 3] = 0
+    x["R"][M - 3] = 0
+    rows = torch.cat([torch.arange(0, M, 211), torch.arange(2040, M, 2048), torch.arange(M - 4, M)]).cuda()
+
+    def of(out, i):
+        return {k: v[i] for k, v in out.items()}
+
+    for residual in (True, False):
+        S = None
+        for call in (forward, lambda y, r: forward_q8(y, 128, r), lambda y, r: forward_q8(y, 0, r)):
+            f = call(x, residual)
+            for lo in range(0, M, 1024):
+                lo = min(lo, M - 1024)
+                part = slice(lo, lo + 1024)
+                one = call({**{k: x[k][part] for k in ("X", "R")}, "gamma": x["gamma"]}, residual)
+                for k in f:
+                    a, b = (v if v.element_size() > 1 else v.view(torch.uint8) for v in (f[k][part], one[k]))
+                    assert torch.equal(a, b), (k, lo)
+            S = f["S"] if residual else x["X"]
+            if residual:
+                assert torch.equal(S, (x["X"].float() + x["R"].float()).to(dt))
+            want = ref.rmsnorm_forward(S[rows], x["gamma"], 1e-5)
+            if "Y" in f:
+                ref.check(of({k: f[k] for k in want}, rows), want, f"{M} x {N}")
+                plain = f
+            else:
+                group = 0 if f["scale"].shape[1] == 1 and N > 128 else 128
+                ref.check_q8(f["Q"][rows], f["scale"][rows], S[rows], x["gamma"], 1e-5, group, f"{M} x {N} {group}")
+                if dt == torch.bfloat16:
+                    assert torch.equal(ref.d(f["Q"][rows].cpu().float()), ref.q8_codes(S[rows], x["gamma"], group))
+        if residual:
+            for name in ("X", "R"):
+                y = x[name].clone()
+                again = forward({**x, name: y}, S=y)
+                assert all(torch.equal(again[k], plain[k]) for k in plain), name
+        else:
+            y = x["X"].clone()
+            assert torch.equal(forward({**x, "X": y}, residual=False, Y=y)["Y"], plain["Y"])
