@@ -395,13 +395,24 @@ int forward_threads(int64_t M, int64_t N, bool f32) {
     return N <= 16 * kLnCols ? 256 : N <= 24 * kLnCols ? kRmsThreads : 512;
 }
 
+// The steps a lane that forward_threads and ln_shape give: one or two of sixteen waves; of bf16 also
+// up to four of four waves and four of eight; of fp32 one of four or eight.
 template <bool kF32, bool kQ8, int kThreads>
-void start_forward(const LnShape& s, dim3 grid, hipStream_t stream, const RmsArgs& a) {
-    const dim3 block(64 * s.W * s.G);
-    if (s.V == 1) hipLaunchKernelGGL((rms_forward_kernel<kF32, kQ8, 1, kThreads>), grid, block, 0, stream, a);
-    else if (s.V == 2) hipLaunchKernelGGL((rms_forward_kernel<kF32, kQ8, 2, kThreads>), grid, block, 0, stream, a);
-    else if constexpr (!kF32 && kThreads < kRmsThreads)
-        hipLaunchKernelGGL((rms_forward_kernel<kF32, kQ8, 4, kThreads>), grid, block, 0, stream, a);
+hipError_t start_forward(const LnShape& s, dim3 grid, hipStream_t stream, const RmsArgs& a) {
+    constexpr bool kOne = kF32 || kThreads != 512;
+    constexpr bool kTwo = kThreads == kRmsThreads || (!kF32 && kThreads == 256);
+    constexpr bool kFour = !kF32 && kThreads < kRmsThreads;
+    auto go = [&](auto v) {
+        hipLaunchKernelGGL((rms_forward_kernel<kF32, kQ8, v.value, kThreads>), grid, dim3(64 * s.W * s.G), 0, stream, a);
+        return hipGetLastError();
+    };
+    if constexpr (kOne)
+        if (s.V == 1) return go(std::integral_constant<int, 1>());
+    if constexpr (kTwo)
+        if (s.V == 2) return go(std::integral_constant<int, 2>());
+    if constexpr (kFour)
+        if (s.V == 4) return go(std::integral_constant<int, 4>());
+    return hipErrorInvalidValue;    // no rule gives this shape
 }
 
 }  // namespace
@@ -430,20 +441,14 @@ hipError_t launch_rmsnorm_forward(const RmsForwardIO& io, hipStream_t stream) {
     a.whole_row = io.group == 0;
     a.groups = io.group ? (int)((N + 127) / 128) : 1;
     a.eps = io.eps;
-    auto go = [&](auto f, auto q, auto t) { start_forward<f.value, q.value, t.value>(s, grid, stream, a); };
+    auto go = [&](auto f, auto q, auto t) { return start_forward<f.value, q.value, t.value>(s, grid, stream, a); };
     auto with = [&](auto f, auto q) {
-        if (threads == 256) go(f, q, std::integral_constant<int, 256>());
-        else if (threads == 512) go(f, q, std::integral_constant<int, 512>());
-        else go(f, q, std::integral_constant<int, kRmsThreads>());
+        if (threads == 256) return go(f, q, std::integral_constant<int, 256>());
+        if (threads == 512) return go(f, q, std::integral_constant<int, 512>());
+        return go(f, q, std::integral_constant<int, kRmsThreads>());
     };
-    if (io.q8) {
-        if (io.f32) with(std::true_type(), std::true_type());
-        else with(std::false_type(), std::true_type());
-    } else {
-        if (io.f32) with(std::true_type(), std::false_type());
-        else with(std::false_type(), std::false_type());
-    }
-    return hipGetLastError();
+    if (io.q8) return io.f32 ? with(std::true_type(), std::true_type()) : with(std::false_type(), std::true_type());
+    return io.f32 ? with(std::true_type(), std::false_type()) : with(std::false_type(), std::false_type());
 }
 
 hipError_t launch_rmsnorm_backward(const void* S, const void* dY, const void* dS, const void* gamma,

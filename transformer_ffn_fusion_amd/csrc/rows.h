@@ -75,7 +75,7 @@ inline LnShape ln_shape(int64_t N, int max_threads) {
     s.V = waves <= most ? 1 : waves <= 2 * most ? 2 : 4;
     s.W = (waves + s.V - 1) / s.V;
     s.G = most / s.W;
-    return s;   // V <= 2 of sixteen waves, 4 of four: N <= 16384, 8192
+    return s;   // N up to 4 x 512 columns a wave (past that G is 0), and up to the V that the caller's kernel has
 }
 
 }  // namespace ffn
