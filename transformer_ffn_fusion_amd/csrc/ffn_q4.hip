@@ -14,14 +14,19 @@
 //    upper mantissa bits of 16: 16 + q) or one conversion for two e2m1 floats; both are
 //    exact.  The group's sum x (16 + q) is corrected by (16 + z) sum x, which one more
 //    matrix instruction against ones gives in the same registers, and scaled in fp32.
+//    (An x far above its group's others leaves a rounding there, 2^-16 |x| s, that the direct
+//    form does not.  That form, q - z by fp16 mantissas and one mixed fma a code, takes 17
+//    instructions per 8 codes instead of 8 and 23 to 50 % longer: the pair of 8192 x 3584
+//    12.8 us instead of 9.3, 8192 x 28672 40.6 instead of 29.6.)
 //  * The waves of a workgroup share its columns and split K; their sums are joined in
 //    LDS in ascending order, so results do not depend on timing, and one launch is all.
-// Measured (kernel; 16 tokens unless said): pair of 8192 x 3584 9.5 us (30.3 MB; without its
-// loads of X 8.5), experts' pairs of 8 x 4096 x 2048 13.5 us (of 69 MB the 58 of experts that
-// have rows), 8192 x 28672 30 us (118 MB, one token 25), 4096 x 4096 with zero points, one
-// token, 4.2 us, of which about 3 are a kernel's way in and out.
-// Three or four stages in flight instead of two: no faster or slower (16 x 4096 x 4096: 5.0
-// us, with three 6.4), sixteen waves likewise (16 x 14336 x 4096: 10.9, 12.1).
+// Measured (replayed in a graph; 16 tokens unless said; cards differ by up to 5 %): pair of
+// 8192 x 3584 9.1 to 9.6 us (30.3 MB; without its loads of X 1 us less), experts' pairs of
+// 8 x 4096 x 2048 13.6 us (of 69 MB the 52 to 69 of the six to eight experts that have rows),
+// 8192 x 28672 29 to 30 us (121 MB; one token 25.4), 4096 x 4096 with zero points, one token, 4.2 us,
+// of which about 3 are a kernel's way in and out.
+// Three stages in flight instead of two: slower (16 x 4096 x 4096: 5.0 us, 6.3; 16 x 14336 x
+// 4096: 11.0, 12.0), and so are sixteen waves.
 #include <type_traits>
 
 #include "ffn_device.h"
@@ -308,7 +313,8 @@ __device__ __forceinline__ uint32_t to_e2m1(float v) {
     return q | (v < 0.f && q ? 8u : 0u);
 }
 
-// 128 k x 64 columns per workgroup: through LDS, so that W is read in whole lines.
+// 128 k x 64 columns per workgroup: through LDS, so that W is read in whole lines.  A weight passes
+// here once in its life, so it was left at this: 4096 x 14336 bf16 145 us, fp32 147 (floors 27, 49).
 template <bool kF32>
 __global__ __launch_bounds__(256) void q4_quantize_kernel(const void* W, uint8_t* Wq, uint16_t* scale,
                                                           uint16_t* zero, int64_t K, int64_t C, int kt_all,
@@ -369,7 +375,8 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const void* W, uint8_t
     }
 }
 
-// One word per thread; the first threads of a tile also place its scales and zeros.
+// One word per thread; the first threads of a tile also place its scales and zeros.  Eight loads of
+// a byte each, a row of codes apart (4096 x 14336: 68 us, floor 17).
 __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* codes, const uint16_t* scale_in,
                                                       const uint16_t* zero_in, uint8_t* Wq, uint16_t* scale,
                                                       uint16_t* zero, int64_t K, int64_t C, int kt_all, int code,
@@ -395,21 +402,27 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* codes, cons
     }
 }
 
-// Column tiles per wave, waves per workgroup, rows at once.  Two tiles share a wave's rows of X, which
-// for 16 rows are more bytes than a tile's codes, and halve the workgroups: taken where at
-// least one workgroup per CU is left (16 x 8192 x 8192: 12.6 -> 10.8 us; 16 x 4096 x 4096, 128
-// workgroups: 5.3 -> 6.4 us; the gated pair shares them already).  Four of integers, where their
+// Column tiles per wave, waves per workgroup, rows at once.  (Both sides of each rule on one card, in
+// turn, replayed in graphs; groups of 128 without zero points unless said.)
+//
+// Two tiles share a wave's rows of X, which for 16 rows are more bytes than a tile's codes, and
+// halve the workgroups: taken where at least one workgroup per CU is left (16 x 8192 x 8192:
+// 10.4 us, with one tile 11.8; 16 x 4096 x 14336: 9.9, 11.9; but 16 x 4096 x 4096, 128 workgroups
+// with two: 6.0, with one 5.0; the gated pair shares them already).  Four of integers, where their
 // fewer workgroups leave no CU with more tiles than two would (16 x 8192 x 28672, eight a CU
-// either way: 34 -> 30 us; 16 x 4096 x 22016, eight instead of six: 13.0 -> 14.8; e2m1, whose
-// rows need no sums: no faster).  Up to one workgroup per CU takes eight waves (16 rows, pair of
-// 8192 x 3584, 224 workgroups: 10.3 us, with four 11.6).  More of them take four: of eight, whose
+// either way: 30.4 us, with two 33.8; 16 x 4096 x 22016, eight instead of six: 14.8, 13.5; e2m1,
+// whose rows need no sums, was no faster).
+//
+// Up to one workgroup per CU takes eight waves (16 rows, pair of 8192 x 3584, 224 workgroups:
+// 9.6 us, with four 10.9; 16 x 14336 x 4096: 10.7, 13.0).  More of them take four: of eight, whose
 // registers fill half a CU or more, the second waits for the first (16 x 4096 x 14336, 448
-// workgroups: 11.8 -> 9.8 us; pair of 4096 x 8192 with zero points, 512: 13.3 -> 11.4).  Experts
-// without rows have workgroups that end at once: those are not counted.
+// workgroups: 9.9 us, with eight 11.7; pair of 4096 x 8192 with zero points, 512: 10.3, 10.8).
+// Experts without rows have workgroups that end at once: those are not counted.
 //
 // Rows at once: 32 where lists are longer than ten rows on average, so that many pass 16 (pair of
-// 8 x 4096 x 2048: 192 rows 32 -> 27 us, 128 23.1 -> 20.2, 96 19.1 -> 17.8; 60 x 2048 x 1408,
-// 512 rows, 8.5 a list: 41.2 -> 42.9, for half again as many registers).
+// 8 x 4096 x 2048: 512 rows 57 us, with 16 at once 69; 192 rows 27.2, 32.1; 96 rows 18.4, 19.7; product of
+// 8 x 14336 x 4096, 512 rows: 183, 237; but 60 x 2048 x 1408, 512 rows, 8.5 a list: 44.6 with 32,
+// 43.7 with 16, for half again as many registers).
 struct Q4Shape {
     int tiles, waves, blocks;
 };

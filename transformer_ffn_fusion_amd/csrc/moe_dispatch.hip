@@ -410,9 +410,12 @@ __device__ __forceinline__ float part_sum(float v, int W) {
 // dY is read once: every piece is multiplied into the k dot products and written,
 // weighted, to the k rows.  The dots are fp32 lane sums over a lane's pieces, then over
 // the wave, then over the W waves, in a fixed order.  Rows of up to 256 columns (kShort)
-// take as many lanes as they have pieces, several tokens to a wave (28000 x 104 fp32, top
-// 7, three quarters dropped: 16 us, a wave each 26).  A token without entries is not read
-// (8000 x 5456 fp32, top 4, three quarters dropped: 110 -> 101 us).
+// take as many lanes as they have pieces, several tokens to a wave (28133 x 104 fp32, top
+// 7, three quarters dropped: 16 us, a wave each 26).  That is 56 MB, 35 read and 21 written, at
+// 3.5 TB/s: a lane has one piece, so its loads of positions, of rows and its stores are one chain
+// with no other piece behind it (none dropped: 175 MB in 53 us, 3.3 TB/s; rows of whole lines,
+// 128 columns, 3.8 and 4.0).  A token without entries is not read (8000 x 5456 fp32, top 4, three
+// quarters dropped: 110 -> 100 us).
 template <bool kF32, int K, bool kShort>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackwardArgs a) {
     __shared__ float s_part[kThreads / 64][K];

@@ -16,7 +16,7 @@
 // many rows with the next rows' loads in flight.  A group of 128 columns is one
 // 16-lane row of a wave, so its largest magnitude needs neither LDS nor a barrier.
 // Measured, bf16 with a residual: 8192 x 8192 forward 98 us, backward 105 us (537 MB each,
-// 5.1 to 5.5 TB/s, the rate of a large copy); 4096 x 4096 into 8 bits 25 us (117 MB).
+// 5.1 to 5.5 TB/s, the rate of a large copy); 4096 x 4096 into 8 bits 25.4 us (117 MB).
 // Stores that pass the caches by (non-temporal) make a single call faster (8 bits 20 us,
 // forward of 4096 x 4096 27 -> 22 us) and the call that reads the rows slower by more: a
 // chain of norm, dispatch and combine of 16384 x 4096 takes 374 us with them, 362 without.
@@ -214,7 +214,8 @@ __global__ __launch_bounds__(kThreads, V == 4 && kThreads == 512 ? 4 : 1) void r
 // A workgroup walks rows blockIdx.x * G + g, + gridDim.x * G, ...; a lane keeps its
 // columns' dgamma sums in registers over all of them: one partial row per workgroup
 // instead of a second pass over s and dy.  part: [workgroup][N].  The loads run kAhead
-// rows ahead; two steps a lane of fp32 (N > 8192) leave no registers for that.
+// rows ahead; two steps a lane of fp32 (N > 8192) leave no registers for that, and of bf16 four
+// registers too few (20 bytes a lane are spilled; 4096 x 12288 with dS 82 us, 4096 x 16384 110: 4.9 TB/s).
 template <bool kF32, int V>
 __global__ __launch_bounds__(kRmsThreads) void rms_backward_kernel(
     const void* S, const void* dY, const void* dS, const void* __restrict__ gamma,
@@ -382,12 +383,13 @@ int64_t rms_backward_blocks(int64_t M, int64_t N) {
 
 // Largest workgroup of the forward.  Few rows: one to a workgroup, of up to sixteen waves, one step
 // a lane as far as they reach: one round trip (16 x 4096 bf16: 2.9 us; two to a workgroup 3.35;
-// 520 x 4096: 5.6, by the shapes of many rows 5.0).  Many rows of fp32: as few steps a lane (8192
-// columns: 96 us, with four waves of four steps 100; 5824: 98, 105).  Of bf16: four waves, several
-// workgroups per CU (8192 columns into 8 bits: 42 us, with sixteen waves 50).  Past 8192 columns two
-// steps a lane, while two workgroups of them fit a CU (12288 bf16 into 8 bits: 45 us, with eight
-// waves of four steps 69); past 12288 one would be alone, and bf16 takes four steps in eight
-// waves, within 128 registers (16384 bf16: 50 us, with sixteen waves 54; into 8 bits 53, 56).
+// 520 x 4096: 5.6, by the shapes of many rows 5.0).  Many rows of fp32: as few steps a lane
+// (3906 x 8192 with a residual: 96 us, with four waves of four steps 100; 5494 x 5824: 97.5, 105).
+// Of bf16: four waves, several workgroups per CU (7812 x 8192 into 8 bits: 42 us, with sixteen waves
+// 50).  Past 8192 columns two steps a lane, while two workgroups of them fit a CU (5208 x 12288 into
+// 8 bits: 45 us, with eight waves of four steps 69); past 12288 one would be alone, and bf16 takes
+// four steps in eight waves, held to 128 registers (3906 x 16384: 49 us, with sixteen waves 54;
+// into 8 bits 54, 56: there 8 registers are spilled, 36 bytes a lane).
 constexpr int64_t kManyRows = 256;
 int forward_threads(int64_t M, int64_t N, bool f32) {
     if (M < kManyRows) return kRmsThreads;
