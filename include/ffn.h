@@ -435,7 +435,9 @@ int moe_ffn_forward_router(const void* X, const void* Wr, const float* br, int64
  *
  * Routing's gradient: with w the softmax over a token's k chosen logits,
  * dlogits[t][topk_ids[t][s]] = w_s (dw_s - sum_j w_j dw_j), all else 0.  Takes the ids that
- * the router gave: an id outside [0, E) is in the sum, but has no logit.
+ * the router gave: an id outside [0, E) is in the sum, but has no logit.  Where entries are
+ * dropped after the router (their ids set to -1 for the dispatch), keep the router's own ids for this
+ * call: a dropped choice still stands in the softmax, with dw = 0, and its logit has a gradient.
  *
  * Data in `dtype` (FFN_BF16 or FFN_F32 but for dispatch), row-major; 1 <= E <= 256,
  * 1 <= k <= 8, M*k below 2^31.  Y may be R itself and dYs may be Ys.  With M == 0 the

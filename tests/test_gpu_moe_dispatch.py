@@ -281,3 +281,39 @@ def test_rows_past_32_bit_offsets_and_more_tokens_than_a_launch():
     assert torch.equal(Xs[p][kept], want[kept])
     ref.check({"dw": dw[at]}, ref.combine_backward(X[at], X[at], torch.where(kept, torch.arange(len(at), device="cuda"), -1)[:, None],
                                                    w[at])[0], "combine's gradients")
+
+
+@pytest.mark.parametrize("M,N,E,k,dtype", [(150, 72, 9, 3, "bfloat16"), (61, 520, 24, 8, "float32")])
+def test_routing_gradient_where_entries_are_dropped_after_the_router(M, N, E, k, dtype):
+    """The router's own ids, and the dispatch's with dropped entries at -1: the logits' gradient is that of the
+    combined rows by differentiation, dropped choices (which still stand in the softmax) among them."""
+    import torch
+    dt = getattr(torch, dtype)
+    print(f"case routing gradient with dropped entries {M} {E} {k} {dtype}", flush=True)
+    g = torch.Generator().manual_seed(M)
+    logits = torch.randn(M, E, generator=g).cuda()
+    ids = torch.empty(M, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(M, k, device="cuda")
+    ffn.moe_route(logits, k, topk_ids=ids, topk_w=w)
+    kept = torch.where(torch.rand(M, k, generator=g).cuda() < 0.3, -1, ids)
+    kept[0] = -1
+    o = dispatch(rows(M, N, dt, 1), kept, E)
+    Ys, dY = rows(M * k, N, dt, 2), rows(M, N, dt, 3)
+    dw, dYs, dl = torch.empty_like(w), torch.empty_like(Ys), torch.full((M, E), float("nan"), device="cuda")
+    ffn.moe_combine_backward(dY, Ys, o["pos"], w, dYs, dw)
+    ffn.moe_route_backward(ids, w, dw, dl)
+    x = ref.d(logits).requires_grad_()
+    v, on = ref._taken(Ys, o["pos"])
+    p = torch.softmax(x.gather(1, ids.cpu().long()), 1)
+    ((v * (p * on)[:, :, None]).sum(1) * ref.d(dY)).sum().backward()
+    # the fp32 weights are within e of the softmax's, and the gradient is linear in products of two of them
+    want, off = ref.combine_backward(dY, Ys, o["pos"], w)[0]["dw"]
+    e = float((ref.d(w) / p.detach() - 1).abs().max())
+    assert e < 1e-5
+    far = ref.route_backward(ids, w, want, E)["dlogits"][1]
+    wd = ref.d(w)
+    far.scatter_add_(1, ids.cpu().long(), wd * (off + (wd * off).sum(1, keepdim=True)))
+    far.scatter_add_(1, ids.cpu().long(), 3 * e * wd * (want.abs() + (wd * want.abs()).sum(1, keepdim=True)))
+    ref.check({"dlogits": dl}, {"dlogits": (x.grad, 1.01 * far + 1e-30)}, f"{M} {E} {k}")
+    gone = (kept < 0).cpu() & (wd > 0.01)
+    assert bool(gone[1:].any()) and bool((x.grad.gather(1, ids.cpu().long())[1:][gone[1:]] != 0).any())

@@ -794,7 +794,9 @@ def moe_combine_backward(dY, Ys, positions, topk_w, dYs, dw, stream=None):
 
 
 def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None):
-    """The gradient of the gate's softmax over the chosen logits: ``dlogits`` (M x E, fp32), written in place."""
+    """The gradient of the gate's softmax over the chosen logits: ``dlogits`` (M x E, fp32), written in place.
+    ``topk_ids`` are the router's own, also where a copy with dropped entries at -1 went into ``moe_dispatch``:
+    a dropped choice still stands in the softmax, and its logit has a gradient."""
     import torch
     M, E = _dims(dlogits, "dlogits", 2)
     k = _dims(topk_ids, "topk_ids", 2)[1]

@@ -22,7 +22,7 @@
 //    LDS in ascending order, so results do not depend on timing, and one launch is all.
 // Measured (replayed in a graph; 16 tokens unless said; cards differ by up to 5 %): pair of
 // 8192 x 3584 9.1 to 9.6 us (30.3 MB; without its loads of X 1 us less), experts' pairs of
-// 8 x 4096 x 2048 13.6 us (of 69 MB the 52 to 69 of the six to eight experts that have rows),
+// 8 x 4096 x 2048 13.6 us (8.65 MB an expert; inputs of which six, eight and six have rows),
 // 8192 x 28672 29 to 30 us (121 MB; one token 25.4), 4096 x 4096 with zero points, one token, 4.2 us,
 // of which about 3 are a kernel's way in and out.
 // Three stages in flight instead of two: slower (16 x 4096 x 4096: 5.0 us, 6.3; 16 x 14336 x
