@@ -282,3 +282,34 @@ def test_workgroups_that_walk_several_rows(M, N, dtype):
         else:
             y = x["X"].clone()
             assert torch.equal(forward({**x, "X": y}, residual=False, Y=y)["Y"], plain["Y"])
+
+
+def test_rows_past_32_bit_offsets():
+    """4.3 x 10^9 values: rows at both ends and where 2^31 and 2^32 values or bytes end."""
+    import torch
+    M, N = (1 << 18) + 77, 16384
+    print(f"case RMS norm {M} x {N}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, M, 1 << 16):
+        part = X[lo:lo + (1 << 16)]
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda", dtype=torch.bfloat16))
+    gamma = (1 + 0.3 * torch.randn(N, generator=g, device="cuda")).to(torch.bfloat16)
+    at = torch.cat([torch.arange(max(0, b - 3), b + 3) for b in (0, 1 << 16, 1 << 17, 1 << 18)] + [torch.arange(M - 4, M)]).unique().cuda()
+    S, rstd = torch.zeros_like(X), torch.zeros(M, device="cuda")
+    Q, scale = torch.zeros(M, N, dtype=torch.float8_e4m3fn, device="cuda"), torch.zeros(M, 128, device="cuda")
+    ffn.ffn_rmsnorm_q8_forward(X, gamma, Q, scale, R=X, S=S, rstd=rstd)
+    assert torch.equal(S[at], X[at] + X[at])
+    ref.check_q8(Q[at], scale[at], S[at], gamma, 1e-5, 128, "8 bits")
+    assert torch.equal(ref.d(Q[at].cpu().float()), ref.q8_codes(S[at], gamma, 128))
+    del Q
+    Y = torch.zeros_like(X)
+    ffn.ffn_rmsnorm_forward(S, gamma, Y)
+    ref.check({"Y": Y[at]}, {"Y": ref.rmsnorm_forward(S[at], gamma, 1e-5)["Y"]}, "forward")
+    dX, dgamma = torch.zeros_like(X), torch.empty(N, device="cuda")
+    ffn.ffn_rmsnorm_backward(S, Y, gamma, rstd, dX, dgamma, dS=X)
+    ref.check({"dX": dX[at]}, {"dX": ref.rmsnorm_backward(S[at], Y[at], gamma, rstd[at], X[at])["dX"]}, "backward")
+    total = sum((Y[lo:lo + 4096].double() * S[lo:lo + 4096].double() * rstd[lo:lo + 4096, None].double()).sum(0) for lo in range(0, M, 4096))
+    mags = sum((Y[lo:lo + 4096].double() * S[lo:lo + 4096].double()).abs().mul_(rstd[lo:lo + 4096, None].double()).sum(0) for lo in range(0, M, 4096))
+    # a workgroup's 1025 rows one after the other, then 256 partial sums; a product's two roundings
+    ref.check({"dgamma": dgamma}, {"dgamma": (total.cpu(), (1025 + 256 + 4) * ref.SUM * mags.cpu())}, "dgamma")
