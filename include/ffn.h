@@ -296,7 +296,7 @@ int ffn_layernorm_backward(const void* X, const void* dY, const void* gamma, con
  * columns: scale = max(max |y|, 2^-100) / 448.  group is 128 (scale: M x
  * ceil(N / 128)) or 0 for whole rows (scale: M).  Of FFN_BF16 data every code is
  * that of the exact quotient, 448 s gamma / max |s gamma|, where max |y| is above
- * 2^-100 and s rstd above 2^-126; of FFN_F32 data a quotient within 2^-22 of the
+ * 2^-100 and s rstd above 2^-125; of FFN_F32 data a quotient within 2^-22 of the
  * halfway point between two codes may become either.
  *
  * S may be X or R itself, Y may be X where there is no R, and dX may be S, dY or
